@@ -1,4 +1,5 @@
-"""B200 (sm_100a) gated delta rule forward pass: Python binding of libgdr.so.
+"""B200 (sm_100a) gated delta rule forward pass, the gated linear recurrence with its
+gradient, and the trainable steps around them: Python binding of libgdr.so.
 
 The binding only marshals arguments: every step of the computation runs in the CUDA
 kernels of ``libgdr.so`` (built in-tree by ``build.py``).  There is no CPU or PyTorch
@@ -6,8 +7,9 @@ fallback: importing works without a GPU, but every call needs the library and CU
 tensors, and fails loudly otherwise.
 
 The functions named ``gdr_*`` mirror the C ABI in ``include/gdr.h`` one to one
-(pointer arguments take torch tensors, None or raw integer addresses).  ``prefill``
-and ``decode_step`` are conveniences that check tensors and allocate the outputs.
+(pointer arguments take torch tensors, None or raw integer addresses).  ``prefill``,
+``decode_step``, ``linear_recurrence``, ``layer_norm`` and the ``*_backward`` functions are
+conveniences that check tensors and allocate the outputs.
 """
 
 from __future__ import annotations
@@ -19,6 +21,12 @@ __all__ = [
     "GdrError", "library", "gdr_prefill_chunked", "gdr_prefill_chunked_f32",
     "gdr_prefill_recurrent", "gdr_prefill_recurrent_f32", "gdr_decode_step",
     "gdr_decode_step_f32", "gdr_status_string", "gdr_device_status", "prefill", "decode_step", "LIB_PATH",
+    "gdr_linear_recurrence", "gdr_linear_recurrence_f32", "gdr_linear_recurrence_backward",
+    "gdr_linear_recurrence_backward_f32", "gdr_layer_norm", "gdr_layer_norm_f32",
+    "gdr_layer_norm_backward", "gdr_layer_norm_backward_f32", "gdr_short_conv_silu_backward",
+    "gdr_gated_rmsnorm_backward", "gdr_gated_rmsnorm_backward_f32", "linear_recurrence",
+    "linear_recurrence_backward", "layer_norm", "layer_norm_backward",
+    "short_conv_silu_backward", "gated_rmsnorm_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdr.so")
@@ -43,6 +51,8 @@ class GdrError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 
 _SIGS = {
     "gdr_prefill_chunked": [_P] * 11 + [_I] * 7 + [_P],
@@ -61,6 +71,17 @@ _SIGS = {
     "gdr_short_conv_silu": [_P] * 6 + [_I] * 4 + [_P],
     "gdr_gated_rmsnorm": [_P] * 4 + [ctypes.c_longlong, _I, ctypes.c_float, _P],
     "gdr_gated_rmsnorm_f32": [_P] * 4 + [ctypes.c_longlong, _I, ctypes.c_float, _P],
+    "gdr_short_conv_silu_backward": [_P] * 10 + [_I] * 4 + [_P],
+    "gdr_gated_rmsnorm_backward": [_P] * 7 + [_L, _I, _F, _P],
+    "gdr_gated_rmsnorm_backward_f32": [_P] * 7 + [_L, _I, _F, _P],
+    "gdr_layer_norm": [_P] * 6 + [_L, _I, _F, _P],
+    "gdr_layer_norm_f32": [_P] * 6 + [_L, _I, _F, _P],
+    "gdr_layer_norm_backward": [_P] * 8 + [_L, _I, _P],
+    "gdr_layer_norm_backward_f32": [_P] * 8 + [_L, _I, _P],
+    "gdr_linear_recurrence": [_P] * 9 + [_I] * 3 + [_L, _P],
+    "gdr_linear_recurrence_f32": [_P] * 9 + [_I] * 3 + [_L, _P],
+    "gdr_linear_recurrence_backward": [_P] * 16 + [_I] * 3 + [_L] * 2 + [_P],
+    "gdr_linear_recurrence_backward_f32": [_P] * 16 + [_I] * 3 + [_L] * 2 + [_P],
     "gdr_prefill_segment_maps": [_P] * 10 + [_I] * 7 + [_P],
     "gdr_segment_combine": [_P] * 5 + [_I] * 4 + [_P],
     "gdr_prefill_chunked_cp": [_P] * 10 + [_I] * 7 + [_P],
@@ -263,13 +284,17 @@ def gdr_short_conv_silu(x, weight, bias, conv_state_in, conv_state_out, y, B, T,
                  (B, T, C, width), stream, check)
 
 
-def _norm_call(name, o, z, weight, y, rows, d, eps, stream, check):
-    fn = getattr(library(), name)
-    status = fn(_ptr(o), _ptr(z), _ptr(weight), _ptr(y), ctypes.c_longlong(int(rows)), int(d),
-                ctypes.c_float(eps), _stream(stream))
+def _rows_call(name, ptrs, rows, d, rest, stream, check):
+    """A row-wise call: pointers, then rows, d and what follows them (eps)."""
+    status = getattr(library(), name)(*[_ptr(p) for p in ptrs], int(rows), int(d), *rest,
+                                      _stream(stream))
     if check and status != GDR_OK:
         raise GdrError(name, status)
     return status
+
+
+def _norm_call(name, o, z, weight, y, rows, d, eps, stream, check):
+    return _rows_call(name, (o, z, weight, y), rows, d, (float(eps),), stream, check)
 
 
 def gdr_gated_rmsnorm(o, z, weight, y, rows, d, eps=1e-6, stream=None, check=True):
@@ -280,6 +305,98 @@ def gdr_gated_rmsnorm(o, z, weight, y, rows, d, eps=1e-6, stream=None, check=Tru
 def gdr_gated_rmsnorm_f32(o, z, weight, y, rows, d, eps=1e-6, stream=None, check=True):
     """The gated RMS normalisation after the rule, fp32 gate (see include/gdr.h)."""
     return _norm_call("gdr_gated_rmsnorm_f32", o, z, weight, y, rows, d, eps, stream, check)
+
+
+def gdr_short_conv_silu_backward(x, weight, bias, conv_state_in, grad_y, grad_conv_state_out,
+                                 grad_x, grad_weight, grad_bias, grad_conv_state_in, B, T, C,
+                                 width=4, stream=None, check=True):
+    """The gradient of gdr_short_conv_silu (see include/gdr.h)."""
+    return _call("gdr_short_conv_silu_backward",
+                 (x, weight, bias, conv_state_in, grad_y, grad_conv_state_out, grad_x,
+                  grad_weight, grad_bias, grad_conv_state_in), (B, T, C, width), stream, check)
+
+
+def gdr_gated_rmsnorm_backward(o, z, weight, grad_y, grad_o, grad_z, grad_weight, rows, d,
+                               eps=1e-6, stream=None, check=True):
+    """The gradient of gdr_gated_rmsnorm, bf16 gate (see include/gdr.h)."""
+    return _rows_call("gdr_gated_rmsnorm_backward",
+                      (o, z, weight, grad_y, grad_o, grad_z, grad_weight), rows, d,
+                      (float(eps),), stream, check)
+
+
+def gdr_gated_rmsnorm_backward_f32(o, z, weight, grad_y, grad_o, grad_z, grad_weight, rows, d,
+                                   eps=1e-6, stream=None, check=True):
+    """The gradient of gdr_gated_rmsnorm_f32, fp32 gate (see include/gdr.h)."""
+    return _rows_call("gdr_gated_rmsnorm_backward_f32",
+                      (o, z, weight, grad_y, grad_o, grad_z, grad_weight), rows, d,
+                      (float(eps),), stream, check)
+
+
+def gdr_layer_norm(x, weight, bias, y, mean, rstd, rows, d, eps=1e-5, stream=None, check=True):
+    """Layer normalisation of bf16 rows (see include/gdr.h)."""
+    return _rows_call("gdr_layer_norm", (x, weight, bias, y, mean, rstd), rows, d,
+                      (float(eps),), stream, check)
+
+
+def gdr_layer_norm_f32(x, weight, bias, y, mean, rstd, rows, d, eps=1e-5, stream=None,
+                       check=True):
+    """Layer normalisation of fp32 rows (see include/gdr.h)."""
+    return _rows_call("gdr_layer_norm_f32", (x, weight, bias, y, mean, rstd), rows, d,
+                      (float(eps),), stream, check)
+
+
+def gdr_layer_norm_backward(x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias, rows,
+                            d, stream=None, check=True):
+    """The gradient of gdr_layer_norm (see include/gdr.h)."""
+    return _rows_call("gdr_layer_norm_backward",
+                      (x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias), rows, d,
+                      (), stream, check)
+
+
+def gdr_layer_norm_backward_f32(x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias,
+                                rows, d, stream=None, check=True):
+    """The gradient of gdr_layer_norm_f32 (see include/gdr.h)."""
+    return _rows_call("gdr_layer_norm_backward_f32",
+                      (x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias), rows, d,
+                      (), stream, check)
+
+
+def gdr_linear_recurrence(x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens, B, T,
+                          C, ld, stream=None, check=True):
+    """The gated linear recurrence (vector state), bf16 x, a, b (see include/gdr.h)."""
+    return _call("gdr_linear_recurrence",
+                 (x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens),
+                 (B, T, C, ld), stream, check)
+
+
+def gdr_linear_recurrence_f32(x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens,
+                              B, T, C, ld, stream=None, check=True):
+    """The gated linear recurrence (vector state), fp32 x, a, b (see include/gdr.h)."""
+    return _call("gdr_linear_recurrence_f32",
+                 (x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens),
+                 (B, T, C, ld), stream, check)
+
+
+def gdr_linear_recurrence_backward(x, a, b, A_log, dt_bias, init_state, out, grad_out,
+                                   grad_final_state, grad_x, grad_a, grad_b, grad_A_log,
+                                   grad_dt_bias, grad_init_state, cu_seqlens, B, T, C, ld,
+                                   ld_grad, stream=None, check=True):
+    """The gradient of gdr_linear_recurrence (see include/gdr.h)."""
+    return _call("gdr_linear_recurrence_backward",
+                 (x, a, b, A_log, dt_bias, init_state, out, grad_out, grad_final_state, grad_x,
+                  grad_a, grad_b, grad_A_log, grad_dt_bias, grad_init_state, cu_seqlens),
+                 (B, T, C, ld, ld_grad), stream, check)
+
+
+def gdr_linear_recurrence_backward_f32(x, a, b, A_log, dt_bias, init_state, out, grad_out,
+                                       grad_final_state, grad_x, grad_a, grad_b, grad_A_log,
+                                       grad_dt_bias, grad_init_state, cu_seqlens, B, T, C, ld,
+                                       ld_grad, stream=None, check=True):
+    """The gradient of gdr_linear_recurrence_f32 (see include/gdr.h)."""
+    return _call("gdr_linear_recurrence_backward_f32",
+                 (x, a, b, A_log, dt_bias, init_state, out, grad_out, grad_final_state, grad_x,
+                  grad_a, grad_b, grad_A_log, grad_dt_bias, grad_init_state, cu_seqlens),
+                 (B, T, C, ld, ld_grad), stream, check)
 
 
 def prefill(q, k, v, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None, chunk=32,
@@ -341,3 +458,233 @@ def decode_step(q, k, v, a, b, A_log, dt_bias, state, out=None, stream=None, era
           (gdr_gla_decode_step_f32 if f32 else gdr_gla_decode_step))
     fn(q, k, v, a, b, A_log, dt_bias, state, out, B, Hk, Hv, dk, dv, stream=stream)
     return out
+
+
+def _check_arg(name, t, dtype, shape, like=None, rows=False):
+    """`t` is a CUDA tensor of this type and shape (None passes), on `like`'s device and
+    contiguous; ``rows``: only its last dimension has to be."""
+    if t is None:
+        return
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if not rows and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_stride(tensors, B, T, C):
+    """Elements between consecutive tokens of [B, T, C] tensors that share one layout: dense,
+    or slices of the last dimension of a wider dense tensor."""
+    if B * T * C == 0:
+        return max(C, 1)
+    first = next(iter(tensors.values()))
+    ld = first.stride(1) if T > 1 else first.stride(0) if B > 1 else C
+    for name, t in tensors.items():
+        if ((C > 1 and t.stride(2) != 1) or (T > 1 and t.stride(1) != ld) or
+                (B > 1 and t.stride(0) != T * ld)):
+            raise ValueError(f"{name}: x, a, b need one layout, dense or slices of the last "
+                             f"dimension of a dense tensor; got strides {t.stride()}")
+    return ld
+
+
+def _input_type(x, name):
+    import torch
+
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bf16 or fp32, got {x.dtype}")
+    return x.dtype
+
+
+def _on_device(t, stream):
+    """Context that makes t's device current, and the stream to use on it."""
+    import torch
+
+    ctx = torch.cuda.device(t.device)
+    return ctx, (torch.cuda.current_stream(t.device) if stream is None else stream)
+
+
+def _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens):
+    import torch
+
+    dtype = _input_type(x, "x")
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B, T, C], got shape {tuple(x.shape)}")
+    B, T, C = x.shape
+    f32 = torch.float32
+    for name, t in dict(x=x, a=a, b=b).items():
+        _check_arg(name, t, dtype, (B, T, C), x, rows=True)
+    nseq = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("packed sequences need B == 1")
+        nseq = cu_seqlens.numel() - 1
+        _check_arg("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), x)
+    _check_arg("A_log", A_log, f32, (C,), x)
+    _check_arg("dt_bias", dt_bias, f32, (C,), x)
+    _check_arg("init_state", init_state, f32, (nseq, C), x)
+    return dtype, nseq, T, C, _token_stride(dict(x=x, a=a, b=b), B, T, C)
+
+
+def linear_recurrence(x, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None, out=None,
+                      final_state=None, stream=None):
+    """The gated linear recurrence h <- h exp(g) + sigmoid(b) x per channel, with the rule's
+    decay g = -exp(A_log) softplus(a + dt_bias): x, a, b [B, T, C] bf16 or fp32, dense or all
+    three slices of the last dimension of a dense tensor; A_log, dt_bias [C]; ``init_state``
+    [Nseq, C] (zeros if None).  With ``cu_seqlens`` (int32, device, [Nseq + 1]) the tokens are
+    packed along T (B must be 1).  T = 1 is a decode step; ``final_state`` may be
+    ``init_state``.  Returns (out [B, T, C] fp32, final_state [Nseq, C] fp32)."""
+    import torch
+
+    dtype, nseq, T, C, ld = _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens)
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty(x.shape, device=x.device, dtype=f32)
+    if final_state is None:
+        final_state = torch.empty((nseq, C), device=x.device, dtype=f32)
+    _check_arg("out", out, f32, x.shape, x)
+    _check_arg("final_state", final_state, f32, (nseq, C), x)
+    ctx, stream = _on_device(x, stream)
+    with ctx:
+        fn = gdr_linear_recurrence_f32 if dtype == f32 else gdr_linear_recurrence
+        fn(x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens, nseq, T, C, ld,
+           stream=stream)
+    return out, final_state
+
+
+def linear_recurrence_backward(x, a, b, A_log, dt_bias, out, grad_out, grad_final_state=None,
+                               init_state=None, cu_seqlens=None, grad_x=None, grad_a=None,
+                               grad_b=None, stream=None):
+    """The gradient of ``linear_recurrence``: its arguments and its ``out``, with grad_out
+    [B, T, C] fp32 and ``grad_final_state`` [Nseq, C] fp32 (zeros if None).  ``grad_x``,
+    ``grad_a``, ``grad_b`` may be given, all three, in one layout as x, a, b may have (for
+    example slices of one projection's gradient).  Returns (grad_x, grad_a, grad_b,
+    grad_A_log [C], grad_dt_bias [C], grad_init_state [Nseq, C])."""
+    import torch
+
+    dtype, nseq, T, C, ld = _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens)
+    f32 = torch.float32
+    _check_arg("out", out, f32, x.shape, x)
+    _check_arg("grad_out", grad_out, f32, x.shape, x)
+    _check_arg("grad_final_state", grad_final_state, f32, (nseq, C), x)
+    grads = dict(grad_x=grad_x, grad_a=grad_a, grad_b=grad_b)
+    if any(g is None for g in grads.values()):
+        if any(g is not None for g in grads.values()):
+            raise ValueError("give grad_x, grad_a and grad_b together, or none of them")
+        grads = {k: torch.empty(x.shape, device=x.device, dtype=dtype) for k in grads}
+    for name, t in grads.items():
+        _check_arg(name, t, dtype, x.shape, x, rows=True)
+    ld_grad = _token_stride(grads, x.shape[0], T, C)
+    grad_A_log, grad_dt_bias = torch.empty((2, C), device=x.device, dtype=f32)
+    grad_init = torch.empty((nseq, C), device=x.device, dtype=f32)
+    ctx, stream = _on_device(x, stream)
+    with ctx:
+        fn = (gdr_linear_recurrence_backward_f32 if dtype == f32 else
+              gdr_linear_recurrence_backward)
+        fn(x, a, b, A_log, dt_bias, init_state, out, grad_out, grad_final_state,
+           grads["grad_x"], grads["grad_a"], grads["grad_b"], grad_A_log, grad_dt_bias, grad_init,
+           cu_seqlens, nseq, T, C, ld, ld_grad, stream=stream)
+    return (grads["grad_x"], grads["grad_a"], grads["grad_b"], grad_A_log, grad_dt_bias,
+            grad_init)
+
+
+def _row_args(x):
+    """(rows, d) of x [..., d]."""
+    d = x.shape[-1] if x.dim() else 0
+    return (x.numel() // d if d else 0), d
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, y=None, stream=None):
+    """Layer normalisation of x [..., d] (bf16 or fp32) over its last dimension: weight and
+    ``bias`` [d] fp32.  ``y`` may be x.  Returns (y, mean [...], rstd [...]); the statistics
+    (fp32) are what ``layer_norm_backward`` takes."""
+    import torch
+
+    dtype, f32 = _input_type(x, "x"), torch.float32
+    rows, d = _row_args(x)
+    _check_arg("x", x, dtype, x.shape)
+    _check_arg("weight", weight, f32, (d,), x)
+    _check_arg("bias", bias, f32, (d,), x)
+    y = torch.empty_like(x) if y is None else y
+    _check_arg("y", y, dtype, x.shape, x)
+    mean, rstd = torch.empty((2,) + tuple(x.shape[:-1]), device=x.device, dtype=f32)
+    ctx, stream = _on_device(x, stream)
+    with ctx:
+        fn = gdr_layer_norm_f32 if dtype == f32 else gdr_layer_norm
+        fn(x, weight, bias, y, mean, rstd, rows, d, eps, stream=stream)
+    return y, mean, rstd
+
+
+def layer_norm_backward(x, weight, mean, rstd, grad_y, grad_x=None, stream=None):
+    """The gradient of ``layer_norm`` from its x, weight and statistics and grad_y (x's type).
+    ``grad_x`` may be grad_y.  Returns (grad_x, grad_weight [d], grad_bias [d])."""
+    import torch
+
+    dtype, f32 = _input_type(x, "x"), torch.float32
+    rows, d = _row_args(x)
+    _check_arg("x", x, dtype, x.shape)
+    _check_arg("weight", weight, f32, (d,), x)
+    for name, t in dict(mean=mean, rstd=rstd).items():
+        _check_arg(name, t, f32, x.shape[:-1], x)
+    _check_arg("grad_y", grad_y, dtype, x.shape, x)
+    grad_x = torch.empty_like(x) if grad_x is None else grad_x
+    _check_arg("grad_x", grad_x, dtype, x.shape, x)
+    grad_weight, grad_bias = torch.empty((2, d), device=x.device, dtype=f32)
+    ctx, stream = _on_device(x, stream)
+    with ctx:
+        fn = gdr_layer_norm_backward_f32 if dtype == f32 else gdr_layer_norm_backward
+        fn(x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias, rows, d, stream=stream)
+    return grad_x, grad_weight, grad_bias
+
+
+def short_conv_silu_backward(x, weight, grad_y, bias=None, conv_state_in=None,
+                             grad_conv_state_out=None, stream=None):
+    """The gradient of gdr_short_conv_silu: x, grad_y [B, T, C] bf16, weight [C, 4], ``bias``
+    [C], ``conv_state_in`` and ``grad_conv_state_out`` [B, C, 3] (zeros if None).  Returns
+    (grad_x, grad_weight, grad_bias, grad_conv_state_in)."""
+    import torch
+
+    f32, bf16 = torch.float32, torch.bfloat16
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B, T, C], got shape {tuple(x.shape)}")
+    B, T, C = x.shape
+    _check_arg("x", x, bf16, x.shape)
+    _check_arg("weight", weight, f32, (C, 4), x)
+    _check_arg("grad_y", grad_y, bf16, x.shape, x)
+    _check_arg("bias", bias, f32, (C,), x)
+    _check_arg("conv_state_in", conv_state_in, f32, (B, C, 3), x)
+    _check_arg("grad_conv_state_out", grad_conv_state_out, f32, (B, C, 3), x)
+    grad_x = torch.empty_like(x)
+    grad_weight = torch.empty_like(weight)
+    grad_bias = torch.empty((C,), device=x.device, dtype=f32)
+    grad_state = torch.empty((B, C, 3), device=x.device, dtype=f32)
+    ctx, stream = _on_device(x, stream)
+    with ctx:
+        gdr_short_conv_silu_backward(x, weight, bias, conv_state_in, grad_y, grad_conv_state_out,
+                                     grad_x, grad_weight, grad_bias, grad_state, B, T, C,
+                                     stream=stream)
+    return grad_x, grad_weight, grad_bias, grad_state
+
+
+def gated_rmsnorm_backward(o, z, weight, grad_y, eps=1e-6, stream=None):
+    """The gradient of gdr_gated_rmsnorm[_f32] over the last dimension d of o [..., d] fp32, z
+    bf16 or fp32, weight [d], grad_y fp32.  Returns (grad_o, grad_z, grad_weight [d])."""
+    import torch
+
+    f32 = torch.float32
+    dtype = _input_type(z, "z")
+    rows, d = _row_args(o)
+    _check_arg("o", o, f32, o.shape)
+    _check_arg("z", z, dtype, o.shape, o)
+    _check_arg("weight", weight, f32, (d,), o)
+    _check_arg("grad_y", grad_y, f32, o.shape, o)
+    grad_o, grad_z, grad_weight = torch.empty_like(o), torch.empty_like(z), torch.empty_like(weight)
+    ctx, stream = _on_device(o, stream)
+    with ctx:
+        fn = gdr_gated_rmsnorm_backward_f32 if dtype == f32 else gdr_gated_rmsnorm_backward
+        fn(o, z, weight, grad_y, grad_o, grad_z, grad_weight, rows, d, eps, stream=stream)
+    return grad_o, grad_z, grad_weight

@@ -395,6 +395,236 @@ int gdr_gated_rmsnorm_f32(const float* o, const float* z, const float* weight, f
     return gated_rmsnorm(o, z, true, weight, y, rows, d, eps, (cudaStream_t)stream);
 }
 
+// ---- gradients of the steps around the rule
+
+int gdr_short_conv_silu_backward(const void* x, const float* weight, const float* bias,
+                                 const float* conv_state_in, const void* grad_y,
+                                 const float* grad_conv_state_out, void* grad_x,
+                                 float* grad_weight, float* grad_bias,
+                                 float* grad_conv_state_in, int B, int T, int C, int width,
+                                 gdr_stream_t stream) {
+    if (!weight || (T > 0 && (!x || !grad_y || !grad_x))) return GDR_ERR_NULL;
+    if (B < 1 || T < 0 || C < 8 || C % 8 != 0) return GDR_ERR_SHAPE;
+    if (width != 4) return GDR_ERR_UNSUPPORTED;
+    if ((long long)B * C * ((long long)T + 64) > 0x3fffffffffffLL || 5LL * C > 0x7fffffffLL ||
+        (long long)B * (((long long)T + 63) / 64) > 0x7fffffLL)
+        return GDR_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(grad_y, 16) || !aligned(grad_x, 16) || !aligned(weight, 16) ||
+        !aligned(bias, 4) || !aligned(conv_state_in, 4) || !aligned(grad_conv_state_out, 4) ||
+        !aligned(grad_weight, 4) || !aligned(grad_bias, 4) || !aligned(grad_conv_state_in, 4))
+        return GDR_ERR_ALIGN;
+    gdr::ConvGrads p;
+    p.x = x; p.weight = weight; p.bias = bias; p.state_in = conv_state_in;
+    p.grad_y = grad_y; p.grad_state_out = grad_conv_state_out;
+    p.grad_x = grad_x; p.grad_weight = grad_weight; p.grad_bias = grad_bias;
+    p.grad_state_in = grad_conv_state_in;
+    p.B = B; p.T = T; p.C = C;
+    return to_status(gdr::launch_short_conv_silu_backward(p, (cudaStream_t)stream));
+}
+
+static int gated_rmsnorm_backward(const float* o, const void* z, bool z_f32, const float* weight,
+                                  const float* grad_y, float* grad_o, void* grad_z,
+                                  float* grad_weight, long long rows, int d, float eps,
+                                  cudaStream_t stream) {
+    if (!weight || !grad_weight || (rows > 0 && (!o || !z || !grad_y || !grad_o || !grad_z)))
+        return GDR_ERR_NULL;
+    if (rows < 0 || !(eps >= 0.f)) return GDR_ERR_SHAPE;
+    if (d != 32 && d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
+    const uintptr_t za = z_f32 ? 16 : 8;
+    if (!aligned(o, 16) || !aligned(grad_y, 16) || !aligned(grad_o, 16) || !aligned(z, za) ||
+        !aligned(grad_z, za) || !aligned(weight, 16) || !aligned(grad_weight, 4))
+        return GDR_ERR_ALIGN;
+    gdr::NormGrads p;
+    p.o = o; p.z = z; p.weight = weight; p.grad_y = grad_y;
+    p.grad_o = grad_o; p.grad_z = grad_z; p.grad_weight = grad_weight;
+    p.rows = rows; p.d = d; p.eps = eps; p.z_f32 = z_f32;
+    return to_status(gdr::launch_gated_rmsnorm_backward(p, stream));
+}
+
+int gdr_gated_rmsnorm_backward(const float* o, const void* z, const float* weight,
+                               const float* grad_y, float* grad_o, void* grad_z,
+                               float* grad_weight, long long rows, int d, float eps,
+                               gdr_stream_t stream) {
+    return gated_rmsnorm_backward(o, z, false, weight, grad_y, grad_o, grad_z, grad_weight, rows,
+                                  d, eps, (cudaStream_t)stream);
+}
+
+int gdr_gated_rmsnorm_backward_f32(const float* o, const float* z, const float* weight,
+                                   const float* grad_y, float* grad_o, float* grad_z,
+                                   float* grad_weight, long long rows, int d, float eps,
+                                   gdr_stream_t stream) {
+    return gated_rmsnorm_backward(o, z, true, weight, grad_y, grad_o, grad_z, grad_weight, rows,
+                                  d, eps, (cudaStream_t)stream);
+}
+
+// ---- layer normalisation
+
+static int layer_norm(const void* x, const float* weight, const float* bias, void* y, float* mean,
+                      float* rstd, long long rows, int d, float eps, InType in,
+                      cudaStream_t stream) {
+    if (!weight || (rows > 0 && (!x || !y))) return GDR_ERR_NULL;
+    if (rows < 0 || d < 8 || d % 8 != 0 || !(eps >= 0.f)) return GDR_ERR_SHAPE;
+    if (d > 32768) return GDR_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(weight, 16) || !aligned(bias, 16) ||
+        !aligned(mean, 4) || !aligned(rstd, 4))
+        return GDR_ERR_ALIGN;
+    gdr::LayerNormParams p;
+    p.x = x; p.weight = weight; p.bias = bias; p.y = y; p.mean = mean; p.rstd = rstd;
+    p.rows = rows; p.d = d; p.eps = eps; p.in = in;
+    return to_status(gdr::launch_layer_norm(p, stream));
+}
+
+int gdr_layer_norm(const void* x, const float* weight, const float* bias, void* y, float* mean,
+                   float* rstd, long long rows, int d, float eps, gdr_stream_t stream) {
+    return layer_norm(x, weight, bias, y, mean, rstd, rows, d, eps, InType::BF16,
+                      (cudaStream_t)stream);
+}
+
+int gdr_layer_norm_f32(const float* x, const float* weight, const float* bias, float* y,
+                       float* mean, float* rstd, long long rows, int d, float eps,
+                       gdr_stream_t stream) {
+    return layer_norm(x, weight, bias, y, mean, rstd, rows, d, eps, InType::F32,
+                      (cudaStream_t)stream);
+}
+
+static int layer_norm_backward(const void* x, const float* weight, const float* mean,
+                               const float* rstd, const void* grad_y, void* grad_x,
+                               float* grad_weight, float* grad_bias, long long rows, int d,
+                               InType in, cudaStream_t stream) {
+    if (!weight || (rows > 0 && (!x || !mean || !rstd || !grad_y || !grad_x))) return GDR_ERR_NULL;
+    if (rows < 0 || d < 8 || d % 8 != 0) return GDR_ERR_SHAPE;
+    if (d > 32768) return GDR_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(grad_y, 16) || !aligned(grad_x, 16) || !aligned(weight, 16) ||
+        !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(grad_weight, 4) ||
+        !aligned(grad_bias, 4))
+        return GDR_ERR_ALIGN;
+    gdr::LayerNormGrads p;
+    p.x = x; p.weight = weight; p.mean = mean; p.rstd = rstd; p.grad_y = grad_y;
+    p.grad_x = grad_x; p.grad_weight = grad_weight; p.grad_bias = grad_bias;
+    p.rows = rows; p.d = d; p.in = in;
+    return to_status(gdr::launch_layer_norm_backward(p, stream));
+}
+
+int gdr_layer_norm_backward(const void* x, const float* weight, const float* mean,
+                            const float* rstd, const void* grad_y, void* grad_x,
+                            float* grad_weight, float* grad_bias, long long rows, int d,
+                            gdr_stream_t stream) {
+    return layer_norm_backward(x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias,
+                               rows, d, InType::BF16, (cudaStream_t)stream);
+}
+
+int gdr_layer_norm_backward_f32(const float* x, const float* weight, const float* mean,
+                                const float* rstd, const float* grad_y, float* grad_x,
+                                float* grad_weight, float* grad_bias, long long rows, int d,
+                                gdr_stream_t stream) {
+    return layer_norm_backward(x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias,
+                               rows, d, InType::F32, (cudaStream_t)stream);
+}
+
+// ---- the gated linear recurrence (vector state)
+
+static int check_recurrence(const gdr::RecurrenceParams& p) {
+    if (!p.A_log || !p.dt_bias) return GDR_ERR_NULL;
+    if (p.T > 0 && (!p.x || !p.a || !p.b || !p.out)) return GDR_ERR_NULL;
+    if (p.nseq < 1 || p.T < 0 || p.C < 8 || p.C % 8 != 0 || p.ld < p.C || p.ld % 8 != 0 ||
+        p.ld > 0x7fffffffLL)
+        return GDR_ERR_SHAPE;
+    // token rows and parameter columns are indexed in 32 bits, their offsets in 64
+    const long long tokens = p.cu_seqlens ? p.T : (long long)p.nseq * p.T;
+    if (tokens > 0x7fffff00LL || p.C > 0x3fffff00) return GDR_ERR_SHAPE;
+    if (!aligned(p.x, 16) || !aligned(p.a, 16) || !aligned(p.b, 16) || !aligned(p.out, 16) ||
+        !aligned(p.A_log, 4) || !aligned(p.dt_bias, 4) || !aligned(p.init_state, 16) ||
+        !aligned(p.final_state, 16) || !aligned(p.cu_seqlens, 4))
+        return GDR_ERR_ALIGN;
+    return GDR_OK;
+}
+
+static int recurrence(const void* x, const void* a, const void* b, const float* A_log,
+                      const float* dt_bias, const float* init_state, float* out,
+                      float* final_state, const int32_t* cu_seqlens, int B, int T, int C,
+                      long long ld, InType in, cudaStream_t stream) {
+    gdr::RecurrenceParams p;
+    p.x = x; p.a = a; p.b = b; p.A_log = A_log; p.dt_bias = dt_bias; p.init_state = init_state;
+    p.out = out; p.final_state = final_state; p.cu_seqlens = cu_seqlens;
+    p.nseq = B; p.T = T; p.C = C; p.ld = ld; p.in = in;
+    const int rc = check_recurrence(p);
+    if (rc != GDR_OK) return rc;
+    return to_status(gdr::launch_recurrence(p, stream));
+}
+
+int gdr_linear_recurrence(const void* x, const void* a, const void* b, const float* A_log,
+                          const float* dt_bias, const float* init_state, float* out,
+                          float* final_state, const int32_t* cu_seqlens, int B, int T, int C,
+                          long long ld, gdr_stream_t stream) {
+    return recurrence(x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens, B, T, C,
+                      ld, InType::BF16, (cudaStream_t)stream);
+}
+
+int gdr_linear_recurrence_f32(const float* x, const float* a, const float* b, const float* A_log,
+                              const float* dt_bias, const float* init_state, float* out,
+                              float* final_state, const int32_t* cu_seqlens, int B, int T, int C,
+                              long long ld, gdr_stream_t stream) {
+    return recurrence(x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens, B, T, C,
+                      ld, InType::F32, (cudaStream_t)stream);
+}
+
+static int recurrence_backward(const void* x, const void* a, const void* b, const float* A_log,
+                               const float* dt_bias, const float* init_state, const float* out,
+                               const float* grad_out, const float* grad_final_state, void* grad_x,
+                               void* grad_a, void* grad_b, float* grad_A_log,
+                               float* grad_dt_bias, float* grad_init_state,
+                               const int32_t* cu_seqlens, int B, int T, int C, long long ld,
+                               long long ld_grad, InType in, cudaStream_t stream) {
+    gdr::RecurrenceParams p;
+    p.x = x; p.a = a; p.b = b; p.A_log = A_log; p.dt_bias = dt_bias; p.init_state = init_state;
+    p.out = const_cast<float*>(out); p.final_state = nullptr; p.cu_seqlens = cu_seqlens;
+    p.nseq = B; p.T = T; p.C = C; p.ld = ld; p.in = in;
+    gdr::RecurrenceGrads r;
+    r.grad_out = grad_out; r.grad_final = grad_final_state;
+    r.grad_x = grad_x; r.grad_a = grad_a; r.grad_b = grad_b;
+    r.grad_A_log = grad_A_log; r.grad_dt_bias = grad_dt_bias; r.grad_init = grad_init_state;
+    r.ld_grad = ld_grad;
+    if (!grad_A_log || !grad_dt_bias) return GDR_ERR_NULL;
+    if (T > 0 && (!grad_out || !grad_x || !grad_a || !grad_b)) return GDR_ERR_NULL;
+    const int rc = check_recurrence(p);
+    if (rc != GDR_OK) return rc;
+    if (ld_grad < C || ld_grad % 8 != 0 || ld_grad > 0x7fffffffLL) return GDR_ERR_SHAPE;
+    if (!aligned(grad_out, 16) || !aligned(grad_final_state, 16) || !aligned(grad_x, 16) ||
+        !aligned(grad_a, 16) || !aligned(grad_b, 16) || !aligned(grad_A_log, 4) ||
+        !aligned(grad_dt_bias, 4) || !aligned(grad_init_state, 16))
+        return GDR_ERR_ALIGN;
+    return to_status(gdr::launch_recurrence_backward(p, r, stream));
+}
+
+int gdr_linear_recurrence_backward(const void* x, const void* a, const void* b,
+                                   const float* A_log, const float* dt_bias,
+                                   const float* init_state, const float* out,
+                                   const float* grad_out, const float* grad_final_state,
+                                   void* grad_x, void* grad_a, void* grad_b, float* grad_A_log,
+                                   float* grad_dt_bias, float* grad_init_state,
+                                   const int32_t* cu_seqlens, int B, int T, int C, long long ld,
+                                   long long ld_grad, gdr_stream_t stream) {
+    return recurrence_backward(x, a, b, A_log, dt_bias, init_state, out, grad_out,
+                               grad_final_state, grad_x, grad_a, grad_b, grad_A_log, grad_dt_bias,
+                               grad_init_state, cu_seqlens, B, T, C, ld, ld_grad, InType::BF16,
+                               (cudaStream_t)stream);
+}
+
+int gdr_linear_recurrence_backward_f32(const float* x, const float* a, const float* b,
+                                       const float* A_log, const float* dt_bias,
+                                       const float* init_state, const float* out,
+                                       const float* grad_out, const float* grad_final_state,
+                                       float* grad_x, float* grad_a, float* grad_b,
+                                       float* grad_A_log, float* grad_dt_bias,
+                                       float* grad_init_state, const int32_t* cu_seqlens, int B,
+                                       int T, int C, long long ld, long long ld_grad,
+                                       gdr_stream_t stream) {
+    return recurrence_backward(x, a, b, A_log, dt_bias, init_state, out, grad_out,
+                               grad_final_state, grad_x, grad_a, grad_b, grad_A_log, grad_dt_bias,
+                               grad_init_state, cu_seqlens, B, T, C, ld, ld_grad, InType::F32,
+                               (cudaStream_t)stream);
+}
+
 int gdr_device_status(gdr_stream_t stream) {
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return GDR_ERR_CUDA;
     const int v = gdr::read_and_clear_tc_status();

@@ -74,6 +74,85 @@ cudaError_t launch_gated_rmsnorm(const float* o, const void* z, bool z_f32, cons
 // Reads and clears the tiled convolution's timeout record (nonzero if set, -1 on error).
 int read_and_clear_conv_status();
 
+// The gated linear recurrence (vector state), forward and backward; linear_recurrence.cu.
+struct RecurrenceParams {
+    const void *x, *a, *b;          // [tokens, C], rows ld elements apart (bf16 or fp32)
+    const float *A_log, *dt_bias;   // [C]
+    const float* init_state;        // [nseq, C] or nullptr (zeros)
+    float* out;                     // [tokens, C]: written by forward, read by backward
+    float* final_state;             // [nseq, C] or nullptr
+    const int32_t* cu_seqlens;      // [nseq + 1] or nullptr (dense: nseq sequences of T)
+    int nseq, T, C;
+    long long ld;
+    InType in;
+};
+struct RecurrenceGrads {
+    const float *grad_out, *grad_final;  // [tokens, C]; [nseq, C] or nullptr (zeros)
+    void *grad_x, *grad_a, *grad_b;      // as x, a, b, rows ld_grad elements apart
+    float *grad_A_log, *grad_dt_bias;    // [C]
+    float* grad_init;                    // [nseq, C] or nullptr
+    long long ld_grad;
+};
+cudaError_t launch_recurrence(const RecurrenceParams& p, cudaStream_t stream);
+cudaError_t launch_recurrence_backward(const RecurrenceParams& p, const RecurrenceGrads& r,
+                                       cudaStream_t stream);
+
+// Layer normalisation of rows of d values (d a multiple of 8, at most 32768); layer_norm.cu.
+struct LayerNormParams {
+    const void* x;
+    const float *weight, *bias;  // [d]; bias or nullptr
+    void* y;
+    float *mean, *rstd;  // [rows], either may be nullptr
+    long long rows;
+    int d;
+    float eps;
+    InType in;
+};
+struct LayerNormGrads {
+    const void* x;
+    const float *weight, *mean, *rstd;
+    const void* grad_y;
+    void* grad_x;
+    float *grad_weight, *grad_bias;  // [d], either may be nullptr
+    long long rows;
+    int d;
+    InType in;
+};
+cudaError_t launch_layer_norm(const LayerNormParams& p, cudaStream_t stream);
+cudaError_t launch_layer_norm_backward(const LayerNormGrads& p, cudaStream_t stream);
+
+// Backward passes of the steps around the rule; mixer_grad.cu.
+struct ConvGrads {
+    const void* x;                   // [B, T, C] bf16
+    const float *weight, *bias;      // [C, 4]; [C] or nullptr
+    const float* state_in;           // [B, C, 3] or nullptr (zeros)
+    const void* grad_y;              // [B, T, C] bf16
+    const float* grad_state_out;     // [B, C, 3] or nullptr (zeros)
+    void* grad_x;                    // [B, T, C] bf16
+    float *grad_weight, *grad_bias;  // [C, 4], [C]; either may be nullptr
+    float* grad_state_in;            // [B, C, 3] or nullptr
+    int B, T, C;
+};
+struct NormGrads {
+    const float* o;
+    const void* z;
+    const float *weight, *grad_y;
+    float* grad_o;
+    void* grad_z;
+    float* grad_weight;
+    long long rows;
+    int d;
+    float eps;
+    bool z_f32;
+};
+cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t stream);
+cudaError_t launch_gated_rmsnorm_backward(const NormGrads& p, cudaStream_t stream);
+
+// out0 [n0] and out1 [N - n0] = the column sums of part [P, N], rows added in a fixed order
+// (either output may be nullptr; P = 0 gives zeros); column_sum.cu.
+cudaError_t launch_column_sum(const float* part, long long P, int N, float* out0, int n0,
+                              float* out1, cudaStream_t stream);
+
 // Composition of per-segment state maps, and segment boundaries of one sequence cut into
 // G segments of L tokens; segments.cu.
 cudaError_t launch_segment_combine(const float* phi, const float* nmap, const float* init,

@@ -20,7 +20,8 @@
  * They agree up to floating-point reassociation, for any gate values: the chunked form
  * keeps each chunk's cumulative log-decay as a pair of floats, so its decay factors stay
  * accurate where single tokens decay by hundreds of nats (gate inputs of +-40 are checked
- * against an fp64 reference).  Inference only (no backward).
+ * against an fp64 reference).  The rule's calls are forward only; the steps around it, layer
+ * normalisation and the gated linear recurrence (a vector state) also have backward calls.
  * The "_f32" suffix marks fp32 q, k, v, a, b (tessera PR #77 names its C-ABI symbols
  * the same way); the unsuffixed calls take bf16 q, k, v, a, b.
  *
@@ -339,6 +340,138 @@ GDR_API int gdr_gated_rmsnorm(const float* o, const void* z, const float* weight
                               long long rows, int d, float eps, gdr_stream_t stream);
 GDR_API int gdr_gated_rmsnorm_f32(const float* o, const float* z, const float* weight, float* y,
                                   long long rows, int d, float eps, gdr_stream_t stream);
+
+/*
+ * Gradients of the two steps around the rule.
+ *
+ * gdr_short_conv_silu_backward: from x, weight, bias and conv_state_in as given to
+ * gdr_short_conv_silu and the gradient grad_y [B, T, C] bf16 of its y, with s_t the sum
+ * before the SiLU (computed again here) and ds_t = grad_y_t sig(s_t) (1 + s_t (1 - sig(s_t))):
+ *   grad_x_t = sum_{i<4} weight[.*4+i] ds_{t+3-i}      [B, T, C] bf16
+ *   grad_weight[c*4+i] = sum_{b,t} ds_t x_{t-3+i}      [C, 4] fp32, NULL to skip
+ *   grad_bias = sum_{b,t} ds_t                         [C] fp32, NULL to skip
+ *   grad_conv_state_in: the sum of grad_x for the three inputs before the call
+ *                                                      [B, C, 3] fp32, NULL to skip
+ * grad_conv_state_out [B, C, 3] fp32 (NULL = zeros) is the gradient of the state after the
+ * call; it is added to the inputs that this state holds.  Sizes and alignment as for
+ * gdr_short_conv_silu; B * ceil(T / 64) below 2^23.  grad_x must not overlap any input, nor
+ * grad_conv_state_in grad_conv_state_out.
+ */
+GDR_API int gdr_short_conv_silu_backward(const void* x, const float* weight, const float* bias,
+                                         const float* conv_state_in, const void* grad_y,
+                                         const float* grad_conv_state_out, void* grad_x,
+                                         float* grad_weight, float* grad_bias,
+                                         float* grad_conv_state_in, int B, int T, int C,
+                                         int width, gdr_stream_t stream);
+
+/*
+ * gdr_gated_rmsnorm_backward: from o, z, weight and eps as given to gdr_gated_rmsnorm and
+ * the gradient grad_y of its y (fp32, o's layout), with r = 1 / sqrt(mean(o^2) + eps) and
+ * q = grad_y weight SiLU(z):
+ *   grad_o = r q - o r^3 mean(q o) (fp32),  grad_z = grad_y o r weight SiLU'(z) (z's type),
+ *   grad_weight [d] = sum over the rows of grad_y o r SiLU(z) (fp32; zeros for no rows).
+ * grad_y, grad_o and weight 16-byte aligned, grad_z as z.  grad_o may be grad_y or o, and
+ * grad_z may be z.
+ */
+GDR_API int gdr_gated_rmsnorm_backward(const float* o, const void* z, const float* weight,
+                                       const float* grad_y, float* grad_o, void* grad_z,
+                                       float* grad_weight, long long rows, int d, float eps,
+                                       gdr_stream_t stream);
+GDR_API int gdr_gated_rmsnorm_backward_f32(const float* o, const float* z, const float* weight,
+                                           const float* grad_y, float* grad_o, float* grad_z,
+                                           float* grad_weight, long long rows, int d, float eps,
+                                           gdr_stream_t stream);
+
+/*
+ * Layer normalisation of `rows` rows of d values in front of the mixer:
+ *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps).
+ * x, y bf16 (the _f32 variant: fp32), dense; weight and bias [d] fp32, bias NULL for none;
+ * mean and rstd [rows] fp32 receive the statistics that the backward call takes, each NULL
+ * to skip.  d a multiple of 8, at most 32768; eps >= 0; x, y, weight, bias 16-byte aligned.
+ * y may be x.
+ */
+GDR_API int gdr_layer_norm(const void* x, const float* weight, const float* bias, void* y,
+                           float* mean, float* rstd, long long rows, int d, float eps,
+                           gdr_stream_t stream);
+GDR_API int gdr_layer_norm_f32(const float* x, const float* weight, const float* bias, float* y,
+                               float* mean, float* rstd, long long rows, int d, float eps,
+                               gdr_stream_t stream);
+
+/*
+ * Its backward pass, from x, weight, the forward call's mean and rstd, and the gradient grad_y
+ * of y (x's type), with xh = (x - mean) rstd and q = grad_y weight:
+ *   grad_x = rstd (q - mean(q) - xh mean(q xh)) (x's type),
+ *   grad_weight = sum over the rows of grad_y xh, grad_bias = sum of grad_y ([d] fp32, each
+ *   NULL to skip; zeros for no rows).
+ * grad_x may be grad_y.
+ */
+GDR_API int gdr_layer_norm_backward(const void* x, const float* weight, const float* mean,
+                                    const float* rstd, const void* grad_y, void* grad_x,
+                                    float* grad_weight, float* grad_bias, long long rows, int d,
+                                    gdr_stream_t stream);
+GDR_API int gdr_layer_norm_backward_f32(const float* x, const float* weight, const float* mean,
+                                        const float* rstd, const float* grad_y, float* grad_x,
+                                        float* grad_weight, float* grad_bias, long long rows,
+                                        int d, gdr_stream_t stream);
+
+/*
+ * The gated linear recurrence: the rule's gates on a vector state.  Every channel c of
+ * every sequence keeps one fp32 value h and each token t does
+ *   h <- h exp(g_t) + sigmoid(b_t) x_t,   out_t <- h,
+ *   g_t = -exp(A_log[c]) softplus(a_t + dt_bias[c])
+ * (Mila "GatedDeltaRule.ixx File Reference", Detailed Description, for the gates; the state
+ * has one value per channel instead of a matrix per head, so there is no key and no erase).
+ *   x, a, b      [B, T, C] bf16 (the _f32 variants: fp32).  Consecutive tokens are ld
+ *                elements apart and sequences T * ld: ld = C for dense tensors, 3 C for
+ *                slices of one [B, T, 3 C] projection.
+ *   A_log, dt_bias [C] fp32
+ *   init_state   [B, C] fp32, or NULL for zeros
+ *   out          [B, T, C] fp32, dense
+ *   final_state  [B, C] fp32, or NULL to skip; may be init_state
+ * With cu_seqlens (device int32 [B + 1], non-decreasing within [0, T]) B sequences are
+ * packed along one token axis of length T, as in gdr_prefill_chunked; rows of out outside
+ * [cu_seqlens[0], cu_seqlens[B]) are left as they were.  Sequences of length 0 are allowed: their
+ * final state is their initial one.  C and ld multiples of 8, ld >= C, fewer than 2^31 - 256
+ * tokens; x, a, b, out and the states 16-byte aligned.  A decode step is a call with T = 1.
+ */
+GDR_API int gdr_linear_recurrence(const void* x, const void* a, const void* b,
+                                  const float* A_log, const float* dt_bias,
+                                  const float* init_state, float* out, float* final_state,
+                                  const int32_t* cu_seqlens, int B, int T, int C, long long ld,
+                                  gdr_stream_t stream);
+GDR_API int gdr_linear_recurrence_f32(const float* x, const float* a, const float* b,
+                                      const float* A_log, const float* dt_bias,
+                                      const float* init_state, float* out, float* final_state,
+                                      const int32_t* cu_seqlens, int B, int T, int C,
+                                      long long ld, gdr_stream_t stream);
+
+/*
+ * Its backward pass, from the forward call's inputs and its `out`, the gradient grad_out
+ * [B, T, C] fp32 of out and grad_final_state [B, C] fp32 of the final state (NULL = zeros).
+ * With D_t the gradient of h after token t (D_t = grad_out_t + exp(g_{t+1}) D_{t+1}; the
+ * last token of a sequence takes grad_final_state instead of the second term), i = sigmoid(b):
+ *   grad_x = i D,  grad_b = x D i (1 - i),  grad_a = -exp(A_log) sigmoid(a + dt_bias) u
+ *   with u_t = exp(g_t) h_{t-1} D_t          (x's type; rows ld_grad elements apart)
+ *   grad_A_log [C] = sum of u g,  grad_dt_bias [C] = sum of grad_a  (fp32, over all tokens)
+ *   grad_init_state [B, C] = exp(g_0) D_0 of each sequence (fp32, NULL to skip; may be
+ *   grad_final_state).
+ * No other output may overlap an input.  Rows outside the sequences are left as they were.
+ */
+GDR_API int gdr_linear_recurrence_backward(const void* x, const void* a, const void* b,
+                                           const float* A_log, const float* dt_bias,
+                                           const float* init_state, const float* out,
+                                           const float* grad_out, const float* grad_final_state,
+                                           void* grad_x, void* grad_a, void* grad_b,
+                                           float* grad_A_log, float* grad_dt_bias,
+                                           float* grad_init_state, const int32_t* cu_seqlens,
+                                           int B, int T, int C, long long ld, long long ld_grad,
+                                           gdr_stream_t stream);
+GDR_API int gdr_linear_recurrence_backward_f32(
+    const float* x, const float* a, const float* b, const float* A_log, const float* dt_bias,
+    const float* init_state, const float* out, const float* grad_out,
+    const float* grad_final_state, float* grad_x, float* grad_a, float* grad_b,
+    float* grad_A_log, float* grad_dt_bias, float* grad_init_state, const int32_t* cu_seqlens,
+    int B, int T, int C, long long ld, long long ld_grad, gdr_stream_t stream);
 
 /*
  * Device-side status of the kernels enqueued so far.  Synchronises `stream`, then returns

@@ -1,0 +1,372 @@
+"""The gated linear recurrence (gdr_linear_recurrence[_f32] and its backward calls) against the
+fp64 oracle, and its refusals.
+
+Tolerances, from the arithmetic before any run.  With u = 2^-22 (the special-function unit's
+exponential and reciprocal; fp32 roundings are 2^-24): the relative error of a log-decay is a
+few u, and x e^-x <= 0.37 bounds what it does to a decay; a state passes at most 16 rounded
+per-token decays inside a tile, 8 joins of tile parts, and one join of two roundings per 64
+tokens.  So |err h| <= (32 + T / 64) u * H with H the same recurrence over absolute values,
+likewise for the adjoint D; products of both get the sum of the two, and sums over tokens
+(64 + T / 16) u of the sum of magnitudes.  A bf16 output adds half a step, 2^-8 of its value."""
+
+import numpy as np
+import pytest
+
+import gated_delta_rule_145_b200 as gdr
+from gated_delta_rule_145_b200 import synth
+from oracle import block
+
+torch = pytest.importorskip("torch")
+U = 2.0 ** -22
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+NAMES = ("h", "final", "dx", "da", "db", "dA_log", "ddt_bias", "dinit")
+
+
+def make(B, T, C, dtype="bf16", seed=0, lens=None, init=True, gate_scale=1.0):
+    rng = np.random.default_rng(seed)
+    cu = None
+    if lens is not None:
+        cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        B, T = 1, max(T, int(cu[-1]))
+    n = B if cu is None else len(lens)
+    r = synth.round_to_bf16 if dtype == "bf16" else (lambda v: v)
+    f = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+    dt = np.exp(rng.uniform(np.log(1e-3), np.log(1e-1), C))
+    return dict(x=r(f(B, T, C)), a=r(gate_scale * f(B, T, C)), b=r(gate_scale * f(B, T, C)),
+                A_log=rng.uniform(0, synth.LN16, C).astype(np.float32),
+                dt_bias=np.log(np.expm1(dt)).astype(np.float32),
+                init=f(n, C) if init else None, cu=cu, go=f(B, T, C),
+                gf=f(n, C) if init else None, dtype=dtype, n=n)
+
+
+def dev(v, dtype=None):
+    if v is None:
+        return None
+    t = torch.from_numpy(np.ascontiguousarray(v)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def on_gpu(m, fused=False):
+    """(arguments of the forward call, out, final, the six gradients)"""
+    dt = torch.bfloat16 if m["dtype"] == "bf16" else torch.float32
+    x, a, b = (dev(m[k], dt) for k in ("x", "a", "b"))
+    if fused:
+        C = x.shape[2]
+        x, a, b = torch.cat([x, a, b], 2).split(C, 2)
+    args = (x, a, b, dev(m["A_log"]), dev(m["dt_bias"]))
+    init, cu = dev(m["init"]), dev(m["cu"])
+    out, final = gdr.linear_recurrence(*args, init, cu)
+    grads = gdr.linear_recurrence_backward(*args, out, dev(m["go"]), dev(m["gf"]), init, cu)
+    torch.cuda.synchronize()
+    assert gdr.gdr_device_status() == gdr.GDR_OK
+    return args, (out, final) + tuple(grads)
+
+
+def expected(m):
+    args = (m["x"], m["a"], m["b"], m["A_log"], m["dt_bias"])
+    ref = block.linear_recurrence(*args, m["init"], m["cu"])
+    ref += block.linear_recurrence_backward(*args, m["go"], m["gf"], m["init"], m["cu"])
+    return ref, block.recurrence_magnitude(*args, m["go"], m["gf"], m["init"], m["cu"])
+
+
+def check(m, got, ref, mag, longest):
+    state, both, sums = 32 + longest / 64, 80 + longest / 32, 96 + m["x"].shape[1] / 16
+    factor = dict(h=state, final=state, dx=4 + state, da=both, db=8 + state, dA_log=sums,
+                  ddt_bias=sums, dinit=4 + state)
+    for name, g, r, k in zip(NAMES, got, ref, mag):
+        g = g.float().cpu().numpy().astype(np.float64)
+        inside = np.isfinite(r)  # rows outside the sequences are not written
+        tol = factor[name] * U * k + 1e-30
+        if name in ("dx", "da", "db"):
+            tol = tol + HALF[m["dtype"]] * np.abs(r)
+        bad = ~(np.abs(g - r) <= tol) & inside
+        worst = np.max((np.abs(g - r) / tol)[inside]) if inside.any() else 0.0
+        assert not bad.any(), f"{name}: {bad.sum()} of {bad.size} outside, worst {worst:.2f} x"
+
+
+gpu = pytest.mark.gpu
+
+# lengths around the token counts of a warp (8, 16), of a tile (64, 128) and of a cluster's
+# step; channel counts around a strip (64), below one and far above
+DENSE = [(1, 1, 8), (3, 1, 64), (64, 1, 72), (2, 2, 136), (1, 15, 64), (2, 16, 64), (1, 17, 8),
+         (1, 63, 64), (2, 64, 56), (1, 65, 128), (2, 127, 64), (1, 128, 200), (1, 129, 64),
+         (1, 255, 64), (3, 257, 72), (1, 1023, 64), (1, 1024, 64), (1, 1025, 8), (2, 777, 1160),
+         (1, 2500, 136), (40, 33, 64)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C", DENSE)
+def test_dense(B, T, C, dtype):
+    m = make(B, T, C, dtype, seed=T * 7 + C, init=(T + C) % 3 != 0)
+    ref, mag = expected(m)
+    check(m, on_gpu(m)[1], ref, mag, T)
+
+
+PACKED = [[1], [0, 5, 0], [1, 1, 1, 1], [17, 0, 64, 1, 130], [300, 3, 128, 129, 0, 1, 255],
+          [0, 1500, 2], [64, 64, 64], [2000]]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", PACKED)
+def test_packed(lens, dtype):
+    m = make(1, 0, 136, dtype, seed=sum(lens) + len(lens), lens=lens)
+    ref, mag = expected(m)
+    check(m, on_gpu(m)[1], ref, mag, max(lens))
+
+
+@gpu
+@pytest.mark.parametrize("B,T,C", [(1, 1, 64), (2, 300, 72), (3, 20, 136)])
+def test_slices_of_one_projection(B, T, C):
+    """x, a, b as slices of [B, T, 3 C], the gradients written into slices of one buffer:
+    bit-identical to dense inputs, and the buffer's other columns untouched"""
+    m = make(B, T, C, seed=5)
+    _, dense = on_gpu(m)
+    args, fused = on_gpu(m, fused=True)
+    for name, p, q in zip(NAMES, dense, fused):
+        assert torch.equal(p, q), name
+    pad = torch.full((B, T, 3 * C + 16), 7.0, device="cuda", dtype=torch.bfloat16)
+    gx, ga, gb = pad[..., 8:8 + 3 * C].split(C, 2)
+    gdr.linear_recurrence_backward(*args, fused[0], dev(m["go"]), dev(m["gf"]), dev(m["init"]),
+                                   grad_x=gx, grad_a=ga, grad_b=gb)
+    torch.cuda.synchronize()
+    for p, q in zip((gx, ga, gb), dense[2:5]):
+        assert torch.equal(p, q)
+    assert (pad[..., :8] == 7).all() and (pad[..., 8 + 3 * C:] == 7).all()
+
+
+@gpu
+@pytest.mark.parametrize("lens,lead", [([100, 30, 200], 0), ([3, 2], 0), ([70, 5], 12)])
+def test_rows_outside_the_sequences_stay_and_are_not_read(lens, lead):
+    """tokens before cu_seqlens[0] and behind cu_seqlens[-1] hold NaN and stay as they were"""
+    C, tail = 72, 37
+    m = make(1, 0, C, seed=3, lens=lens)
+    T = lead + sum(lens) + tail
+    big = {}
+    for k in ("x", "a", "b", "go"):
+        big[k] = np.full((1, T, C), np.nan, np.float32)
+        big[k][:, lead:lead + sum(lens)] = m[k]
+    cu = dev((m["cu"] + lead).astype(np.int32))
+    x, a, b = (dev(big[k], torch.bfloat16) for k in ("x", "a", "b"))
+    args = (x, a, b, dev(m["A_log"]), dev(m["dt_bias"]))
+    out = torch.full((1, T, C), 5.0, device="cuda")
+    grads = [torch.full((1, T, C), 5.0, device="cuda", dtype=torch.bfloat16) for _ in range(3)]
+    _, final = gdr.linear_recurrence(*args, dev(m["init"]), cu, out=out)
+    kept = out.clone()
+    kept[:, :lead] = float("nan")
+    kept[:, lead + sum(lens):] = float("nan")
+    got = gdr.linear_recurrence_backward(*args, kept, dev(big["go"]), dev(m["gf"]),
+                                         dev(m["init"]), cu, *grads)
+    torch.cuda.synchronize()
+    _, want = on_gpu(m)
+    for v, w in zip((out,) + got[:3], (want[0],) + want[2:5]):
+        assert (v[:, :lead] == 5).all() and (v[:, lead + sum(lens):] == 5).all()
+        assert torch.equal(v[:, lead:lead + sum(lens)], w)
+    assert torch.equal(final, want[1])
+    for v, w in zip(got[3:], want[5:]):
+        assert torch.equal(v, w)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_extreme_gates(dtype):
+    """decays that underflow in one token, decays of exactly 1, closed and open input gates"""
+    m = make(2, 300, 64, dtype, seed=11)
+    m["a"][:, ::3] = -200.0
+    m["a"][:, 1::7] = 100.0
+    m["b"][:, ::5] = 150.0
+    m["b"][:, 2::5] = -150.0
+    ref, mag = expected(m)
+    check(m, on_gpu(m)[1], ref, mag, 300)
+
+
+@gpu
+def test_infinite_and_nan_inputs_stay_in_their_channel_and_after_their_token():
+    m = make(2, 200, 64, "f32", seed=12, init=False)
+    clean = on_gpu(m)[1]
+    m["x"][0, 90, 3] = np.inf
+    m["x"][0, 100, 5] = np.nan
+    out, final = on_gpu(m)[1][:2]
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, 90:, 3] = True
+    hit[0, 100:, 5] = True
+    assert torch.equal(out[~hit], clean[0][~hit])
+    assert torch.isinf(out[0, 90, 3]) and torch.isnan(out[0, 100:, 5]).all()
+    assert torch.equal(final[1], clean[1][1])
+
+
+@gpu
+@pytest.mark.parametrize("T0", [1, 40, 300])
+def test_steps_continue_a_prompt_in_place(T0):
+    """a prompt, then single-token calls that update the state in place, equal one call"""
+    m = make(3, T0 + 6, 136, seed=T0)
+    args, want = on_gpu(m)
+    x, a, b, A, dt = args
+    part = lambda t, lo, hi: t[:, lo:hi].contiguous()  # noqa: E731
+    outs = []
+    out, state = gdr.linear_recurrence(*(part(t, 0, T0) for t in (x, a, b)), A, dt,
+                                       dev(m["init"]))
+    outs.append(out)
+    for t in range(T0, T0 + 6):
+        o, s = gdr.linear_recurrence(*(part(v, t, t + 1) for v in (x, a, b)), A, dt, state,
+                                     final_state=state)
+        assert s is state
+        outs.append(o)
+    torch.cuda.synchronize()
+    ref, mag = expected(m)
+    got = torch.cat(outs, 1).cpu().numpy()
+    assert (np.abs(got - ref[0]) <= (40 + T0 / 64) * U * mag[0] + 1e-30).all()
+    assert (np.abs(state.cpu().numpy() - ref[1]) <= (40 + T0 / 64) * U * mag[1] + 1e-30).all()
+
+
+@gpu
+def test_no_tokens():
+    C = 64
+    e = torch.empty((2, 0, C), device="cuda", dtype=torch.bfloat16)
+    p = torch.zeros(C, device="cuda")
+    init, gf = torch.randn(2, C, device="cuda"), torch.randn(2, C, device="cuda")
+    out, final = gdr.linear_recurrence(e, e, e, p, p, init)
+    g = gdr.linear_recurrence_backward(e, e, e, p, p, out, torch.empty(2, 0, C, device="cuda"),
+                                       gf, init)
+    torch.cuda.synchronize()
+    assert torch.equal(final, init) and torch.equal(g[5], gf)
+    assert (g[3] == 0).all() and (g[4] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("B,T,C", [(1, 700, 64), (4, 300, 136), (64, 1, 64), (5, 9, 64)])
+def test_same_bits_again_alone_and_from_a_graph(B, T, C):
+    m = make(B, T, C, seed=B + T)
+    args, first = on_gpu(m)
+    _, again = on_gpu(m)
+    for name, p, q in zip(NAMES, first, again):
+        assert torch.equal(p, q), name
+    # the first sequence alone
+    one = dict(m, x=m["x"][:1], a=m["a"][:1], b=m["b"][:1], go=m["go"][:1], n=1)
+    if m["init"] is not None:
+        one.update(init=m["init"][:1], gf=m["gf"][:1])
+    alone = on_gpu(one)[1]
+    U_ = (32 + T / 64) * U
+    mag = expected(one)[1]
+    diff = (alone[0][0] - first[0][0]).abs().cpu().numpy()
+    assert (diff <= 2 * U_ * mag[0][0] + 1e-30).all()
+    # captured once, replayed twice on fresh inputs in the same buffers
+    init, go, gf = dev(m["init"]), dev(m["go"]), dev(m["gf"])
+    out, final = torch.empty_like(first[0]), torch.empty_like(first[1])
+    graph, cap = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=cap):
+        gdr.linear_recurrence(*args, init, out=out, final_state=final, stream=cap)
+        grads = gdr.linear_recurrence_backward(*args, out, go, gf, init, stream=cap)
+    torch.cuda.current_stream().wait_stream(cap)
+    for _ in range(2):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, p, q in zip(NAMES, (out, final) + tuple(grads), first):
+            assert torch.equal(p, q), name
+    assert gdr.gdr_device_status() == gdr.GDR_OK
+    del graph
+
+
+@gpu
+def test_two_streams_at_once():
+    """calls on two streams without ordering between them: each has its own workspace"""
+    ms = [make(2, 400, 136, seed=s) for s in (1, 2)]
+    want = [on_gpu(m)[1] for m in ms]
+    streams = [torch.cuda.Stream() for _ in ms]
+    ready = []
+    for m in ms:
+        dt = torch.bfloat16
+        ready.append(([dev(m[k], dt) for k in ("x", "a", "b")] + [dev(m["A_log"]), dev(m["dt_bias"])],
+                      dev(m["init"]), dev(m["go"]), dev(m["gf"])))
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            args, init, go, gf = ready[i]
+            with torch.cuda.stream(s):
+                out, final = gdr.linear_recurrence(*args, init)
+                got[i] = (out, final) + gdr.linear_recurrence_backward(*args, out, go, gf, init)
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for name, p, q in zip(NAMES, w, g):
+            assert torch.equal(p, q), name
+
+
+# --------------------------------------------------------------------------- refusals (no GPU)
+
+A = 1 << 20  # fake aligned addresses: every call below fails a check before any launch
+
+
+def _fwd(name="gdr_linear_recurrence", **kw):
+    args = dict(x=A, a=A, b=A, A_log=A, dt_bias=A, init_state=None, out=A, final_state=None,
+                cu_seqlens=None, B=1, T=16, C=64, ld=64)
+    args.update(kw)
+    return getattr(gdr, name)(**args, stream=0, check=False)
+
+
+def _bwd(name="gdr_linear_recurrence_backward", **kw):
+    args = dict(x=A, a=A, b=A, A_log=A, dt_bias=A, init_state=None, out=A, grad_out=A,
+                grad_final_state=None, grad_x=A, grad_a=A, grad_b=A, grad_A_log=A,
+                grad_dt_bias=A, grad_init_state=None, cu_seqlens=None, B=1, T=16, C=64, ld=64,
+                ld_grad=64)
+    args.update(kw)
+    return getattr(gdr, name)(**args, stream=0, check=False)
+
+
+@pytest.mark.parametrize("call,suffix", [(_fwd, ""), (_fwd, "_f32"), (_bwd, ""), (_bwd, "_f32")])
+def test_refusals(call, suffix):
+    name = call.__defaults__[0] + suffix
+    for p in ("x", "a", "b", "A_log", "dt_bias", "out"):
+        assert call(name, **{p: None}) == gdr.GDR_ERR_NULL, p
+    for kw in (dict(B=0), dict(T=-1), dict(C=0), dict(C=60), dict(ld=56), dict(ld=68),
+               dict(C=64, ld=32), dict(B=1 << 20, T=1 << 12), dict(ld=1 << 40)):
+        assert call(name, **kw) == gdr.GDR_ERR_SHAPE, kw
+    for p in ("x", "a", "b", "out", "init_state"):
+        assert call(name, **{p: A + 8}) == gdr.GDR_ERR_ALIGN, p
+    for p in ("A_log", "dt_bias", "cu_seqlens"):
+        assert call(name, **{p: A + 2}) == gdr.GDR_ERR_ALIGN, p
+    if call is _fwd:
+        assert call(name, final_state=A + 8) == gdr.GDR_ERR_ALIGN
+    else:
+        for p in ("grad_out", "grad_x", "grad_a", "grad_b", "grad_A_log", "grad_dt_bias"):
+            assert call(name, **{p: None}) == gdr.GDR_ERR_NULL, p
+        for p in ("grad_out", "grad_x", "grad_a", "grad_b", "grad_final_state",
+                  "grad_init_state"):
+            assert call(name, **{p: A + 8}) == gdr.GDR_ERR_ALIGN, p
+        assert call(name, ld_grad=56) == gdr.GDR_ERR_SHAPE
+        assert call(name, ld_grad=68) == gdr.GDR_ERR_SHAPE
+
+
+def test_binding_refuses_cpu_tensors():
+    x, p = torch.zeros(1, 4, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdr.linear_recurrence(x, x, x, p, p)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdr.linear_recurrence_backward(x, x, x, p, p, x, x)
+
+
+@gpu
+def test_binding_refuses_what_does_not_fit():
+    x, p = torch.zeros(2, 4, 64, device="cuda"), torch.zeros(64, device="cuda")
+    h = x.half()
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        gdr.linear_recurrence(h, h, h, p, p)
+    with pytest.raises(ValueError, match="a must be"):
+        gdr.linear_recurrence(x, x.bfloat16(), x, p, p)
+    with pytest.raises(ValueError, match="shape"):
+        gdr.linear_recurrence(x, x, x, p[:8], p)
+    with pytest.raises(ValueError, match="layout"):
+        gdr.linear_recurrence(x, x.transpose(0, 1).contiguous().transpose(0, 1), x, p, p)
+    with pytest.raises(ValueError, match="layout"):
+        gdr.linear_recurrence(x, x[:1].expand(2, 4, 64), x, p, p)
+    with pytest.raises(ValueError, match="B == 1"):
+        gdr.linear_recurrence(x, x, x, p, p, cu_seqlens=torch.zeros(2, device="cuda",
+                                                                    dtype=torch.int32))
+    with pytest.raises(ValueError, match="together"):
+        gdr.linear_recurrence_backward(x, x, x, p, p, x, x, grad_x=x)
+    with pytest.raises(gdr.GdrError):
+        gdr.linear_recurrence(x[..., :60].contiguous(), x[..., :60].contiguous(),
+                              x[..., :60].contiguous(), p[:60], p[:60])
