@@ -96,6 +96,8 @@ struct RecurrenceGrads {
 cudaError_t launch_recurrence(const RecurrenceParams& p, cudaStream_t stream);
 cudaError_t launch_recurrence_backward(const RecurrenceParams& p, const RecurrenceGrads& r,
                                        cudaStream_t stream);
+// Reads and clears the tiled recurrence's timeout record (nonzero if set, -1 on error).
+int read_and_clear_recurrence_status();
 
 // Layer normalisation of rows of d values (d a multiple of 8, at most 32768); layer_norm.cu.
 struct LayerNormParams {
@@ -174,7 +176,7 @@ cudaError_t workspace_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 size_t noalloc_scratch_bytes();
 cudaError_t noalloc_scratch(void** ptr);
 
-// Reads and clears the tensor-core kernels', the tiled convolution's and the self-test's
+// Reads and clears the tensor-core kernels', the tiled convolution's and recurrence's and the self-test's
 // timeout records (nonzero if set, 0 if not, -1 on a CUDA error); workspace.cu.
 int read_and_clear_tc_status();
 

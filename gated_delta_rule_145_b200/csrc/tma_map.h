@@ -53,4 +53,20 @@ inline bool make_bf16_map_plain(CUtensorMap* map, const void* base, uint64_t wid
            CUDA_SUCCESS;
 }
 
+// As make_bf16_map_plain for bf16 or fp32 elements and rows `pitch` elements apart (pitch x
+// element size a multiple of 16 bytes, pitch >= width).
+inline bool make_map_pitched(CUtensorMap* map, const void* base, bool f32, uint64_t width,
+                             uint64_t rows, uint64_t pitch, uint32_t box_w, uint32_t box_h) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {width, rows};
+    const cuuint64_t strides[1] = {pitch * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {box_w, box_h};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gdr
