@@ -252,14 +252,20 @@ constexpr int kStrip = 64;
 constexpr int kMaxCluster = 8;
 constexpr int kTileThreads = 32 * kWarps;
 
-template <typename Tin, int TOK, int STAGES>
+// Shared memory of a CTA: per slot the x, a, b tiles, and for the backward pass dout's.
+template <typename Tin_, int TOK_, int STAGES_, bool Grad>
 struct alignas(128) TileSmem {
-    static constexpr int kRows = kWarps * TOK;
-    Tin in[STAGES][3][kRows][kStrip];
+    using Tin = Tin_;
+    static constexpr int TOK = TOK_, STAGES = STAGES_, kRows = kWarps * TOK;
+    struct alignas(128) Slot {
+        Tin in[3][kRows][kStrip];
+        float dout[Grad ? kRows : 1][Grad ? kStrip : 4];
+    };
+    Slot slot[STAGES];
     float4 part[2][kWarps][32];       // per warp and lane: P pair, H pair; by step parity
     float2 log_part[2][kWarps][32];   // log2 of P
     float4 peer[2][kMaxCluster][32];  // the cluster's tiles: coded factor pair, H pair
-    uint64_t full[STAGES];
+    uint64_t full[STAGES], peers_in[2];
 };
 
 // The factor 2^y, y <= 0, coded for carry(): for y > -0.5, W = expm1(y ln 2) with its sign
@@ -292,13 +298,40 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Store to the same shared-memory variable of CTA `rank` of this cluster.
-__device__ __forceinline__ void store_peer(float4* p, uint32_t rank, float4 v) {
-    uint32_t a;
+// Asynchronous store to the same shared-memory variable of CTA `rank` of this cluster; its 16
+// bytes are counted on that CTA's `bar`.  (A cluster barrier per step, whose release also
+// waits for the step's global stores, cost a third of the forward pass.)
+__device__ __forceinline__ void store_peer(float4* p, uint64_t* bar, uint32_t rank, float4 v) {
+    uint32_t a, b;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(tc::smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
                  : "memory");
+}
+// Bounded wait for a phase that peers' stores complete (acquire at cluster scope).
+__device__ __forceinline__ bool peers_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool peers_wait(uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < 64; ++i)
+        if (peers_test(bar, parity)) return true;
+    const uint64_t t0 = tc::globaltimer();
+    do {
+        for (int i = 0; i < 64; ++i) {
+            __nanosleep(tc::kPollSleepNs);
+            if (peers_test(bar, parity)) return true;
+        }
+    } while (tc::globaltimer() - t0 <= tc::kWaitLimitNs);
+    return false;
 }
 
 __device__ __forceinline__ float2 smem_pair(const float* p) {
@@ -308,32 +341,37 @@ __device__ __forceinline__ float2 smem_pair(const __nv_bfloat16* p) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
 }
 
-// The three input tiles whose first row is token `row` (before or past the tensor: zeros).
-template <typename Smem>
-__device__ __forceinline__ void load_tile(Smem& sm, int st, const CUtensorMap* mx,
-                                          const CUtensorMap* ma, const CUtensorMap* mb, int c0,
-                                          int row) {
-    tc::mbar_arrive_expect_tx(&sm.full[st], (uint32_t)sizeof(sm.in[0]));
-    tc::tma_load_2d(&sm.in[st][0][0][0], mx, c0, row, &sm.full[st]);
-    tc::tma_load_2d(&sm.in[st][1][0][0], ma, c0, row, &sm.full[st]);
-    tc::tma_load_2d(&sm.in[st][2][0][0], mb, c0, row, &sm.full[st]);
+// Tensor maps of a tiled call: boxes of kStrip channels x a tile's tokens.
+struct Maps {
+    CUtensorMap x, a, b, dout;
+};
+
+// Starts the copies of the tile whose first row is token `row` (rows before or past the tensor
+// read as zeros) into slot st.
+template <bool Grad, typename Smem>
+__device__ __forceinline__ void load_tile(Smem& sm, int st, const Maps& m, int c0, int row) {
+    auto& s = sm.slot[st];
+    tc::mbar_arrive_expect_tx(&sm.full[st],
+                              (uint32_t)(sizeof(s.in) + (Grad ? sizeof(s.dout) : 0)));
+    tc::tma_load_2d(&s.in[0][0][0], &m.x, c0, row, &sm.full[st]);
+    tc::tma_load_2d(&s.in[1][0][0], &m.a, c0, row, &sm.full[st]);
+    tc::tma_load_2d(&s.in[2][0][0], &m.b, c0, row, &sm.full[st]);
+    if constexpr (Grad) tc::tma_load_2d(&s.dout[0][0], &m.dout, c0, row, &sm.full[st]);
 }
 
 // After a wait that gave up, copies may still be in flight: the CTA stays for them (each
 // wait is bounded too).
-template <typename Smem>
-__device__ __noinline__ void wait_in_flight(Smem& sm, int stages, int tiles, int K, int rank) {
-    const int last = (tiles - 1 - rank) / K;  // this CTA's last step with a tile
-    for (int i = 0; i < stages; ++i) {
-        const int s = last - (last - i + stages) % stages;
-        if (s >= 0) tc::mbar_wait(&sm.full[i], (uint32_t)(s / stages) & 1u);
-    }
+__device__ __noinline__ void wait_in_flight(uint64_t* full, int stages, int issued) {
+    for (int s = max(0, issued - stages); s < issued; ++s)
+        tc::mbar_wait(&full[s % stages], (uint32_t)(s / stages) & 1u);
 }
 
 // From the warps' pairs in sm.part[buf] and the state S before the cluster's step: the state
 // before this warp's tokens; S moves past the step.
 template <bool Cluster, typename Smem>
-__device__ __forceinline__ float2 join(Smem& sm, int buf, int warp, int lane, float2& S) {
+__device__ __forceinline__ float2 join(Smem& sm, int step, int warp, int lane, float2& S,
+                                       bool& dead) {
+    const int buf = step & 1;
     float2 G = make_float2(0.f, 0.f), H = G, Gp = G, Hp = G;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -346,8 +384,14 @@ __device__ __forceinline__ float2 join(Smem& sm, int buf, int warp, int lane, fl
     float2 in = S;
     if constexpr (Cluster) {
         const uint32_t K = cluster_size(), rank = cluster_rank();
-        if (warp < K) store_peer(&sm.peer[buf][rank][lane], warp, all);
-        cluster_barrier();
+        if (threadIdx.x == 0)
+            tc::mbar_arrive_expect_tx(&sm.peers_in[buf], K * (uint32_t)sizeof(sm.peer[0][0]));
+        if (warp < K) store_peer(&sm.peer[buf][rank][lane], &sm.peers_in[buf], warp, all);
+        if (!dead && !peers_wait(&sm.peers_in[buf], (uint32_t)(step >> 1) & 1u)) {
+            dead = true;
+            if (lane == 0) atomicExch(&g_recurrence_status, 1);
+        }
+        __syncwarp();
         for (uint32_t k = 0; k < K; ++k) {
             if (k == rank) in = S;
             const float4 v = sm.peer[buf][k][lane];
@@ -359,49 +403,70 @@ __device__ __forceinline__ float2 join(Smem& sm, int buf, int warp, int lane, fl
     return __ffma2_rn(ex2f2(Gp), in, Hp);
 }
 
-template <typename Tin, int TOK, int STAGES, bool Cluster>
-__global__ void __launch_bounds__(kTileThreads, 2)
-recurrence_tile_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap ma,
-                       const __grid_constant__ CUtensorMap mb, RecurrenceParams p, int strips) {
-    using Smem = TileSmem<Tin, TOK, STAGES>;
-    constexpr int kRows = Smem::kRows;
+// What the CTAs of both tiled kernels share: their place, their tokens, their barriers.
+struct Place {
+    int warp, lane, K, rank, seq, c0, c, tiles, steps;
+    long long t0, t1;
+    bool in_c;
+};
+template <bool Cluster>
+__device__ __forceinline__ Place place_of(const RecurrenceParams& p, int strips, int rows) {
+    Place w;
+    w.warp = threadIdx.x / 32;
+    w.lane = threadIdx.x % 32;
+    w.K = Cluster ? (int)cluster_size() : 1;
+    w.rank = Cluster ? (int)cluster_rank() : 0;
+    const int unit = blockIdx.x / w.K;
+    w.seq = unit / strips;
+    w.c0 = unit % strips * kStrip;
+    w.c = w.c0 + 2 * w.lane;
+    w.in_c = w.c < p.C;  // C is even
+    seq_bounds(p.cu_seqlens, w.seq, p.T, w.t0, w.t1);
+    w.tiles = (int)((w.t1 - w.t0 + rows - 1) / rows);
+    w.steps = (w.tiles + w.K - 1) / w.K;
+    return w;
+}
+template <typename Smem>
+__device__ __forceinline__ void init_barriers(Smem& sm) {
+    for (int i = 0; i < Smem::STAGES; ++i) tc::mbar_init(&sm.full[i], 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.peers_in[i], 1);
+    tc::mbar_init_fence();
+}
+
+template <typename Smem, int Blocks, bool Cluster>
+__global__ void __launch_bounds__(kTileThreads, Blocks)
+recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, int strips) {
+    constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int K = Cluster ? (int)cluster_size() : 1, rank = Cluster ? (int)cluster_rank() : 0;
-    const int unit = blockIdx.x / K, strip = unit % strips, seq = unit / strips;
-    long long t0, t1;
-    seq_bounds(p.cu_seqlens, seq, p.T, t0, t1);
-    const int tiles = (int)((t1 - t0 + kRows - 1) / kRows), steps = (tiles + K - 1) / K;
-    const int c0 = strip * kStrip, c = c0 + 2 * lane;
-    const bool in_c = c < p.C;  // C is even
+    const Place w = place_of<Cluster>(p, strips, kRows);
     Channels ch = {};
-    if (in_c) ch = load_channels(p.A_log, p.dt_bias, c);
-    const size_t at = (size_t)seq * p.C + c;
-    float2 S = in_c && p.init_state ? *reinterpret_cast<const float2*>(p.init_state + at)
-                                    : make_float2(0.f, 0.f);
+    if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
+    const size_t at = (size_t)w.seq * p.C + w.c;
+    float2 S = w.in_c && p.init_state ? *reinterpret_cast<const float2*>(p.init_state + at)
+                                      : make_float2(0.f, 0.f);
+    int issued = 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) tc::mbar_init(&sm.full[i], 1);
-        tc::mbar_init_fence();
-        for (int i = 0; i < STAGES && i * K + rank < tiles; ++i)
-            load_tile(sm, i, &mx, &ma, &mb, c0, (int)(t0 + (long long)(i * K + rank) * kRows));
+        init_barriers(sm);
+        for (; issued < STAGES && issued * w.K + w.rank < w.tiles; ++issued)
+            load_tile<false>(sm, issued, maps, w.c0,
+                             (int)(w.t0 + (long long)(issued * w.K + w.rank) * kRows));
     }
     // the barriers are set up; in a cluster, every CTA has started and has read its state
     if constexpr (Cluster) cluster_barrier(); else __syncthreads();
     bool dead = false;
-    for (int step = 0; step < steps; ++step) {
-        const int tile = step * K + rank, st = step % STAGES, buf = step & 1;
-        const bool have = tile < tiles;
+    for (int step = 0; step < w.steps; ++step) {
+        const int tile = step * w.K + w.rank, st = step % STAGES, buf = step & 1;
         // tokens of this warp within the sequence
-        const long long w0 = t0 + (long long)tile * kRows + warp * TOK;
-        const int live = (int)min((long long)TOK, max(0LL, t1 - w0));
-        if (have && !dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
+        const long long first = w.t0 + (long long)tile * kRows + w.warp * TOK;
+        const int live = (int)min((long long)TOK, max(0LL, w.t1 - first));
+        if (tile < w.tiles && !dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
             dead = true;
-            if (lane == 0) atomicExch(&g_recurrence_status, 1);
+            if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
         }
         __syncwarp();
         float2 lam[TOK], u[TOK], G = make_float2(0.f, 0.f), H = G;
-        const Tin* row = &sm.in[st][0][warp * TOK][2 * lane];
+        const auto* row = &sm.slot[st].in[0][w.warp * TOK][2 * w.lane];
         auto gates = [&](int i) {
             const float2 xv = smem_pair(row + i * kStrip);
             const float2 av = smem_pair(row + (kRows + i) * kStrip);
@@ -426,16 +491,18 @@ recurrence_tile_kernel(const __grid_constant__ CUtensorMap mx, const __grid_cons
                 }
             }
         }
-        sm.part[buf][warp][lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
-        sm.log_part[buf][warp][lane] = G;
+        sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
+        sm.log_part[buf][w.warp][w.lane] = G;
         __syncthreads();
         // every warp has read the tile: its slot takes the tile STAGES steps ahead
-        if (threadIdx.x == 0 && !dead && tile + STAGES * K < tiles)
-            load_tile(sm, st, &mx, &ma, &mb, c0,
-                      (int)(t0 + (long long)(tile + STAGES * K) * kRows));
-        float2 h = join<Cluster>(sm, buf, warp, lane, S);
-        float* out = p.out + w0 * p.C + c;
-        if (in_c) {
+        if (threadIdx.x == 0 && !dead && issued * w.K + w.rank < w.tiles) {
+            load_tile<false>(sm, st, maps, w.c0,
+                             (int)(w.t0 + (long long)(issued * w.K + w.rank) * kRows));
+            ++issued;
+        }
+        float2 h = join<Cluster>(sm, step, w.warp, w.lane, S, dead);
+        float* out = p.out + first * p.C + w.c;
+        if (w.in_c) {
             if (live == TOK) {
 #pragma unroll
                 for (int i = 0; i < TOK; ++i) {
@@ -450,84 +517,89 @@ recurrence_tile_kernel(const __grid_constant__ CUtensorMap mx, const __grid_cons
                 }
             }
             // the warp with the sequence's last token: its h, so that the two agree
-            if (live > 0 && w0 + live == t1 && p.final_state)
+            if (live > 0 && first + live == w.t1 && p.final_state)
                 *reinterpret_cast<float2*>(p.final_state + at) = h;
         }
         __syncwarp();
     }
-    if (tiles == 0 && rank == 0 && warp == 0 && in_c && p.final_state)
+    if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && p.final_state)
         *reinterpret_cast<float2*>(p.final_state + at) = S;
-    if (dead && threadIdx.x == 0) wait_in_flight(sm, STAGES, tiles, K, rank);
+    if (dead && threadIdx.x == 0) wait_in_flight(sm.full, STAGES, issued);
+    // no CTA leaves while a peer may still store to it
+    if constexpr (Cluster) cluster_barrier();
 }
 
 // The same pass against time: with E the gradient that reaches h_t from later tokens,
 // D_t = dout_t + E and E <- exp(g_t) D_t, so tokens are taken from the last one back and a
 // warp's pair is (P, H) of E.  Tiles are counted from the sequence's end.  Everything that
 // multiplies D is formed while the tile is read, so that the second run over a warp's tokens,
-// after the join, is short.  dout and h come by plain loads issued before the tile is
-// waited for.  part [units * K][2 C]: each CTA's sums for A_log and dt_bias.
-template <typename Tin, int TOK, int STAGES, bool Cluster>
-__global__ void __launch_bounds__(kTileThreads, 2)
-recurrence_tile_backward_kernel(const __grid_constant__ CUtensorMap mx,
-                                const __grid_constant__ CUtensorMap ma,
-                                const __grid_constant__ CUtensorMap mb, RecurrenceParams p,
+// after the join, is short.  h comes by plain loads, one step ahead.
+// part [units * K][2 C]: each CTA's sums for A_log and dt_bias.
+template <typename Smem, int Blocks, bool Cluster>
+__global__ void __launch_bounds__(kTileThreads, Blocks)
+recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrenceParams p,
                                 RecurrenceGrads r, float* part, int strips) {
-    using Smem = TileSmem<Tin, TOK, STAGES>;
-    constexpr int kRows = Smem::kRows;
+    constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
+    using Tin = typename Smem::Tin;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int K = Cluster ? (int)cluster_size() : 1, rank = Cluster ? (int)cluster_rank() : 0;
-    const int unit = blockIdx.x / K, strip = unit % strips, seq = unit / strips;
-    long long t0, t1;
-    seq_bounds(p.cu_seqlens, seq, p.T, t0, t1);
-    const int tiles = (int)((t1 - t0 + kRows - 1) / kRows), steps = (tiles + K - 1) / K;
-    const int c0 = strip * kStrip, c = c0 + 2 * lane;
-    const bool in_c = c < p.C;  // C is even
+    const Place w = place_of<Cluster>(p, strips, kRows);
     Channels ch = {};
-    if (in_c) ch = load_channels(p.A_log, p.dt_bias, c);
-    const size_t at = (size_t)seq * p.C + c;
+    if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
+    const size_t at = (size_t)w.seq * p.C + w.c;
     const float2 zero = make_float2(0.f, 0.f);
-    float2 S = in_c && r.grad_final ? *reinterpret_cast<const float2*>(r.grad_final + at) : zero;
-    const float2 init = in_c && p.init_state
-                            ? *reinterpret_cast<const float2*>(p.init_state + at) : zero;
+    float2 S = w.in_c && r.grad_final ? *reinterpret_cast<const float2*>(r.grad_final + at) : zero;
+    int issued = 0;
+    // a sequence's first tile may start before it, at a negative row even
+    auto first_row = [&](int step) {
+        return (int)(w.t1 - (long long)(step * w.K + w.rank + 1) * kRows);
+    };
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) tc::mbar_init(&sm.full[i], 1);
-        tc::mbar_init_fence();
-        // a sequence's first tile may start before it, at a negative row even
-        for (int i = 0; i < STAGES && i * K + rank < tiles; ++i)
-            load_tile(sm, i, &mx, &ma, &mb, c0, (int)(t1 - (long long)(i * K + rank + 1) * kRows));
+        init_barriers(sm);
+        for (; issued < STAGES && issued * w.K + w.rank < w.tiles; ++issued)
+            load_tile<true>(sm, issued, maps, w.c0, first_row(issued));
     }
+    // the states before a step's tokens of this warp: last, last - 1, ...
+    float2 prev[TOK];
+    auto load_prev = [&](int step) {
+        const long long last = w.t1 - (long long)(step * w.K + w.rank) * kRows - w.warp * TOK - 1;
+        const float* h = p.out + (last - 1) * p.C + w.c;
+        if (last - TOK >= w.t0 && w.in_c) {
+#pragma unroll
+            for (int i = 0; i < TOK; ++i) prev[i] = load_pair(h - (size_t)i * p.C);
+        } else {
+#pragma unroll
+            for (int i = 0; i < TOK; ++i) {
+                prev[i] = zero;
+                if (w.in_c && last - i > w.t0) prev[i] = load_pair(h - (size_t)i * p.C);
+                if (w.in_c && last - i == w.t0 && p.init_state)
+                    prev[i] = *reinterpret_cast<const float2*>(p.init_state + at);
+            }
+        }
+    };
+    load_prev(0);
     if constexpr (Cluster) cluster_barrier(); else __syncthreads();
     float2 acc_A = zero, acc_bias = zero;
     bool dead = false;
-    for (int step = 0; step < steps; ++step) {
-        const int tile = step * K + rank, st = step % STAGES, buf = step & 1;
-        const bool have = tile < tiles;
-        // this warp's tokens: last, last - 1, ...
-        const long long last = t1 - (long long)tile * kRows - warp * TOK - 1;
-        const int live = have ? (int)min((long long)TOK, max(0LL, last + 1 - t0)) : 0;
-        float2 d[TOK], prev[TOK];
-#pragma unroll
-        for (int i = 0; i < TOK; ++i) {
-            const bool in = i < live && in_c;
-            d[i] = in ? load_pair(r.grad_out + (last - i) * p.C + c) : zero;
-            prev[i] = !in ? zero : last - i > t0 ? load_pair(p.out + (last - i - 1) * p.C + c) : init;
-        }
-        if (have && !dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
+    for (int step = 0; step < w.steps; ++step) {
+        const int tile = step * w.K + w.rank, st = step % STAGES, buf = step & 1;
+        const long long last = w.t1 - (long long)tile * kRows - w.warp * TOK - 1;
+        const int live = (int)min((long long)TOK, max(0LL, last + 1 - w.t0));
+        if (tile < w.tiles && !dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
             dead = true;
-            if (lane == 0) atomicExch(&g_recurrence_status, 1);
+            if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
         }
         __syncwarp();
         GradFactors f[TOK];
         float2 G = zero, H = zero;
-        const Tin* row = &sm.in[st][0][kRows - 1 - warp * TOK][2 * lane];
+        const auto* row = &sm.slot[st].in[0][kRows - 1 - w.warp * TOK][2 * w.lane];
+        const float* dout = &sm.slot[st].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
         auto gates = [&](int i) {
             float2 y;
             f[i] = grad_factors(smem_pair(row - i * kStrip), smem_pair(row + (kRows - i) * kStrip),
                                 smem_pair(row + (2 * kRows - i) * kStrip), prev[i], ch, y);
             G = __fadd2_rn(G, y);
-            H = __fmul2_rn(f[i].lam, __fadd2_rn(d[i], H));
+            H = __fmul2_rn(f[i].lam, __fadd2_rn(smem_pair(dout - i * kStrip), H));
         };
         if (live == TOK) {
 #pragma unroll
@@ -538,49 +610,59 @@ recurrence_tile_backward_kernel(const __grid_constant__ CUtensorMap mx,
                 if (i < live) gates(i);
             }
         }
-        sm.part[buf][warp][lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
-        sm.log_part[buf][warp][lane] = G;
+        if (step + 1 < w.steps) load_prev(step + 1);
+        sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
+        sm.log_part[buf][w.warp][w.lane] = G;
         __syncthreads();
-        if (threadIdx.x == 0 && !dead && tile + STAGES * K < tiles)
-            load_tile(sm, st, &mx, &ma, &mb, c0,
-                      (int)(t1 - (long long)(tile + STAGES * K + 1) * kRows));
-        float2 E = join<Cluster>(sm, buf, warp, lane, S);
-        if (in_c) {
-            Tin* dx = static_cast<Tin*>(r.grad_x) + last * r.ld_grad + c;
-            Tin* da = static_cast<Tin*>(r.grad_a) + last * r.ld_grad + c;
-            Tin* db = static_cast<Tin*>(r.grad_b) + last * r.ld_grad + c;
+        // every warp is done with the step before: its slot takes the tile STAGES steps later
+        if (threadIdx.x == 0 && !dead && step > 0 && issued * w.K + w.rank < w.tiles) {
+            load_tile<true>(sm, issued % STAGES, maps, w.c0, first_row(issued));
+            ++issued;
+        }
+        float2 E = join<Cluster>(sm, step, w.warp, w.lane, S, dead);
+        if (w.in_c) {
+            Tin* dx = static_cast<Tin*>(r.grad_x) + last * r.ld_grad + w.c;
+            Tin* da = static_cast<Tin*>(r.grad_a) + last * r.ld_grad + w.c;
+            Tin* db = static_cast<Tin*>(r.grad_b) + last * r.ld_grad + w.c;
+            auto token = [&](int i) {
+                const float2 D = __fadd2_rn(smem_pair(dout - i * kStrip), E);
+                const long long o = i * r.ld_grad;
+                store_grads(f[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
+                E = __fmul2_rn(f[i].lam, D);
+            };
+            if (live == TOK) {
 #pragma unroll
-            for (int i = 0; i < TOK; ++i) {
-                if (i < live) {
-                    const float2 D = __fadd2_rn(d[i], E);
-                    store_grads(f[i], D, dx - i * r.ld_grad, da - i * r.ld_grad,
-                                db - i * r.ld_grad, acc_A, acc_bias);
-                    E = __fmul2_rn(f[i].lam, D);
+                for (int i = 0; i < TOK; ++i) token(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) {
+                    if (i < live) token(i);
                 }
             }
             // the warp with the sequence's first token
-            if (live > 0 && last + 1 - live == t0 && r.grad_init)
+            if (live > 0 && last + 1 - live == w.t0 && r.grad_init)
                 *reinterpret_cast<float2*>(r.grad_init + at) = E;
         }
         __syncwarp();
     }
-    if (tiles == 0 && rank == 0 && warp == 0 && in_c && r.grad_init)
+    if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && r.grad_init)
         *reinterpret_cast<float2*>(r.grad_init + at) = S;
     __syncthreads();
-    sm.part[0][warp][lane] = make_float4(acc_A.x, acc_A.y, acc_bias.x, acc_bias.y);
+    sm.part[0][w.warp][w.lane] = make_float4(acc_A.x, acc_A.y, acc_bias.x, acc_bias.y);
     __syncthreads();
-    if (warp == 0 && in_c) {
-        float4 s = sm.part[0][0][lane];
+    if (w.warp == 0 && w.in_c) {
+        float4 s = sm.part[0][0][w.lane];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            const float4 v = sm.part[0][w][lane];
+        for (int k = 1; k < kWarps; ++k) {
+            const float4 v = sm.part[0][k][w.lane];
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
-        float* o = part + ((size_t)seq * K + rank) * 2 * p.C + c;
+        float* o = part + ((size_t)w.seq * w.K + w.rank) * 2 * p.C + w.c;
         *reinterpret_cast<float2*>(o) = make_float2(s.x, s.y);
         *reinterpret_cast<float2*>(o + p.C) = make_float2(s.z, s.w);
     }
-    if (dead && threadIdx.x == 0) wait_in_flight(sm, STAGES, tiles, K, rank);
+    if (dead && threadIdx.x == 0) wait_in_flight(sm.full, STAGES, issued);
+    if constexpr (Cluster) cluster_barrier();
 }
 
 // Rows of CTAs of the sequential form: the partial sums have one row each.
@@ -603,15 +685,14 @@ int mean_length(const RecurrenceParams& p) {
 bool use_tiles(const RecurrenceParams& p) { return mean_length(p) > 16; }
 
 // CTAs per cluster for `units` (sequence, strip) pairs of `tiles` tiles: the K that keeps the
-// largest share of the SMs' slots (two CTAs each) at work until the last wave is done.
-int cluster_of(long long units, int tiles) {
+// largest share of the SMs' slots (`blocks` CTAs each) at work until the last wave is done.
+int cluster_of(long long units, int tiles, int blocks) {
     const int sms = sm_count(), most = std::min(tiles, kMaxCluster);
     int best = 1;
     double best_share = 0.0;
     for (int K = 1; K <= most; ++K) {
-        const long long n = units * K;
-        const long long width = n <= sms ? sms : 2LL * sms;
-        const double share = (double)n / (double)((n + width - 1) / width * width);
+        const long long n = units * K, per = std::min<long long>(blocks, (n + sms - 1) / sms);
+        const double share = (double)n / (double)((n + per * sms - 1) / (per * sms) * per * sms);
         if (share > best_share + 0.02) best = K, best_share = share;
     }
     return best;
@@ -636,51 +717,68 @@ cudaError_t launch_tiles(Kernel kernel, long long grid, int K, size_t smem, cuda
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-struct Maps {
-    CUtensorMap x, a, b;
-};
-bool make_maps(Maps& m, const RecurrenceParams& p, int rows_of_box) {
+bool make_maps(Maps& m, const RecurrenceParams& p, const float* dout, int box) {
     const uint64_t rows = p.cu_seqlens ? (uint64_t)p.T : (uint64_t)p.nseq * p.T;
     const bool f32 = p.in == InType::F32;
-    return make_map_pitched(&m.x, p.x, f32, p.C, rows, p.ld, kStrip, rows_of_box) &&
-           make_map_pitched(&m.a, p.a, f32, p.C, rows, p.ld, kStrip, rows_of_box) &&
-           make_map_pitched(&m.b, p.b, f32, p.C, rows, p.ld, kStrip, rows_of_box);
+    return make_map_pitched(&m.x, p.x, f32, p.C, rows, p.ld, kStrip, box) &&
+           make_map_pitched(&m.a, p.a, f32, p.C, rows, p.ld, kStrip, box) &&
+           make_map_pitched(&m.b, p.b, f32, p.C, rows, p.ld, kStrip, box) &&
+           (!dout || make_map_pitched(&m.dout, dout, true, p.C, rows, p.C, kStrip, box));
 }
 
-// Tokens per warp.  Forward holds two values per token and channel in registers, 16 bf16
-// tokens; fp32 tiles are twice as large in shared memory, and backward holds six values.
-template <typename Tin> constexpr int kFwdTok = sizeof(Tin) == 2 ? 16 : 8;
-constexpr int kBwdTok = 8;
-constexpr int kStages = 2;
+// Tokens per warp, slots, CTAs per SM.
+#ifndef FTOK
+#define FTOK 8
+#define FST 2
+#define FBL 3
+#define BTOK 8
+#define BST 2
+#define BBL 2
+#define GTOK 4
+#define GST 2
+#define GBL 2
+#endif
+template <typename Tin>
+struct Form {
+    static constexpr bool kBf16 = sizeof(Tin) == 2;
+    using Fwd = TileSmem<Tin, FTOK, FST, false>;
+    static constexpr int kFwdBlocks = kBf16 ? FBL : 2;
+    using Bwd = TileSmem<Tin, kBf16 ? BTOK : GTOK, kBf16 ? BST : GST, true>;
+    static constexpr int kBwdBlocks = kBf16 ? BBL : GBL;
+};
 
 template <typename Tin>
 cudaError_t forward_tiles(const RecurrenceParams& p, cudaStream_t stream) {
-    using Smem = TileSmem<Tin, kFwdTok<Tin>, kStages>;
+    using Smem = typename Form<Tin>::Fwd;
+    constexpr int kBlocks = Form<Tin>::kFwdBlocks;
     const int strips = (p.C + kStrip - 1) / kStrip;
     const long long units = (long long)p.nseq * strips;
-    const int K = cluster_of(units, (mean_length(p) + Smem::kRows - 1) / Smem::kRows);
+    const int K = cluster_of(units, (mean_length(p) + Smem::kRows - 1) / Smem::kRows, kBlocks);
     Maps m;
-    if (units * K > 0x7fffffffLL || !make_maps(m, p, Smem::kRows)) return cudaErrorNotSupported;
-    auto kernel = K > 1 ? recurrence_tile_kernel<Tin, kFwdTok<Tin>, kStages, true>
-                        : recurrence_tile_kernel<Tin, kFwdTok<Tin>, kStages, false>;
-    return launch_tiles(kernel, units * K, K, sizeof(Smem), stream, m.x, m.a, m.b, p, strips);
+    if (units * K > 0x7fffffffLL || !make_maps(m, p, nullptr, Smem::kRows))
+        return cudaErrorNotSupported;
+    auto kernel = K > 1 ? recurrence_tile_kernel<Smem, kBlocks, true>
+                        : recurrence_tile_kernel<Smem, kBlocks, false>;
+    return launch_tiles(kernel, units * K, K, sizeof(Smem), stream, m, p, strips);
 }
 
 template <typename Tin>
 cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, cudaStream_t stream) {
-    using Smem = TileSmem<Tin, kBwdTok, kStages>;
+    using Smem = typename Form<Tin>::Bwd;
+    constexpr int kBlocks = Form<Tin>::kBwdBlocks;
     const int strips = (p.C + kStrip - 1) / kStrip;
     const long long units = (long long)p.nseq * strips;
-    const int K = cluster_of(units, (mean_length(p) + Smem::kRows - 1) / Smem::kRows);
+    const int K = cluster_of(units, (mean_length(p) + Smem::kRows - 1) / Smem::kRows, kBlocks);
     Maps m;
-    if (units * K > 0x7fffffffLL || !make_maps(m, p, Smem::kRows)) return cudaErrorNotSupported;
+    if (units * K > 0x7fffffffLL || !make_maps(m, p, r.grad_out, Smem::kRows))
+        return cudaErrorNotSupported;
     const long long rows = (long long)p.nseq * K;
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);
     if (e != cudaSuccess) return e;
-    auto kernel = K > 1 ? recurrence_tile_backward_kernel<Tin, kBwdTok, kStages, true>
-                        : recurrence_tile_backward_kernel<Tin, kBwdTok, kStages, false>;
-    e = launch_tiles(kernel, units * K, K, sizeof(Smem), stream, m.x, m.a, m.b, p, r, part, strips);
+    auto kernel = K > 1 ? recurrence_tile_backward_kernel<Smem, kBlocks, true>
+                        : recurrence_tile_backward_kernel<Smem, kBlocks, false>;
+    e = launch_tiles(kernel, units * K, K, sizeof(Smem), stream, m, p, r, part, strips);
     if (e == cudaSuccess)
         e = launch_column_sum(part, rows, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
     const cudaError_t f = cudaFreeAsync(part, stream);
