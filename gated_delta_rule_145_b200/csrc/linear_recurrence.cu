@@ -23,7 +23,7 @@ namespace {
 // Set by a tiled kernel that gave up a bounded wait; gdr_device_status reads it.
 __device__ int g_recurrence_status;
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2f(float x) {
     float y;
@@ -55,59 +55,50 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
     __stcs(reinterpret_cast<unsigned int*>(p), *reinterpret_cast<const uint32_t*>(&r));
 }
 
-// The gates of two channels.  A = -exp(A_log), A2 = A log2(e): the log-decay is kept in
-// base 2, y = log2(e) g, as the special-function unit's exponential takes it.
+// The gates of two channels in base 2, as the special-function unit's exponential takes them:
+// A = -exp(A_log), bias = dt_bias log2(e).
 struct Channels {
-    float2 A, A2, bias;
+    float2 A, bias;
 };
 
-// softplus(z) = max(z, 0) + log1p(t) with t = e^{-|z|} in (0, 1], and log1p(t) = t Q(t),
-// Q the degree-8 polynomial whose largest relative error on [0, 1] is smallest (3e-8; a
-// weighted least-squares fit).  Small values of softplus are slow channels, whose state
-// sums over many tokens: there the relative error of g, not the absolute one, is what the
+// zl = log2(e) z for z = a + dt_bias; t = e^{-|z|} in (0, 1]; y = A log2(e) softplus(z), the
+// base-2 log-decay.  softplus(z) = max(z, 0) + log1p(t) and log2(e) log1p(t) = t Q(t), Q the
+// degree-8 polynomial whose largest relative error on [0, 1] is smallest (3e-8; a weighted
+// least-squares fit).  Small values of softplus are slow channels, whose state sums over
+// many tokens: there the relative error of the log-decay, not the absolute one, is what the
 // result sees, so log(1 + t) from the special-function unit (absolute error) will not do.
-__device__ __forceinline__ float2 log1p_poly2(float2 t) {
-    float2 q = bcast2(5.232629366e-03f);
-    q = __ffma2_rn(q, t, bcast2(-2.950498648e-02f));
-    q = __ffma2_rn(q, t, bcast2(7.822556049e-02f));
-    q = __ffma2_rn(q, t, bcast2(-1.366321445e-01f));
-    q = __ffma2_rn(q, t, bcast2(1.910599321e-01f));
-    q = __ffma2_rn(q, t, bcast2(-2.484297901e-01f));
-    q = __ffma2_rn(q, t, bcast2(3.331909776e-01f));
-    q = __ffma2_rn(q, t, bcast2(-4.999949336e-01f));
-    q = __ffma2_rn(q, t, bcast2(9.999999404e-01f));
-    return __fmul2_rn(q, t);
-}
-
 struct Gate {
-    float2 z, t, p;  // a + dt_bias, e^{-|z|}, softplus(z)
+    float2 zl, t, y;
 };
 __device__ __forceinline__ Gate decay_gate(float2 a, const Channels& ch) {
     Gate g;
-    g.z = __fadd2_rn(a, ch.bias);
-    g.t = ex2f2(make_float2(-fabsf(g.z.x) * kLog2e, -fabsf(g.z.y) * kLog2e));
-    g.p = __fadd2_rn(make_float2(fmaxf(g.z.x, 0.f), fmaxf(g.z.y, 0.f)), log1p_poly2(g.t));
+    g.zl = __ffma2_rn(a, bcast2(kLog2e), ch.bias);
+    g.t = ex2f2(make_float2(-fabsf(g.zl.x), -fabsf(g.zl.y)));
+    float2 q = bcast2(7.549088448e-03f);
+    q = __ffma2_rn(q, g.t, bcast2(-4.256669804e-02f));
+    q = __ffma2_rn(q, g.t, bcast2(1.128556207e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(-1.971185058e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(2.756412029e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(-3.584084213e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(4.806929529e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(-7.213401794e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(1.442695022e+00f));
+    q = __ffma2_rn(q, g.t, make_float2(fmaxf(g.zl.x, 0.f), fmaxf(g.zl.y, 0.f)));
+    g.y = __fmul2_rn(ch.A, q);
     return g;
 }
 
-__device__ __forceinline__ float2 sigmoid2(float2 b) {
+// x sigmoid(b)
+__device__ __forceinline__ float2 gated_input(float2 x, float2 b) {
     const float2 e = ex2f2(__fmul2_rn(b, bcast2(-kLog2e)));
-    return rcpf2(__fadd2_rn(e, bcast2(1.f)));
-}
-
-// sigmoid(v) and 1 - sigmoid(v), both to full relative accuracy, from t = e^{-|v|}
-__device__ __forceinline__ void sigmoid_both(float v, float t, float& s, float& c) {
-    const float r = rcpf(1.f + t), tr = t * r;
-    s = v >= 0.f ? r : tr;
-    c = v >= 0.f ? tr : r;
+    return __fmul2_rn(x, rcpf2(__fadd2_rn(e, bcast2(1.f))));
 }
 
 __device__ __forceinline__ Channels load_channels(const float* A_log, const float* dt_bias,
                                                   int c) {
     Channels ch;
     ch.A = make_float2(-expf(A_log[c]), -expf(A_log[c + 1]));
-    ch.A2 = __fmul2_rn(ch.A, bcast2(kLog2e));
-    ch.bias = make_float2(dt_bias[c], dt_bias[c + 1]);
+    ch.bias = __fmul2_rn(make_float2(dt_bias[c], dt_bias[c + 1]), bcast2(kLog2e));
     return ch;
 }
 
@@ -122,29 +113,30 @@ __device__ __forceinline__ void seq_bounds(const int32_t* cu, int s, int T, long
 }
 
 // One token's backward step on two channels: its decay (and its base-2 logarithm y), and the
-// factors of D, the gradient of its h, in dx, db, da and dA_log, from the inputs and the state
-// before the token.  Both forms of the backward pass use it, so they agree bit for bit
-// where they add in the same order.
+// factors of D, the gradient of its h, in dx, db, da and (times log2 e) dA_log, from the
+// inputs and the state before the token.  sigmoid(v) is r = 1 / (1 + t) for v >= 0 and t r
+// below, t = e^{-|v|}, so that small values keep their relative accuracy; sigmoid(v) (1 -
+// sigmoid(v)) is t r^2 for both signs.  Both forms of the backward pass use it, so they agree
+// bit for bit where they add in the same order.
 struct GradFactors {
     float2 lam, x, b, a, A;
 };
 __device__ __forceinline__ GradFactors grad_factors(float2 x, float2 a, float2 b, float2 prev,
                                                     const Channels& ch, float2& y) {
     const Gate g = decay_gate(a, ch);
-    float2 sz, si, ci;
-    float unused;
-    sigmoid_both(g.z.x, g.t.x, sz.x, unused);
-    sigmoid_both(g.z.y, g.t.y, sz.y, unused);
-    sigmoid_both(b.x, ex2f(-fabsf(b.x) * kLog2e), si.x, ci.x);
-    sigmoid_both(b.y, ex2f(-fabsf(b.y) * kLog2e), si.y, ci.y);
-    y = __fmul2_rn(ch.A2, g.p);
+    y = g.y;
     GradFactors f;
-    f.lam = ex2f2(y);
-    const float2 lpA = __fmul2_rn(__fmul2_rn(f.lam, prev), ch.A);
-    f.x = si;
-    f.b = __fmul2_rn(x, __fmul2_rn(si, ci));
-    f.a = __fmul2_rn(lpA, sz);
-    f.A = __fmul2_rn(lpA, g.p);
+    f.lam = ex2f2(g.y);
+    const float2 rz = rcpf2(__fadd2_rn(g.t, bcast2(1.f))), tz = __fmul2_rn(g.t, rz);
+    const float2 slope = make_float2(g.zl.x >= 0.f ? rz.x : tz.x, g.zl.y >= 0.f ? rz.y : tz.y);
+    const float2 bl = __fmul2_rn(b, bcast2(kLog2e));
+    const float2 tb = ex2f2(make_float2(-fabsf(bl.x), -fabsf(bl.y)));
+    const float2 rb = rcpf2(__fadd2_rn(tb, bcast2(1.f))), tr = __fmul2_rn(tb, rb);
+    f.x = make_float2(bl.x >= 0.f ? rb.x : tr.x, bl.y >= 0.f ? rb.y : tr.y);
+    f.b = __fmul2_rn(x, __fmul2_rn(rb, tr));
+    const float2 lp = __fmul2_rn(f.lam, prev);
+    f.a = __fmul2_rn(__fmul2_rn(lp, ch.A), slope);
+    f.A = __fmul2_rn(lp, g.y);
     return f;
 }
 template <typename Tin>
@@ -184,8 +176,7 @@ recurrence_seq_kernel(RecurrenceParams p) {
             const float2 xv = load_pair(x + t * p.ld), av = load_pair(a + t * p.ld),
                          bv = load_pair(b + t * p.ld);
             const Gate g = decay_gate(av, ch);
-            const float2 lam = ex2f2(__fmul2_rn(ch.A2, g.p));
-            h = __ffma2_rn(lam, h, __fmul2_rn(sigmoid2(bv), xv));
+            h = __ffma2_rn(ex2f2(g.y), h, gated_input(xv, bv));
             store_pair(p.out + t * p.C + c, h);
         }
         if (p.final_state) *reinterpret_cast<float2*>(p.final_state + at) = h;
@@ -228,13 +219,13 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
         if (r.grad_init) *reinterpret_cast<float2*>(r.grad_init + at) = D;
     }
     float* row = part + (size_t)blockIdx.y * 2 * p.C;
-    *reinterpret_cast<float2*>(row + c) = acc_A;
+    *reinterpret_cast<float2*>(row + c) = __fmul2_rn(acc_A, bcast2(kLn2));
     *reinterpret_cast<float2*>(row + p.C + c) = acc_bias;
 }
 
 // ------------------------------------------------------------------- tiled form
 // One pass over the data with the time axis split three ways.  A CTA owns a strip of 64
-// channels of one sequence and takes tiles of kWarps * TOK tokens; warp w holds tokens
+// channels of one sequence and takes tiles of WARPS * TOK tokens; warp w holds tokens
 // [w TOK, (w + 1) TOK) of the tile in registers, two channels per lane.  K CTAs of a cluster
 // take K consecutive tiles at a time.  The recurrence is affine, h_end = P h_start + H, so
 // each warp forms (P, H) of its tokens from zero, the CTA composes its warps' pairs through
@@ -247,25 +238,27 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
 // thousands of tokens, and factors rounded near 1 would lose in every tile what the small
 // W does not.  A factor below 2^-0.5 acts as P itself: there S + W S would cancel, and a
 // large forgotten state would leave its rounding error in a small new one.
-constexpr int kWarps = 8;
 constexpr int kStrip = 64;
 constexpr int kMaxCluster = 8;
-constexpr int kTileThreads = 32 * kWarps;
 
 // Shared memory of a CTA: per slot the x, a, b tiles, and for the backward pass dout's.
-template <typename Tin_, int TOK_, int STAGES_, bool Grad>
+template <typename Tin_, int WARPS_, int TOK_, int STAGES_, bool Grad>
 struct alignas(128) TileSmem {
     using Tin = Tin_;
-    static constexpr int TOK = TOK_, STAGES = STAGES_, kRows = kWarps * TOK;
+    static constexpr int WARPS = WARPS_, TOK = TOK_, STAGES = STAGES_, kRows = WARPS * TOK;
+    static_assert(WARPS >= kMaxCluster, "warp w sends to peer w");
     struct alignas(128) Slot {
         Tin in[3][kRows][kStrip];
         float dout[Grad ? kRows : 1][Grad ? kStrip : 4];
     };
     Slot slot[STAGES];
-    float4 part[2][kWarps][32];       // per warp and lane: P pair, H pair; by step parity
-    float2 log_part[2][kWarps][32];   // log2 of P
-    float4 peer[2][kMaxCluster][32];  // the cluster's tiles: coded factor pair, H pair
-    uint64_t full[STAGES], peers_in[2];
+    float4 part[2][WARPS][32];       // per warp and lane: P pair, H pair; by step parity
+    float2 log_part[2][WARPS][32];   // log2 of P
+    // The cluster's tiles: coded factor pair, H pair; by step modulo 4.  A CTA publishes step
+    // s + 4 only once it has every peer's step s + 2, which a peer publishes after all its
+    // warps are done with step s: nothing still unread is overwritten.
+    float4 peer[4][kMaxCluster][32];
+    uint64_t full[STAGES], peers_in[4];
 };
 
 // The factor 2^y, y <= 0, coded for carry(): for y > -0.5, W = expm1(y ln 2) with its sign
@@ -309,31 +302,6 @@ __device__ __forceinline__ void store_peer(float4* p, uint64_t* bar, uint32_t ra
                  ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
                  : "memory");
 }
-// Bounded wait for a phase that peers' stores complete (acquire at cluster scope).
-__device__ __forceinline__ bool peers_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __noinline__ bool peers_wait(uint64_t* bar, uint32_t parity) {
-    for (int i = 0; i < 64; ++i)
-        if (peers_test(bar, parity)) return true;
-    const uint64_t t0 = tc::globaltimer();
-    do {
-        for (int i = 0; i < 64; ++i) {
-            __nanosleep(tc::kPollSleepNs);
-            if (peers_test(bar, parity)) return true;
-        }
-    } while (tc::globaltimer() - t0 <= tc::kWaitLimitNs);
-    return false;
-}
-
 __device__ __forceinline__ float2 smem_pair(const float* p) {
     return *reinterpret_cast<const float2*>(p);
 }
@@ -366,41 +334,64 @@ __device__ __noinline__ void wait_in_flight(uint64_t* full, int stages, int issu
         tc::mbar_wait(&full[s % stages], (uint32_t)(s / stages) & 1u);
 }
 
-// From the warps' pairs in sm.part[buf] and the state S before the cluster's step: the state
-// before this warp's tokens; S moves past the step.
+// What a warp keeps of a step between its two runs over the step's tokens: the pair of the
+// tokens before its own in the tile, and (no cluster) the whole tile's, coded.
+struct Joined {
+    float2 P, H;
+    float4 all;
+};
+
+// Composes the warps' pairs in sm.part (after the barrier behind their stores) and, in a
+// cluster, starts the exchange of the CTAs' tiles.
 template <bool Cluster, typename Smem>
-__device__ __forceinline__ float2 join(Smem& sm, int step, int warp, int lane, float2& S,
-                                       bool& dead) {
+__device__ __forceinline__ Joined publish(Smem& sm, int step, int warp, int lane) {
     const int buf = step & 1;
     float2 G = make_float2(0.f, 0.f), H = G, Gp = G, Hp = G;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) Gp = G, Hp = H;
+    for (int w = 0; w < Smem::WARPS; ++w) {
+        if (w == warp) {  // uniform: a branch, not eight times four selects
+            Gp = G;
+            Hp = H;
+            asm volatile("");
+        }
         const float4 v = sm.part[buf][w][lane];
         H = __ffma2_rn(make_float2(v.x, v.y), H, make_float2(v.z, v.w));
         G = __fadd2_rn(G, sm.log_part[buf][w][lane]);
     }
-    const float4 all = make_float4(code_factor(G.x), code_factor(G.y), H.x, H.y);
+    Joined j;
+    j.P = ex2f2(Gp);
+    j.H = Hp;
+    j.all = make_float4(code_factor(G.x), code_factor(G.y), H.x, H.y);
+    if constexpr (Cluster) {
+        uint64_t* bar = &sm.peers_in[step & 3];
+        const uint32_t K = cluster_size();
+        if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(bar, K * (uint32_t)sizeof(sm.peer[0][0]));
+        if (warp < K) store_peer(&sm.peer[step & 3][cluster_rank()][lane], bar, warp, j.all);
+    }
+    return j;
+}
+
+// The state before this warp's tokens of the step; S moves from before the step to behind it.
+template <bool Cluster, typename Smem>
+__device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int step, int lane,
+                                              float2& S, bool& dead) {
     float2 in = S;
     if constexpr (Cluster) {
-        const uint32_t K = cluster_size(), rank = cluster_rank();
-        if (threadIdx.x == 0)
-            tc::mbar_arrive_expect_tx(&sm.peers_in[buf], K * (uint32_t)sizeof(sm.peer[0][0]));
-        if (warp < K) store_peer(&sm.peer[buf][rank][lane], &sm.peers_in[buf], warp, all);
-        if (!dead && !peers_wait(&sm.peers_in[buf], (uint32_t)(step >> 1) & 1u)) {
+        if (!dead && !tc::mbar_wait(&sm.peers_in[step & 3], (uint32_t)(step >> 2) & 1u)) {
             dead = true;
             if (lane == 0) atomicExch(&g_recurrence_status, 1);
         }
         __syncwarp();
+        const uint32_t K = cluster_size(), rank = cluster_rank();
         for (uint32_t k = 0; k < K; ++k) {
             if (k == rank) in = S;
-            const float4 v = sm.peer[buf][k][lane];
+            const float4 v = sm.peer[step & 3][k][lane];
             S = make_float2(carry(S.x, v.x, v.z), carry(S.y, v.y, v.w));
         }
     } else {
-        S = make_float2(carry(S.x, all.x, all.z), carry(S.y, all.y, all.w));
+        S = make_float2(carry(S.x, j.all.x, j.all.z), carry(S.y, j.all.y, j.all.w));
     }
-    return __ffma2_rn(ex2f2(Gp), in, Hp);
+    return __ffma2_rn(j.P, in, j.H);
 }
 
 // What the CTAs of both tiled kernels share: their place, their tokens, their barriers.
@@ -429,12 +420,12 @@ __device__ __forceinline__ Place place_of(const RecurrenceParams& p, int strips,
 template <typename Smem>
 __device__ __forceinline__ void init_barriers(Smem& sm) {
     for (int i = 0; i < Smem::STAGES; ++i) tc::mbar_init(&sm.full[i], 1);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.peers_in[i], 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&sm.peers_in[i], 1);
     tc::mbar_init_fence();
 }
 
 template <typename Smem, int Blocks, bool Cluster>
-__global__ void __launch_bounds__(kTileThreads, Blocks)
+__global__ void __launch_bounds__(32 * Smem::WARPS, Blocks)
 recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, int strips) {
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -455,27 +446,35 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
     // the barriers are set up; in a cluster, every CTA has started and has read its state
     if constexpr (Cluster) cluster_barrier(); else __syncthreads();
     bool dead = false;
-    for (int step = 0; step < w.steps; ++step) {
-        const int tile = step * w.K + w.rank, st = step % STAGES, buf = step & 1;
-        // tokens of this warp within the sequence
-        const long long first = w.t0 + (long long)tile * kRows + w.warp * TOK;
-        const int live = (int)min((long long)TOK, max(0LL, w.t1 - first));
-        if (tile < w.tiles && !dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
+    struct Held {
+        float2 lam[TOK], u[TOK];
+        Joined j;
+    };
+    // tokens of this warp in a step: the first one, and how many are within the sequence
+    auto first_of = [&](int step) {
+        return w.t0 + (long long)(step * w.K + w.rank) * kRows + w.warp * TOK;
+    };
+    auto live_of = [&](long long first) { return (int)min((long long)TOK, max(0LL, w.t1 - first)); };
+    // the run from zero, up to the exchange
+    auto read_tile = [&](int step, Held& k) {
+        const int st = step % STAGES, buf = step & 1, live = live_of(first_of(step));
+        if (step * w.K + w.rank < w.tiles && !dead &&
+            !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
             dead = true;
             if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
         }
         __syncwarp();
-        float2 lam[TOK], u[TOK], G = make_float2(0.f, 0.f), H = G;
+        float2 G = make_float2(0.f, 0.f), H = G;
         const auto* row = &sm.slot[st].in[0][w.warp * TOK][2 * w.lane];
         auto gates = [&](int i) {
             const float2 xv = smem_pair(row + i * kStrip);
             const float2 av = smem_pair(row + (kRows + i) * kStrip);
             const float2 bv = smem_pair(row + (2 * kRows + i) * kStrip);
-            const float2 y = __fmul2_rn(ch.A2, decay_gate(av, ch).p);
-            lam[i] = ex2f2(y);
-            u[i] = __fmul2_rn(sigmoid2(bv), xv);
+            const float2 y = decay_gate(av, ch).y;
+            k.lam[i] = ex2f2(y);
+            k.u[i] = gated_input(xv, bv);
             G = __fadd2_rn(G, y);
-            H = __ffma2_rn(lam[i], H, u[i]);
+            H = __ffma2_rn(k.lam[i], H, k.u[i]);
         };
         if (live == TOK) {
 #pragma unroll
@@ -486,8 +485,8 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
                 if (i < live) {
                     gates(i);
                 } else {
-                    lam[i] = make_float2(1.f, 1.f);
-                    u[i] = make_float2(0.f, 0.f);
+                    k.lam[i] = make_float2(1.f, 1.f);
+                    k.u[i] = make_float2(0.f, 0.f);
                 }
             }
         }
@@ -500,19 +499,25 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
                              (int)(w.t0 + (long long)(issued * w.K + w.rank) * kRows));
             ++issued;
         }
-        float2 h = join<Cluster>(sm, step, w.warp, w.lane, S, dead);
+        k.j = publish<Cluster>(sm, step, w.warp, w.lane);
+    };
+    // the run from the true start state
+    auto write_tile = [&](int step, const Held& k) {
+        float2 h = start_state<Cluster>(sm, k.j, step, w.lane, S, dead);
+        const long long first = first_of(step);
+        const int live = live_of(first);
         float* out = p.out + first * p.C + w.c;
         if (w.in_c) {
             if (live == TOK) {
 #pragma unroll
                 for (int i = 0; i < TOK; ++i) {
-                    h = __ffma2_rn(lam[i], h, u[i]);
+                    h = __ffma2_rn(k.lam[i], h, k.u[i]);
                     store_pair(out + (size_t)i * p.C, h);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < TOK; ++i) {
-                    h = __ffma2_rn(lam[i], h, u[i]);
+                    h = __ffma2_rn(k.lam[i], h, k.u[i]);
                     if (i < live) store_pair(out + (size_t)i * p.C, h);
                 }
             }
@@ -521,6 +526,25 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
                 *reinterpret_cast<float2*>(p.final_state + at) = h;
         }
         __syncwarp();
+    };
+    if constexpr (Cluster) {
+        // a step's exchange runs while the next step's tile is read
+        Held even, odd;
+        if (w.steps > 0) read_tile(0, even);
+        for (int step = 0; step < w.steps; step += 2) {
+            if (step + 1 < w.steps) read_tile(step + 1, odd);
+            write_tile(step, even);
+            if (step + 1 < w.steps) {
+                if (step + 2 < w.steps) read_tile(step + 2, even);
+                write_tile(step + 1, odd);
+            }
+        }
+    } else {
+        Held k;
+        for (int step = 0; step < w.steps; ++step) {
+            read_tile(step, k);
+            write_tile(step, k);
+        }
     }
     if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && p.final_state)
         *reinterpret_cast<float2*>(p.final_state + at) = S;
@@ -536,11 +560,14 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
 // after the join, is short.  h comes by plain loads, one step ahead.
 // part [units * K][2 C]: each CTA's sums for A_log and dt_bias.
 template <typename Smem, int Blocks, bool Cluster>
-__global__ void __launch_bounds__(kTileThreads, Blocks)
+__global__ void __launch_bounds__(32 * Smem::WARPS, Blocks)
 recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrenceParams p,
                                 RecurrenceGrads r, float* part, int strips) {
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
     using Tin = typename Smem::Tin;
+    // steps after which a tile's dout is no longer needed: the exchange takes one of two
+    constexpr int kHeld = Cluster ? 2 : 1;
+    static_assert(STAGES > kHeld, "a slot has to be free for the next tile");
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     const Place w = place_of<Cluster>(p, strips, kRows);
@@ -581,25 +608,33 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
     if constexpr (Cluster) cluster_barrier(); else __syncthreads();
     float2 acc_A = zero, acc_bias = zero;
     bool dead = false;
-    for (int step = 0; step < w.steps; ++step) {
-        const int tile = step * w.K + w.rank, st = step % STAGES, buf = step & 1;
-        const long long last = w.t1 - (long long)tile * kRows - w.warp * TOK - 1;
-        const int live = (int)min((long long)TOK, max(0LL, last + 1 - w.t0));
-        if (tile < w.tiles && !dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
+    struct Held {
+        GradFactors f[TOK];
+        Joined j;
+    };
+    auto last_of = [&](int step) {
+        return w.t1 - (long long)(step * w.K + w.rank) * kRows - w.warp * TOK - 1;
+    };
+    auto live_of = [&](long long last) {
+        return (int)min((long long)TOK, max(0LL, last + 1 - w.t0));
+    };
+    auto read_tile = [&](int step, Held& k) {
+        const int st = step % STAGES, buf = step & 1, live = live_of(last_of(step));
+        if (step * w.K + w.rank < w.tiles && !dead &&
+            !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
             dead = true;
             if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
         }
         __syncwarp();
-        GradFactors f[TOK];
         float2 G = zero, H = zero;
         const auto* row = &sm.slot[st].in[0][kRows - 1 - w.warp * TOK][2 * w.lane];
         const float* dout = &sm.slot[st].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
         auto gates = [&](int i) {
             float2 y;
-            f[i] = grad_factors(smem_pair(row - i * kStrip), smem_pair(row + (kRows - i) * kStrip),
-                                smem_pair(row + (2 * kRows - i) * kStrip), prev[i], ch, y);
+            k.f[i] = grad_factors(smem_pair(row - i * kStrip), smem_pair(row + (kRows - i) * kStrip),
+                                  smem_pair(row + (2 * kRows - i) * kStrip), prev[i], ch, y);
             G = __fadd2_rn(G, y);
-            H = __fmul2_rn(f[i].lam, __fadd2_rn(smem_pair(dout - i * kStrip), H));
+            H = __fmul2_rn(k.f[i].lam, __fadd2_rn(smem_pair(dout - i * kStrip), H));
         };
         if (live == TOK) {
 #pragma unroll
@@ -614,12 +649,19 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
         sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
         sm.log_part[buf][w.warp][w.lane] = G;
         __syncthreads();
-        // every warp is done with the step before: its slot takes the tile STAGES steps later
-        if (threadIdx.x == 0 && !dead && step > 0 && issued * w.K + w.rank < w.tiles) {
+        // every warp is done with step - kHeld: its slot takes the tile STAGES steps later
+        if (threadIdx.x == 0 && !dead && step >= kHeld && issued * w.K + w.rank < w.tiles) {
             load_tile<true>(sm, issued % STAGES, maps, w.c0, first_row(issued));
             ++issued;
         }
-        float2 E = join<Cluster>(sm, step, w.warp, w.lane, S, dead);
+        k.j = publish<Cluster>(sm, step, w.warp, w.lane);
+    };
+    auto write_tile = [&](int step, const Held& k) {
+        float2 E = start_state<Cluster>(sm, k.j, step, w.lane, S, dead);
+        const long long last = last_of(step);
+        const int live = live_of(last);
+        const float* dout =
+            &sm.slot[step % STAGES].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
         if (w.in_c) {
             Tin* dx = static_cast<Tin*>(r.grad_x) + last * r.ld_grad + w.c;
             Tin* da = static_cast<Tin*>(r.grad_a) + last * r.ld_grad + w.c;
@@ -627,8 +669,8 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
             auto token = [&](int i) {
                 const float2 D = __fadd2_rn(smem_pair(dout - i * kStrip), E);
                 const long long o = i * r.ld_grad;
-                store_grads(f[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
-                E = __fmul2_rn(f[i].lam, D);
+                store_grads(k.f[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
+                E = __fmul2_rn(k.f[i].lam, D);
             };
             if (live == TOK) {
 #pragma unroll
@@ -644,6 +686,25 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
                 *reinterpret_cast<float2*>(r.grad_init + at) = E;
         }
         __syncwarp();
+    };
+    if constexpr (Cluster) {
+        // a step's exchange runs while the next step's tile is read
+        Held even, odd;
+        if (w.steps > 0) read_tile(0, even);
+        for (int step = 0; step < w.steps; step += 2) {
+            if (step + 1 < w.steps) read_tile(step + 1, odd);
+            write_tile(step, even);
+            if (step + 1 < w.steps) {
+                if (step + 2 < w.steps) read_tile(step + 2, even);
+                write_tile(step + 1, odd);
+            }
+        }
+    } else {
+        Held k;
+        for (int step = 0; step < w.steps; ++step) {
+            read_tile(step, k);
+            write_tile(step, k);
+        }
     }
     if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && r.grad_init)
         *reinterpret_cast<float2*>(r.grad_init + at) = S;
@@ -653,12 +714,12 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
     if (w.warp == 0 && w.in_c) {
         float4 s = sm.part[0][0][w.lane];
 #pragma unroll
-        for (int k = 1; k < kWarps; ++k) {
+        for (int k = 1; k < Smem::WARPS; ++k) {
             const float4 v = sm.part[0][k][w.lane];
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
         float* o = part + ((size_t)w.seq * w.K + w.rank) * 2 * p.C + w.c;
-        *reinterpret_cast<float2*>(o) = make_float2(s.x, s.y);
+        *reinterpret_cast<float2*>(o) = __fmul2_rn(make_float2(s.x, s.y), bcast2(kLn2));
         *reinterpret_cast<float2*>(o + p.C) = make_float2(s.z, s.w);
     }
     if (dead && threadIdx.x == 0) wait_in_flight(sm.full, STAGES, issued);
@@ -681,31 +742,54 @@ int mean_length(const RecurrenceParams& p) {
     return p.cu_seqlens ? (p.T + p.nseq - 1) / p.nseq : p.T;
 }
 
+// (sequence, strip of channels) pairs, each one chain of tiles.
+long long units_of(const RecurrenceParams& p) {
+    return (long long)p.nseq * ((p.C + kStrip - 1) / kStrip);
+}
+
 // Sequences of up to a warp's tokens leave the tiled form's other warps idle.
 bool use_tiles(const RecurrenceParams& p) { return mean_length(p) > 16; }
 
-// CTAs per cluster for `units` (sequence, strip) pairs of `tiles` tiles: the K that keeps the
-// largest share of the SMs' slots (`blocks` CTAs each) at work until the last wave is done.
-int cluster_of(long long units, int tiles, int blocks) {
-    const int sms = sm_count(), most = std::min(tiles, kMaxCluster);
-    int best = 1;
-    double best_share = 0.0;
-    for (int K = 1; K <= most; ++K) {
-        const long long n = units * K, per = std::min<long long>(blocks, (n + sms - 1) / sms);
-        const double share = (double)n / (double)((n + per * sms - 1) / (per * sms) * per * sms);
-        if (share > best_share + 0.02) best = K, best_share = share;
+// CTAs per cluster for `units` (sequence, strip) pairs of `tiles` tiles.  A cluster's CTAs
+// take one SM each, so K of them for every unit pay only while the units leave SMs idle: the
+// largest K whose clusters the device still holds at once, at one CTA per SM.  (96 units of
+// 8192 tokens: 141 us forward with K = 1, 168 with K = 2, 178 with K = 3.)
+template <typename Kernel>
+cudaError_t cluster_of(Kernel kernel, int threads, size_t smem, long long units, int tiles, int* K) {
+    *K = 1;
+    const int most = (int)std::min<long long>({(long long)kMaxCluster, (long long)tiles,
+                                               sm_count() / units});
+    if (most < 2) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    for (int k = most; e == cudaSuccess && k > 1; --k) {
+        cudaLaunchAttribute attr = {};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)k;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(units * k));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+        if (e == cudaSuccess && fit >= units) {
+            *K = k;
+            break;
+        }
     }
-    return best;
+    return e;
 }
 
 template <typename Kernel, typename... Args>
-cudaError_t launch_tiles(Kernel kernel, long long grid, int K, size_t smem, cudaStream_t stream,
-                         Args... args) {
+cudaError_t launch_tiles(Kernel kernel, long long grid, int threads, int K, size_t smem,
+                         cudaStream_t stream, Args... args) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kTileThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
@@ -726,63 +810,86 @@ bool make_maps(Maps& m, const RecurrenceParams& p, const float* dout, int box) {
            (!dout || make_map_pitched(&m.dout, dout, true, p.C, rows, p.C, kStrip, box));
 }
 
-// Tokens per warp, slots, CTAs per SM.
-#ifndef FTOK
-#define FTOK 8
-#define FST 2
-#define FBL 3
-#define BTOK 8
-#define BST 2
-#define BBL 2
-#define GTOK 4
-#define GST 2
-#define GBL 2
-#endif
-template <typename Tin>
-struct Form {
-    static constexpr bool kBf16 = sizeof(Tin) == 2;
-    using Fwd = TileSmem<Tin, FTOK, FST, false>;
-    static constexpr int kFwdBlocks = kBf16 ? FBL : 2;
-    using Bwd = TileSmem<Tin, kBf16 ? BTOK : GTOK, kBf16 ? BST : GST, true>;
-    static constexpr int kBwdBlocks = kBf16 ? BBL : GBL;
+// Warps, tokens per warp, slots, CTAs per SM of each kernel.  Registers set the tokens (two
+// values per token and channel forward, five backward, twice that in a cluster, where a
+// warp holds two steps), shared memory the slots.
+template <typename Tin, bool Cluster> struct Forms;
+template <> struct Forms<__nv_bfloat16, false> {
+    using Fwd = TileSmem<__nv_bfloat16, 8, 12, 2, false>;
+    using Bwd = TileSmem<__nv_bfloat16, 8, 8, 3, true>;
+    static constexpr int kFwdBlocks = 2;
+};
+template <> struct Forms<__nv_bfloat16, true> {
+    using Fwd = TileSmem<__nv_bfloat16, 8, 16, 2, false>;
+    using Bwd = TileSmem<__nv_bfloat16, 8, 8, 3, true>;
+    static constexpr int kFwdBlocks = 1;
+};
+template <> struct Forms<float, false> {
+    using Fwd = TileSmem<float, 8, 8, 2, false>;
+    using Bwd = TileSmem<float, 8, 8, 3, true>;
+    static constexpr int kFwdBlocks = 2;
+};
+template <> struct Forms<float, true> {
+    using Fwd = TileSmem<float, 8, 8, 3, false>;
+    using Bwd = TileSmem<float, 8, 8, 3, true>;
+    static constexpr int kFwdBlocks = 1;
 };
 
-template <typename Tin>
-cudaError_t forward_tiles(const RecurrenceParams& p, cudaStream_t stream) {
-    using Smem = typename Form<Tin>::Fwd;
-    constexpr int kBlocks = Form<Tin>::kFwdBlocks;
+template <typename Tin, bool Cluster>
+cudaError_t forward_tiles(const RecurrenceParams& p, int K, cudaStream_t stream) {
+    using F = Forms<Tin, Cluster>;
+    using Smem = typename F::Fwd;
     const int strips = (p.C + kStrip - 1) / kStrip;
-    const long long units = (long long)p.nseq * strips;
-    const int K = cluster_of(units, (mean_length(p) + Smem::kRows - 1) / Smem::kRows, kBlocks);
+    const long long grid = (long long)p.nseq * strips * K;
     Maps m;
-    if (units * K > 0x7fffffffLL || !make_maps(m, p, nullptr, Smem::kRows))
-        return cudaErrorNotSupported;
-    auto kernel = K > 1 ? recurrence_tile_kernel<Smem, kBlocks, true>
-                        : recurrence_tile_kernel<Smem, kBlocks, false>;
-    return launch_tiles(kernel, units * K, K, sizeof(Smem), stream, m, p, strips);
+    if (grid > 0x7fffffffLL || !make_maps(m, p, nullptr, Smem::kRows)) return cudaErrorNotSupported;
+    return launch_tiles(recurrence_tile_kernel<Smem, F::kFwdBlocks, Cluster>, grid,
+                        32 * Smem::WARPS, K, sizeof(Smem), stream, m, p, strips);
 }
 
-template <typename Tin>
-cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, cudaStream_t stream) {
-    using Smem = typename Form<Tin>::Bwd;
-    constexpr int kBlocks = Form<Tin>::kBwdBlocks;
+template <typename Tin, bool Cluster>
+cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, int K,
+                           cudaStream_t stream) {
+    using Smem = typename Forms<Tin, Cluster>::Bwd;
     const int strips = (p.C + kStrip - 1) / kStrip;
-    const long long units = (long long)p.nseq * strips;
-    const int K = cluster_of(units, (mean_length(p) + Smem::kRows - 1) / Smem::kRows, kBlocks);
+    const long long grid = (long long)p.nseq * strips * K, rows = (long long)p.nseq * K;
     Maps m;
-    if (units * K > 0x7fffffffLL || !make_maps(m, p, r.grad_out, Smem::kRows))
+    if (grid > 0x7fffffffLL || !make_maps(m, p, r.grad_out, Smem::kRows))
         return cudaErrorNotSupported;
-    const long long rows = (long long)p.nseq * K;
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);
     if (e != cudaSuccess) return e;
-    auto kernel = K > 1 ? recurrence_tile_backward_kernel<Smem, kBlocks, true>
-                        : recurrence_tile_backward_kernel<Smem, kBlocks, false>;
-    e = launch_tiles(kernel, units * K, K, sizeof(Smem), stream, m, p, r, part, strips);
+    e = launch_tiles(recurrence_tile_backward_kernel<Smem, 1, Cluster>, grid,
+                     32 * Smem::WARPS, K, sizeof(Smem), stream, m, p, r, part, strips);
     if (e == cudaSuccess)
         e = launch_column_sum(part, rows, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
     const cudaError_t f = cudaFreeAsync(part, stream);
     return e != cudaSuccess ? e : f;
+}
+
+template <typename Tin>
+cudaError_t forward_tiles(const RecurrenceParams& p, cudaStream_t stream) {
+    using F = Forms<Tin, true>;
+    using Smem = typename F::Fwd;
+    int K = 1;
+    const cudaError_t e =
+        cluster_of(recurrence_tile_kernel<Smem, F::kFwdBlocks, true>, 32 * Smem::WARPS, sizeof(Smem),
+                   units_of(p), (mean_length(p) + Smem::kRows - 1) / Smem::kRows, &K);
+    if (e != cudaSuccess) return e;
+    return K > 1 ? forward_tiles<Tin, true>(p, K, stream) : forward_tiles<Tin, false>(p, 1, stream);
+}
+
+template <typename Tin>
+cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r,
+                           cudaStream_t stream) {
+    using Smem = typename Forms<Tin, true>::Bwd;
+    int K = 1;
+    const cudaError_t e =
+        cluster_of(recurrence_tile_backward_kernel<Smem, 1, true>, 32 * Smem::WARPS, sizeof(Smem),
+                   units_of(p), (mean_length(p) + Smem::kRows - 1) / Smem::kRows, &K);
+    if (e != cudaSuccess) return e;
+    return K > 1 ? backward_tiles<Tin, true>(p, r, K, stream)
+                 : backward_tiles<Tin, false>(p, r, 1, stream);
 }
 
 }  // namespace
