@@ -6,6 +6,7 @@
 // over y), so a call's result does not depend on which CTA finished first, as it would with
 // atomic adds.  With P = 0 the sums are zero.
 #include "gdr_internal.h"
+#include "tcgen05.cuh"
 
 namespace gdr {
 
@@ -17,11 +18,13 @@ __global__ void __launch_bounds__(kSumX * kSumY)
 column_sum_kernel(const float* __restrict__ part, long long P, int N, float* __restrict__ out0,
                   int n0, float* __restrict__ out1) {
     __shared__ float sm[kSumY][kSumX + 1];
+    // launched while the kernel before it in the stream, which wrote part, may still run
+    tc::grid_dep_wait();
     const int x = threadIdx.x % kSumX, y = threadIdx.x / kSumX;
     const int n = blockIdx.x * kSumX + x;
     float s = 0.f;
     if (n < N) {
-#pragma unroll 4
+#pragma unroll 8
         for (long long p = y; p < P; p += kSumY) s += part[p * N + n];
     }
     sm[y][x] = s;
@@ -42,9 +45,16 @@ column_sum_kernel(const float* __restrict__ part, long long P, int N, float* __r
 cudaError_t launch_column_sum(const float* part, long long P, int N, float* out0, int n0,
                               float* out1, cudaStream_t stream) {
     if (N <= 0) return cudaSuccess;
-    column_sum_kernel<<<(unsigned)((N + kSumX - 1) / kSumX), kSumX * kSumY, 0, stream>>>(
-        part, P, N, out0, n0, out1);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((N + kSumX - 1) / kSumX));
+    cfg.blockDim = dim3(kSumX * kSumY);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, column_sum_kernel, part, P, N, out0, n0, out1);
 }
 
 }  // namespace gdr

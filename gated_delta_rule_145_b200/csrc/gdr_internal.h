@@ -122,6 +122,8 @@ struct LayerNormGrads {
 };
 cudaError_t launch_layer_norm(const LayerNormParams& p, cudaStream_t stream);
 cudaError_t launch_layer_norm_backward(const LayerNormGrads& p, cudaStream_t stream);
+// Reads and clears its timeout record (nonzero if set, -1 on error).
+int read_and_clear_layer_norm_status();
 
 // Backward passes of the steps around the rule; mixer_grad.cu.
 struct ConvGrads {
@@ -176,7 +178,8 @@ cudaError_t workspace_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 size_t noalloc_scratch_bytes();
 cudaError_t noalloc_scratch(void** ptr);
 
-// Reads and clears the tensor-core kernels', the tiled convolution's and recurrence's and the self-test's
+// Reads and clears the tensor-core kernels', the tiled convolution's and recurrence's, the
+// layer norm's and the self-test's
 // timeout records (nonzero if set, 0 if not, -1 on a CUDA error); workspace.cu.
 int read_and_clear_tc_status();
 

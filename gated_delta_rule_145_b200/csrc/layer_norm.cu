@@ -3,254 +3,635 @@
 //     y  = xh * weight + bias,  xh = (x - mean) * rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
 //     dx = rstd * (dyw - mean(dyw) - xh * mean(dyw * xh)),  dyw = dy * weight
 //     dweight = sum_rows dy * xh,  dbias = sum_rows dy.
-// Both are bound by memory (forward: x in, y out; backward: x, dy in, dx out).  A row lives in
-// the registers of the threads that loaded it, eight adjacent values each, so it is read
-// once; the variance is taken from the centred values (two passes over registers), which
-// keeps its accuracy where the mean is far from zero.
+// Both are bound by memory (forward: x in, y out; backward: x, dy in, dx out), and a row is
+// read once.  The variance is taken from the centred values (a second pass over registers),
+// which keeps its accuracy where the mean is far from zero.
 #include <algorithm>
 
 #include "gdr_common.cuh"
 #include "gdr_internal.h"
+#include "tcgen05.cuh"
 
 namespace gdr {
 
 namespace {
 
-constexpr int kVec = 8;           // adjacent values per thread
-constexpr int kSubThreads = 256;  // block of the narrow form
-constexpr int kSubMaxD = 256;     // widest row of the narrow form: one warp's lanes
+// Set by a backward kernel that gave up a bounded wait; gdr_device_status reads it.
+__device__ int g_layer_norm_status;
 
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[kVec]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[kVec]) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+constexpr int kVec = 8;  // adjacent values per thread and vector
+
+// Eight values as loaded: four registers of bf16 pairs, or eight of fp32.
+template <typename Tin>
+struct Raw;
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
+    __device__ __forceinline__ void lds(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
+        v[0] = make_float2(a.x, a.y);
+        v[1] = make_float2(a.z, a.w);
+        v[2] = make_float2(b.x, b.y);
+        v[3] = make_float2(b.z, b.w);
+    }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        u = __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void lds(const __nv_bfloat16* p) {
+        u = *reinterpret_cast<const uint4*>(p);
+    }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    }
+};
+__device__ __forceinline__ void store_vec(float* p, const float2 (&v)[4]) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
 }
-__device__ __forceinline__ void store_vec(float* p, const float (&v)[kVec]) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
-}
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[kVec]) {
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float2 (&v)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 r = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(v[i].x, v[i].y);
         w[i] = *reinterpret_cast<const uint32_t*>(&r);
     }
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
-__device__ __forceinline__ void load_param(const float* p, float (&v)[kVec]) {
+__device__ __forceinline__ void load_param(const float* p, float2 (&v)[4]) {
     const float4 a = *reinterpret_cast<const float4*>(p);
     const float4 b = *(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ float2 bcast2(float v) { return make_float2(v, v); }
+
+// Sum over `lanes` adjacent lanes (a power of two).
+template <int lanes>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+    for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// Sum over the threads that share a row.  Sub: `tpr` adjacent lanes (a power of two).
-// Otherwise the whole block, through `sm` (one float2 per warp; the caller alternates
-// between two buffers, so one barrier per sum is enough).
-template <bool Sub>
-__device__ __forceinline__ float2 row_sum(float2 v, int tpr, float2* sm) {
-    if constexpr (Sub) {
-        for (int o = tpr / 2; o > 0; o /= 2) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+// ------------------------------------------------------------------------------- forward
+// A row belongs to L adjacent lanes, NV vectors each, L vectors apart, and stays in their
+// registers as loaded (bf16 in pairs): no barrier, and a whole row of loads in flight per
+// warp; U rows at a time where rows are short.  (One block per row, eight values per thread and
+// two barriers, ran [8192, 6144] bf16 at 0.25 of HBM.)  Statistics, then y, re-expand the
+// registers.
+template <typename Tin, int NV>
+constexpr int kRawRegs = NV * (sizeof(Tin) == 2 ? 4 : 8);
+template <typename Tin, int NV>
+constexpr int kRowsAtOnce = kRawRegs<Tin, NV> <= 8 ? 4 : kRawRegs<Tin, NV> <= 16 ? 2 : 1;
+
+// blocks of 128 threads per SM whose registers hold the raw values and ~60 more
+template <int raw>
+constexpr int kForwardBlocks = 512 / (raw + 60);
+
+template <typename Tin, int NV, int L>
+__global__ void __launch_bounds__(128, kForwardBlocks<kRawRegs<Tin, NV> * kRowsAtOnce<Tin, NV>>)
+layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* __restrict__ bias,
+                  Tin* y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
+                  long long rows, int d, float eps) {
+    constexpr int U = kRowsAtOnce<Tin, NV>;
+    const int lane = threadIdx.x % L, per = blockDim.x / L;
+    // weight, then bias (zeros without one); Staged: then a row of x per warp
+    extern __shared__ __align__(128) float params[];
+    for (int i = 4 * threadIdx.x; i < d; i += 4 * blockDim.x) {
+        *reinterpret_cast<float4*>(params + i) = *reinterpret_cast<const float4*>(weight + i);
+        *reinterpret_cast<float4*>(params + d + i) =
+            bias ? *reinterpret_cast<const float4*>(bias + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    for (long long base = (long long)blockIdx.x * per * U; base < rows;
+         base += (long long)gridDim.x * per * U) {
+        const long long row0 = base + threadIdx.x / L;  // then per rows apart
+        Raw<Tin> raw[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = row0 + u * per;
+            const Tin* xp = x + row * d + kVec * lane;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                if (row < rows && kVec * (lane + n * L) < d)
+                    raw[u][n].load(xp + n * L * kVec);
+                else
+                    raw[u][n].zero();
+            }
         }
-        return v;
-    } else {
-        v.x = warp_sum(v.x);
-        v.y = warp_sum(v.y);
-        const int lane = threadIdx.x % 32, nw = blockDim.x / 32;
-        if (lane == 0) sm[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = lane < nw ? sm[lane] : make_float2(0.f, 0.f);
-        return make_float2(warp_sum(v.x), warp_sum(v.y));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = row0 + u * per;
+            float2 s2 = bcast2(0.f), q2 = s2;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                float2 v[4];
+                raw[u][n].get(v);
+                s2 = __fadd2_rn(s2, __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3])));
+            }
+            const float mean = lane_sum<L>(s2.x + s2.y) / (float)d;
+            const float2 neg = bcast2(-mean);
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                float2 v[4];
+                raw[u][n].get(v);
+                if (kVec * (lane + n * L) < d) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = __fadd2_rn(v[e], neg);
+                        q2 = __ffma2_rn(v[e], v[e], q2);
+                    }
+                }
+            }
+            const float rstd = 1.0f / sqrtf(lane_sum<L>(q2.x + q2.y) / (float)d + eps);
+            if (row < rows && lane == 0) {
+                if (mean_out) mean_out[row] = mean;
+                if (rstd_out) rstd_out[row] = rstd;
+            }
+            Tin* yp = y + row * d + kVec * lane;
+            const float2 r2 = bcast2(rstd);
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int c = kVec * (lane + n * L);
+                if (row < rows && c < d) {
+                    float2 v[4], w[4], b[4];
+                    raw[u][n].get(v);
+                    load_param(params + c, w);
+                    load_param(params + d + c, b);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[e], neg), r2), w[e], b[e]);
+                    store_vec(yp + n * L * kVec, v);
+                }
+            }
+        }
     }
 }
 
-// A block takes `rpb` rows at a time (Sub: one per group of `tpr` lanes; otherwise one),
-// grid-stride.  NV vectors per thread, `tpr` vectors apart.
-template <typename Tin, int NV, bool Sub>
-__global__ void __launch_bounds__(Sub ? kSubThreads : 1024)
-layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* __restrict__ bias,
-                  Tin* y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
-                  long long rows, int d, int tpr, float eps) {
-    __shared__ float2 sm[2][32];
-    const int rpb = Sub ? kSubThreads / tpr : 1;
-    const int sub = Sub ? threadIdx.x / tpr : 0, lane = Sub ? threadIdx.x % tpr : threadIdx.x;
-    for (long long base = (long long)blockIdx.x * rpb; base < rows;
-         base += (long long)gridDim.x * rpb) {
-        const long long row = base + sub;
-        const bool live = row < rows;
-        float v[NV][kVec];
-        float s = 0.f;
+// Few rows: a block per row, NV vectors per thread.
+__device__ __forceinline__ float block_sum(float v, float* sm) {
+    v = warp_sum(v);
+    const int lane = threadIdx.x % 32, nw = blockDim.x / 32;
+    if (lane == 0) sm[threadIdx.x / 32] = v;
+    __syncthreads();
+    return warp_sum(lane < nw ? sm[lane] : 0.f);
+}
+
+template <typename Tin, int NV>
+__global__ void __launch_bounds__(1024)
+layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
+                        const float* __restrict__ bias, Tin* y, float* __restrict__ mean_out,
+                        float* __restrict__ rstd_out, long long rows, int d, float eps) {
+    __shared__ float sm[2][32];  // each sum has its own: one barrier per sum
+    const int tpr = blockDim.x;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+        Raw<Tin> raw[NV];
+        float2 s2 = bcast2(0.f), q2 = s2;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int c = kVec * (lane + n * tpr);
-            if (live && c < d) {
-                load_vec(x + row * d + c, v[n]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) v[n][e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) s += v[n][e];
+            const int c = kVec * ((int)threadIdx.x + n * tpr);
+            if (c < d) raw[n].load(x + row * d + c); else raw[n].zero();
         }
-        const float mean = row_sum<Sub>(make_float2(s, 0.f), tpr, sm[0]).x / (float)d;
-        float ss = 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const bool in = kVec * (lane + n * tpr) < d;
+            float2 v[4];
+            raw[n].get(v);
+            s2 = __fadd2_rn(s2, __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3])));
+        }
+        const float mean = block_sum(s2.x + s2.y, sm[0]) / (float)d;
+        const float2 neg = bcast2(-mean);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                v[n][e] -= mean;
-                if (in) ss += v[n][e] * v[n][e];
+        for (int n = 0; n < NV; ++n) {
+            float2 v[4];
+            raw[n].get(v);
+            if (kVec * ((int)threadIdx.x + n * tpr) < d) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = __fadd2_rn(v[e], neg);
+                    q2 = __ffma2_rn(v[e], v[e], q2);
+                }
             }
         }
-        const float var = row_sum<Sub>(make_float2(ss, 0.f), tpr, sm[1]).x / (float)d;
-        const float rstd = 1.0f / sqrtf(var + eps);
-        if (live && lane == 0) {
+        const float rstd = 1.0f / sqrtf(block_sum(q2.x + q2.y, sm[1]) / (float)d + eps);
+        if (threadIdx.x == 0) {
             if (mean_out) mean_out[row] = mean;
             if (rstd_out) rstd_out[row] = rstd;
         }
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int c = kVec * (lane + n * tpr);
-            if (!live || c >= d) continue;
-            float w[kVec], bs[kVec], o[kVec];
-            load_param(weight + c, w);
-            if (bias) load_param(bias + c, bs);
+            const int c = kVec * ((int)threadIdx.x + n * tpr);
+            if (c < d) {
+                float2 v[4], w[4], b[4];
+                raw[n].get(v);
+                load_param(weight + c, w);
+                if (bias) {
+                    load_param(bias + c, b);
+                } else {
+                    b[0] = b[1] = b[2] = b[3] = bcast2(0.f);
+                }
 #pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                o[e] = v[n][e] * rstd * w[e] + (bias ? bs[e] : 0.f);
-            store_vec(y + row * d + c, o);
+                for (int e = 0; e < 4; ++e)
+                    v[e] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[e], neg), bcast2(rstd)), w[e], b[e]);
+                store_vec(y + row * d + c, v);
+            }
         }
     }
 }
 
-// As above; the columns' sums stay in registers over all rows of a block and leave as one
-// row of part [gridDim.x][2 d] (dweight, then dbias).
-template <typename Tin, int NV, bool Sub>
-__global__ void __launch_bounds__(Sub ? kSubThreads : 1024)
+// Wide rows, forward and backward: thread -> kVec columns (NV times) of all its block's rows, so
+// that the parameters, and backward the columns' sums, stay in registers.  The block takes
+// groups of up to kRingRows rows from a ring in shared memory (bulk copies: rows are
+// contiguous), so the bytes in flight depend neither on registers nor on barriers.  A group
+// passes through its phases in consecutive iterations (sum, centred sum, output; backward:
+// both sums, output), so one barrier per iteration serves them all, and a phase's sums are
+// there when the next one starts.  (A warp per row re-read the parameters for every row: at
+// [8192, 6144] bf16 their four times larger L1 traffic held it at 0.46 of HBM.)
+constexpr int kRingRows = 4;
+
+// Adds v[0 .. 7] over the warp: lane l ends with the sum of v[l % 8].  Each exchange halves
+// the values a lane still carries: 9 shuffles instead of 40.
+__device__ __forceinline__ float sum8(float (&v)[8], int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float keep = lane & 4 ? v[k + 4] : v[k], send = lane & 4 ? v[k] : v[k + 4];
+        v[k] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float keep = lane & 2 ? v[k + 2] : v[k], send = lane & 2 ? v[k] : v[k + 2];
+        v[k] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
+    }
+    const float keep = lane & 1 ? v[1] : v[0], send = lane & 1 ? v[0] : v[1];
+    float s = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    return s;
+}
+// The block's eight sums, over its warps' rows of sm: lane l gets value l % 8.
+__device__ __forceinline__ float total8(const float (*sm)[8], int nw, int lane) {
+    float t = 0.f;
+    for (int i = lane / 8; i < nw; i += 4) t += sm[i][lane % 8];
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    return t;
+}
+
+// A block's groups of rows and their ring; T tensors per slot.  Slots are counted along
+// instead of taken modulo their number: a 64-bit remainder costs as much as a row's work.
+template <typename Tin, int T>
+struct Ring {
+    Tin* base;
+    uint64_t* full;
+    int stages, group_rows, d, mine, slot_elems;
+    long long rows;
+    int issued = 0, issue_slot = 0;
+    __device__ __forceinline__ Ring(uint8_t* smem, uint64_t* bars, int stages_, int group_rows_,
+                                    long long rows_, int d_)
+        : base(reinterpret_cast<Tin*>(smem)), full(bars), stages(stages_), group_rows(group_rows_),
+          d(d_), slot_elems(T * d_ * group_rows_), rows(rows_) {
+        const long long groups = (rows + group_rows - 1) / group_rows;
+        mine = (int)((groups - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    }
+    __device__ __forceinline__ long long row0(int k) const {
+        return (blockIdx.x + (long long)k * gridDim.x) * group_rows;
+    }
+    __device__ __forceinline__ int count(int k) const {  // 0 outside [0, mine)
+        return k < 0 || k >= mine ? 0 : (int)min((long long)group_rows, rows - row0(k));
+    }
+    __device__ __forceinline__ int next(int slot) const { return slot + 1 == stages ? 0 : slot + 1; }
+    // one thread: the next group's copies, if there is one
+    __device__ __forceinline__ void issue(const Tin* a, const Tin* b) {
+        if (issued >= mine) return;
+        const uint32_t bytes = (uint32_t)count(issued) * (uint32_t)(d * sizeof(Tin));
+        uint64_t* bar = &full[issue_slot];
+        Tin* to = base + (size_t)issue_slot * slot_elems;
+        const long long from = row0(issued) * d;
+        tc::mbar_arrive_expect_tx(bar, T * bytes);
+        tc::bulk_load(to, a + from, bytes, bar);
+        if (T > 1) tc::bulk_load(to + d * group_rows, b + from, bytes, bar);
+        ++issued;
+        issue_slot = next(issue_slot);
+    }
+    // after a wait that gave up, copies may still be in flight: the block stays for them
+    __device__ __forceinline__ void drain() const {
+        for (int k = max(0, issued - stages); k < issued; ++k)
+            tc::mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1u);
+    }
+};
+
+// ------------------------------------------------------------------------------ backward
+// part [gridDim.x][2 d]: each block's sums over its rows, dweight, then dbias.
+template <typename Tin, int NV>
+__global__ void __launch_bounds__(512)
 layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ weight,
                            const float* __restrict__ mean, const float* __restrict__ rstd,
-                           const Tin* dy, Tin* dx, float* __restrict__ part, long long rows,
-                           int d, int tpr) {
-    __shared__ float2 sm[2][32];
-    __shared__ float acc_sm[Sub ? kSubThreads * kVec : 1];
-    const int rpb = Sub ? kSubThreads / tpr : 1;
-    const int sub = Sub ? threadIdx.x / tpr : 0, lane = Sub ? threadIdx.x % tpr : threadIdx.x;
-    float w[NV][kVec], dw[NV][kVec], db[NV][kVec];
+                           const Tin* dy, Tin* dx, float* __restrict__ part, long long rows, int d,
+                           int stages, int group_rows) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ float sums[2][16][8];
+    __shared__ uint64_t full[8];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, nw = blockDim.x / 32;
+    Ring<Tin, 2> ring(smem_raw, full, stages, group_rows, rows, d);
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) tc::mbar_init(&full[i], 1);
+        tc::mbar_init_fence();
+        for (int i = 0; i < stages; ++i) ring.issue(x, dy);
+    }
+    float2 w[NV][4], dw[NV][4], db[NV][4];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int c = kVec * (lane + n * tpr);
+        const int c = kVec * (tid + n * (int)blockDim.x);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) w[n][e] = dw[n][e] = db[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) w[n][e] = dw[n][e] = db[n][e] = bcast2(0.f);
         if (c < d) load_param(weight + c, w[n]);
     }
-    int buf = 0;
+    __syncthreads();
+    // statistics of group k + 1, loaded while group k is worked on: lane r those of row r
+    float mu_next = 0.f, rs_next = 0.f;
+    auto load_stats = [&](int k) {
+        if (lane < ring.count(k)) {
+            mu_next = -mean[ring.row0(k) + lane];
+            rs_next = rstd[ring.row0(k) + lane];
+        }
+    };
+    load_stats(0);
+    bool dead = false;
+    int slot = 0;
+    uint32_t parity = 0;
     const float inv = 1.0f / (float)d;
-    for (long long base = (long long)blockIdx.x * rpb; base < rows;
-         base += (long long)gridDim.x * rpb, buf ^= 1) {
-        const long long row = base + sub;
-        const bool live = row < rows;
-        const float mu = live ? mean[row] : 0.f, rs = live ? rstd[row] : 0.f;
-        float xh[NV][kVec], g[NV][kVec];
-        float2 m = make_float2(0.f, 0.f);
+    for (int k = 0; k < ring.mine; ++k) {
+        const int n_rows = ring.count(k);
+        float m[8], mu[kRingRows], rs[kRingRows];
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c = kVec * (lane + n * tpr);
-            if (live && c < d) {
-                load_vec(x + row * d + c, xh[n]);
-                load_vec(dy + row * d + c, g[n]);
-            } else {
+        for (int r = 0; r < kRingRows; ++r) {
+            mu[r] = __shfl_sync(0xffffffffu, mu_next, r);
+            rs[r] = __shfl_sync(0xffffffffu, rs_next, r);
+            m[2 * r] = m[2 * r + 1] = 0.f;
+        }
+        load_stats(k + 1);
+        if (!dead && !tc::mbar_wait(&full[slot], parity)) {
+            dead = true;
+            if (lane == 0) atomicExch(&g_layer_norm_status, 1);
+        }
+        __syncwarp();
+        const Tin *xs = ring.base + (size_t)slot * ring.slot_elems, *gs = xs + d * group_rows;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) xh[n][e] = mu, g[n][e] = 0.f;
-            }
+        for (int r = 0; r < kRingRows; ++r) {
+            if (r < n_rows) {
+                const float2 r2 = bcast2(rs[r]), shift = bcast2(mu[r]);
+                float2 m1 = bcast2(0.f), m2 = m1;
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                xh[n][e] = (xh[n][e] - mu) * rs;
-                dw[n][e] += g[n][e] * xh[n][e];
-                db[n][e] += g[n][e];
-                g[n][e] *= w[n][e];
-                m.x += g[n][e];
-                m.y += g[n][e] * xh[n][e];
+                for (int n = 0; n < NV; ++n) {
+                    const int c = kVec * (tid + n * (int)blockDim.x);
+                    if (c < d) {
+                        Raw<Tin> a, b;
+                        a.lds(xs + r * d + c);
+                        b.lds(gs + r * d + c);
+                        float2 xv[4], g[4];
+                        a.get(xv);
+                        b.get(g);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 xh = __fmul2_rn(__fadd2_rn(xv[e], shift), r2);
+                            dw[n][e] = __ffma2_rn(g[e], xh, dw[n][e]);
+                            db[n][e] = __fadd2_rn(db[n][e], g[e]);
+                            const float2 q = __fmul2_rn(g[e], w[n][e]);
+                            m1 = __fadd2_rn(m1, q);
+                            m2 = __ffma2_rn(q, xh, m2);
+                        }
+                    }
+                }
+                m[2 * r] = m1.x + m1.y;
+                m[2 * r + 1] = m2.x + m2.y;
             }
         }
-        m = row_sum<Sub>(m, tpr, sm[buf]);
-        m.x *= inv;
-        m.y *= inv;
+        const float s = sum8(m, lane);
+        if (lane < 8) sums[k & 1][warp][lane] = s;
+        __syncthreads();
+        const float t = total8(sums[k & 1], nw, lane) * -inv;
+        Tin* dxp = dx + ring.row0(k) * d;
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c = kVec * (lane + n * tpr);
-            if (!live || c >= d) continue;
-            float o[kVec];
+        for (int r = 0; r < kRingRows; ++r) {
+            const float n1 = __shfl_sync(0xffffffffu, t, 2 * r);
+            const float n2 = __shfl_sync(0xffffffffu, t, 2 * r + 1);
+            if (r < n_rows) {
+                const float2 r2 = bcast2(rs[r]), shift = bcast2(mu[r]);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) o[e] = rs * (g[n][e] - m.x - xh[n][e] * m.y);
-            store_vec(dx + row * d + c, o);
+                for (int n = 0; n < NV; ++n) {
+                    const int c = kVec * (tid + n * (int)blockDim.x);
+                    if (c < d) {
+                        Raw<Tin> a, b;
+                        a.lds(xs + r * d + c);
+                        b.lds(gs + r * d + c);
+                        float2 xv[4], g[4];
+                        a.get(xv);
+                        b.get(g);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 xh = __fmul2_rn(__fadd2_rn(xv[e], shift), r2);
+                            const float2 q = __ffma2_rn(g[e], w[n][e], bcast2(n1));
+                            g[e] = __fmul2_rn(__ffma2_rn(xh, bcast2(n2), q), r2);
+                        }
+                        store_vec(dxp + (long long)r * d + c, g);
+                    }
+                }
+            }
         }
+        __syncthreads();
+        // every warp is done with the group: its slot takes the next one
+        if (tid == 0 && !dead) ring.issue(x, dy);
+        slot = ring.next(slot);
+        if (slot == 0) parity ^= 1;
     }
     float* out = part + (size_t)blockIdx.x * 2 * d;
-    if constexpr (Sub) {
-        // the groups of lanes that took other rows hold the same columns
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            __syncthreads();
+    for (int n = 0; n < NV; ++n) {
+        const int c = kVec * (tid + n * (int)blockDim.x);
+        if (c < d) {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) acc_sm[e * kSubThreads + threadIdx.x] = k ? db[0][e] : dw[0][e];
-            __syncthreads();
-            for (int c = threadIdx.x; c < d; c += kSubThreads) {
-                float s = 0.f;
-                for (int q = 0; q < rpb; ++q) s += acc_sm[(c % kVec) * kSubThreads + q * tpr + c / kVec];
-                out[k * d + c] = s;
+            for (int e = 0; e < 4; ++e) {
+                *reinterpret_cast<float2*>(out + c + 2 * e) = dw[n][e];
+                *reinterpret_cast<float2*>(out + d + c + 2 * e) = db[n][e];
             }
         }
-    } else {
+    }
+    if (dead && tid == 0) ring.drain();
+}
+
+// Narrow rows (d <= 256): L adjacent lanes per row, one vector each, U rows of loads in flight.
+constexpr int kNarrowThreads = 256, kNarrowRows = 4;
+
+template <typename Tin, int L>
+__global__ void __launch_bounds__(kNarrowThreads)
+layer_norm_backward_narrow_kernel(const Tin* __restrict__ x, const float* __restrict__ weight,
+                                  const float* __restrict__ mean, const float* __restrict__ rstd,
+                                  const Tin* dy, Tin* dx, float* __restrict__ part, long long rows,
+                                  int d) {
+    constexpr int per = kNarrowThreads / L, U = kNarrowRows;
+    __shared__ float acc[kVec][kNarrowThreads];
+    const int lane = threadIdx.x % L, c = kVec * lane;
+    const bool in = c < d;
+    float2 w[4], dw[4], db[4];
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c = kVec * (lane + n * tpr);
-            if (c >= d) continue;
+    for (int e = 0; e < 4; ++e) w[e] = dw[e] = db[e] = bcast2(0.f);
+    if (in) load_param(weight + c, w);
+    const float inv = 1.0f / (float)d;
+    for (long long base = (long long)blockIdx.x * per * U; base < rows;
+         base += (long long)gridDim.x * per * U) {
+        Raw<Tin> a[U], b[U];
+        float mu[U], rs[U];
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                out[c + e] = dw[n][e];
-                out[d + c + e] = db[n][e];
+        for (int u = 0; u < U; ++u) {
+            const long long row = base + u * per + threadIdx.x / L;
+            const bool live = row < rows;
+            mu[u] = live ? mean[row] : 0.f;
+            rs[u] = live ? rstd[row] : 0.f;
+            a[u].zero();
+            b[u].zero();
+            if (live && in) {
+                a[u].load(x + row * d + c);
+                b[u].load(dy + row * d + c);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = base + u * per + threadIdx.x / L;
+            const float2 r2 = bcast2(rs[u]), shift = bcast2(-mu[u]);
+            float2 xh[4], g[4], m1 = bcast2(0.f), m2 = m1;
+            a[u].get(xh);
+            b[u].get(g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                xh[e] = __fmul2_rn(__fadd2_rn(xh[e], shift), r2);
+                dw[e] = __ffma2_rn(g[e], xh[e], dw[e]);
+                db[e] = __fadd2_rn(db[e], g[e]);
+                g[e] = __fmul2_rn(g[e], w[e]);
+                m1 = __fadd2_rn(m1, g[e]);
+                m2 = __ffma2_rn(g[e], xh[e], m2);
+            }
+            const float2 n1 = bcast2(lane_sum<L>(m1.x + m1.y) * -inv);
+            const float2 n2 = bcast2(lane_sum<L>(m2.x + m2.y) * -inv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                g[e] = __fmul2_rn(__ffma2_rn(xh[e], n2, __fadd2_rn(g[e], n1)), r2);
+            if (row < rows && in) store_vec(dx + row * d + c, g);
+        }
+    }
+    // the groups of lanes that took other rows hold the same columns
+    float* out = part + (size_t)blockIdx.x * 2 * d;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[2 * e][threadIdx.x] = k ? db[e].x : dw[e].x;
+            acc[2 * e + 1][threadIdx.x] = k ? db[e].y : dw[e].y;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < d; i += kNarrowThreads) {
+            float s = 0.f;
+            for (int q = 0; q < per; ++q) s += acc[i % kVec][q * L + i / kVec];
+            out[k * d + i] = s;
         }
     }
 }
 
-// How rows of d values are laid out over threads.
-struct Shape {
-    int threads, tpr, nv, rpb;
-    bool sub;
-};
-Shape shape_of(int d) {
-    Shape s;
-    const int vecs = (d + kVec - 1) / kVec;
-    s.sub = d <= kSubMaxD;
-    if (s.sub) {
-        s.tpr = 1;
-        while (s.tpr < vecs) s.tpr *= 2;
-        s.threads = kSubThreads;
-        s.nv = 1;
-        s.rpb = kSubThreads / s.tpr;
-    } else {
-        s.nv = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
-        s.threads = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
-        s.tpr = s.threads;
-        s.rpb = 1;
+// Rows too wide for the ring (two slots, or 32 columns for each of 512 threads): the columns' sums by threads that keep eight columns
+// over a slice of the rows, then dx by a block per row that reads it twice.
+constexpr int kRingMaxD = 16384;
+
+template <typename Tin>
+__global__ void __launch_bounds__(128)
+layer_norm_columns_kernel(const Tin* __restrict__ x, const float* __restrict__ mean,
+                          const float* __restrict__ rstd, const Tin* __restrict__ dy,
+                          float* __restrict__ part, long long rows, int d) {
+    const int c = kVec * (blockIdx.x * 128 + threadIdx.x);
+    if (c >= d) return;
+    float2 dw[4], db[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dw[e] = db[e] = bcast2(0.f);
+    for (long long row = blockIdx.y; row < rows; row += gridDim.y) {
+        Raw<Tin> a, b;
+        a.load(x + row * d + c);
+        b.load(dy + row * d + c);
+        float2 xv[4], g[4];
+        a.get(xv);
+        b.get(g);
+        const float2 r2 = bcast2(rstd[row]), shift = bcast2(-mean[row]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dw[e] = __ffma2_rn(g[e], __fmul2_rn(__fadd2_rn(xv[e], shift), r2), dw[e]);
+            db[e] = __fadd2_rn(db[e], g[e]);
+        }
     }
-    return s;
+    float* out = part + (size_t)blockIdx.y * 2 * d + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<float2*>(out + 2 * e) = dw[e];
+        *reinterpret_cast<float2*>(out + d + 2 * e) = db[e];
+    }
+}
+
+template <typename Tin>
+__global__ void __launch_bounds__(1024)
+layer_norm_backward_wide_kernel(const Tin* __restrict__ x, const float* __restrict__ weight,
+                                const float* __restrict__ mean, const float* __restrict__ rstd,
+                                const Tin* dy, Tin* dx, long long rows, int d) {
+    __shared__ float sm[2][32];
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+        const float2 r2 = bcast2(rstd[row]), shift = bcast2(-mean[row]);
+        float2 m1 = bcast2(0.f), m2 = m1;
+        for (int c = kVec * threadIdx.x; c < d; c += kVec * blockDim.x) {
+            Raw<Tin> a, b;
+            a.load(x + row * d + c);
+            b.load(dy + row * d + c);
+            float2 xv[4], g[4], w[4];
+            a.get(xv);
+            b.get(g);
+            load_param(weight + c, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 q = __fmul2_rn(g[e], w[e]);
+                m1 = __fadd2_rn(m1, q);
+                m2 = __ffma2_rn(q, __fmul2_rn(__fadd2_rn(xv[e], shift), r2), m2);
+            }
+        }
+        const float2 n1 = bcast2(block_sum(m1.x + m1.y, sm[0]) / -(float)d);
+        const float2 n2 = bcast2(block_sum(m2.x + m2.y, sm[1]) / -(float)d);
+        for (int c = kVec * threadIdx.x; c < d; c += kVec * blockDim.x) {
+            Raw<Tin> a, b;
+            a.load(x + row * d + c);
+            b.load(dy + row * d + c);
+            float2 xv[4], g[4], w[4];
+            a.get(xv);
+            b.get(g);
+            load_param(weight + c, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 xh = __fmul2_rn(__fadd2_rn(xv[e], shift), r2);
+                g[e] = __fmul2_rn(__ffma2_rn(xh, n2, __ffma2_rn(g[e], w[e], n1)), r2);
+            }
+            store_vec(dx + row * d + c, g);
+        }
+    }
 }
 
 int sm_count() {
@@ -261,45 +642,160 @@ int sm_count() {
     return n;
 }
 
-// Blocks of a grid-stride pass: 1024 threads' worth per SM, at most one row group each.
-unsigned grid_of(const Shape& s, long long rows) {
-    const long long need = (rows + s.rpb - 1) / s.rpb;
-    const long long fit = (long long)sm_count() * std::max(1, 1024 / s.threads);
-    return (unsigned)std::min(need, fit);
-}
+// Shared memory for rings, per SM; beside it each block needs its sums and barriers.
+constexpr size_t kRoom = 216 * 1024;
+
+// Rows per group and slots of a ring whose rows take `row` bytes per slot, for `blocks` blocks per
+// SM: the most rows per group that leave `want` slots (a group's phases and one to fill).
+struct RingShape {
+    int group_rows, stages;
+    RingShape(size_t row, int blocks, int want) {
+        const size_t room = kRoom / blocks;
+        group_rows = kRingRows;
+        while (group_rows > 1 && want * group_rows * row > room) group_rows /= 2;
+        stages = (int)std::min<size_t>(want, room / (group_rows * row));
+    }
+};
+
+// 16-byte loads of a row that one lane keeps: 128 registers.
+constexpr int kMaxWarpVecs = 32;
 
 template <typename Tin>
 cudaError_t forward(const LayerNormParams& p, cudaStream_t stream) {
-    const Shape s = shape_of(p.d);
-    const unsigned grid = grid_of(s, p.rows);
     const Tin* x = static_cast<const Tin*>(p.x);
     Tin* y = static_cast<Tin*>(p.y);
-    auto go = [&](auto kernel) {
-        kernel<<<grid, s.threads, 0, stream>>>(x, p.weight, p.bias, y, p.mean, p.rstd, p.rows,
-                                               p.d, s.tpr, p.eps);
+    const int vecs = (p.d + kVec - 1) / kVec, sms = sm_count();
+    // a warp takes ~16 us for a row of 6144, a block 4: up to four rows per SM go to blocks
+    if (kVec * vecs * sizeof(Tin) > 32 * 16 * kMaxWarpVecs || (vecs > 128 && p.rows <= 4LL * sms)) {
+        const int nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;  // at most 512 threads, to d = 16384
+        const int threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+        const unsigned grid = (unsigned)std::min<long long>(p.rows, sms * 2LL);
+        auto kernel = nv == 1   ? layer_norm_block_kernel<Tin, 1>
+                      : nv == 2 ? layer_norm_block_kernel<Tin, 2>
+                                : layer_norm_block_kernel<Tin, 4>;
+        kernel<<<grid, threads, 0, stream>>>(x, p.weight, p.bias, y, p.mean, p.rstd, p.rows, p.d,
+                                             p.eps);
+        return cudaGetLastError();
+    }
+    auto go = [&](auto kernel, int L, int U) {
+        // few rows: one warp per block, to use more SMs
+        const int threads = p.rows * L <= 128LL * sms * U ? 32 : 128;
+        const long long per = (long long)threads / L * U, need = (p.rows + per - 1) / per;
+        const size_t smem = 2 * sizeof(float) * p.d;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        int blocks = 1;  // of the grid-stride pass, per SM
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem);
+        if (e != cudaSuccess) return e;
+        const unsigned grid = (unsigned)std::min<long long>(need, (long long)sms * std::max(1, blocks));
+        kernel<<<grid, threads, smem, stream>>>(x, p.weight, p.bias, y, p.mean, p.rstd, p.rows, p.d,
+                                                p.eps);
+        return cudaGetLastError();
     };
-    if (s.sub) go(layer_norm_kernel<Tin, 1, true>);
-    else if (s.nv == 1) go(layer_norm_kernel<Tin, 1, false>);
-    else if (s.nv == 2) go(layer_norm_kernel<Tin, 2, false>);
-    else go(layer_norm_kernel<Tin, 4, false>);
-    return cudaGetLastError();
+    if (vecs <= 1) return go(layer_norm_kernel<Tin, 1, 1>, 1, kRowsAtOnce<Tin, 1>);
+    if (vecs <= 4) return go(layer_norm_kernel<Tin, 1, 4>, 4, kRowsAtOnce<Tin, 1>);
+    if (vecs <= 8) return go(layer_norm_kernel<Tin, 1, 8>, 8, kRowsAtOnce<Tin, 1>);
+    if (vecs <= 16) return go(layer_norm_kernel<Tin, 1, 16>, 16, kRowsAtOnce<Tin, 1>);
+    if (vecs <= 32) return go(layer_norm_kernel<Tin, 1, 32>, 32, kRowsAtOnce<Tin, 1>);
+    if (vecs <= 64) return go(layer_norm_kernel<Tin, 2, 32>, 32, kRowsAtOnce<Tin, 2>);
+    if (vecs <= 128) return go(layer_norm_kernel<Tin, 4, 32>, 32, kRowsAtOnce<Tin, 4>);
+    if (vecs <= 256) return go(layer_norm_kernel<Tin, 8, 32>, 32, kRowsAtOnce<Tin, 8>);
+    if (vecs <= 384) return go(layer_norm_kernel<Tin, 12, 32>, 32, kRowsAtOnce<Tin, 12>);
+    if (sizeof(Tin) == 4 || vecs <= 512) return go(layer_norm_kernel<Tin, 16, 32>, 32, kRowsAtOnce<Tin, 16>);
+    if constexpr (sizeof(Tin) == 2) {
+        if (vecs <= 768) return go(layer_norm_kernel<Tin, 24, 32>, 32, kRowsAtOnce<Tin, 24>);
+        return go(layer_norm_kernel<Tin, 32, 32>, 32, kRowsAtOnce<Tin, 32>);
+    }
+    return cudaErrorNotSupported;
 }
 
+// Launches of the backward pass: how many blocks (= rows of partial sums) and on what.
 template <typename Tin>
-cudaError_t backward(const LayerNormGrads& p, const Shape& s, unsigned grid, float* part,
+struct BackwardPlan {
+    bool narrow, wide;
+    int L, nv, threads, group_rows, stages;
+    size_t smem;
+    unsigned grid;
+    explicit BackwardPlan(const LayerNormGrads& p) {
+        const int vecs = (p.d + kVec - 1) / kVec;
+        narrow = vecs <= 32;
+        if (narrow) {
+            L = vecs <= 1 ? 1 : vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
+            const long long per = (long long)kNarrowThreads / L * kNarrowRows;
+            grid = (unsigned)std::min<long long>((p.rows + per - 1) / per, (long long)sm_count() * 4);
+            return;
+        }
+        wide = p.d > kRingMaxD || RingShape(2 * sizeof(Tin) * p.d, 1, 2).stages < 2;
+        if (wide) {  // slices of rows, for two blocks per SM
+            const long long across = (vecs + 127) / 128;
+            grid = (unsigned)std::min<long long>(p.rows, std::max<long long>(1, 2 * sm_count() / across));
+            return;
+        }
+        // at most 512 threads of 8 to 32 columns; two slots of the most rows that fit
+        nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+        threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+        const size_t row = 2 * sizeof(Tin) * p.d;  // x and dy
+        const RingShape ring(row, 1, 2);
+        group_rows = ring.group_rows;
+        stages = ring.stages;
+        smem = (size_t)stages * group_rows * row;
+        const long long groups = (p.rows + group_rows - 1) / group_rows;
+        const long long blocks = std::max<long long>(
+            1, std::min<long long>((long long)(kRoom / (smem + 2048)), 1024 / threads));
+        grid = (unsigned)std::min<long long>(groups, blocks * sm_count());
+    }
+};
+
+template <typename Tin>
+cudaError_t backward(const LayerNormGrads& p, const BackwardPlan<Tin>& plan, float* part,
                      cudaStream_t stream) {
     const Tin* x = static_cast<const Tin*>(p.x);
     const Tin* dy = static_cast<const Tin*>(p.grad_y);
     Tin* dx = static_cast<Tin*>(p.grad_x);
-    auto go = [&](auto kernel) {
-        kernel<<<grid, s.threads, 0, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx, part, p.rows,
-                                               p.d, s.tpr);
-    };
-    if (s.sub) go(layer_norm_backward_kernel<Tin, 1, true>);
-    else if (s.nv == 1) go(layer_norm_backward_kernel<Tin, 1, false>);
-    else if (s.nv == 2) go(layer_norm_backward_kernel<Tin, 2, false>);
-    else go(layer_norm_backward_kernel<Tin, 4, false>);
+    if (plan.narrow) {
+        auto go = [&](auto kernel) {
+            kernel<<<plan.grid, kNarrowThreads, 0, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx,
+                                                             part, p.rows, p.d);
+        };
+        switch (plan.L) {
+            case 1: go(layer_norm_backward_narrow_kernel<Tin, 1>); break;
+            case 4: go(layer_norm_backward_narrow_kernel<Tin, 4>); break;
+            case 8: go(layer_norm_backward_narrow_kernel<Tin, 8>); break;
+            case 16: go(layer_norm_backward_narrow_kernel<Tin, 16>); break;
+            default: go(layer_norm_backward_narrow_kernel<Tin, 32>); break;
+        }
+        return cudaGetLastError();
+    }
+    if (plan.wide) {
+        const dim3 grid((unsigned)((p.d + 128 * kVec - 1) / (128 * kVec)), plan.grid);
+        layer_norm_columns_kernel<Tin><<<grid, 128, 0, stream>>>(x, p.mean, p.rstd, dy, part, p.rows, p.d);
+        layer_norm_backward_wide_kernel<Tin><<<(unsigned)std::min<long long>(p.rows, 2LL * sm_count()),
+                                               1024, 0, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx,
+                                                                  p.rows, p.d);
+        return cudaGetLastError();
+    }
+    auto kernel = plan.nv == 1   ? layer_norm_backward_kernel<Tin, 1>
+                  : plan.nv == 2 ? layer_norm_backward_kernel<Tin, 2>
+                                 : layer_norm_backward_kernel<Tin, 4>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)plan.smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<plan.grid, plan.threads, plan.smem, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx, part,
+                                                           p.rows, p.d, plan.stages, plan.group_rows);
     return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t backward(const LayerNormGrads& p, cudaStream_t stream) {
+    const BackwardPlan<Tin> plan(p);
+    float* part = nullptr;
+    cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * plan.grid * 2 * p.d, stream);
+    if (e != cudaSuccess) return e;
+    e = backward<Tin>(p, plan, part, stream);
+    if (e == cudaSuccess)
+        e = launch_column_sum(part, plan.grid, 2 * p.d, p.grad_weight, p.d, p.grad_bias, stream);
+    const cudaError_t f = cudaFreeAsync(part, stream);
+    return e != cudaSuccess ? e : f;
 }
 
 }  // namespace
@@ -312,17 +808,17 @@ cudaError_t launch_layer_norm(const LayerNormParams& p, cudaStream_t stream) {
 cudaError_t launch_layer_norm_backward(const LayerNormGrads& p, cudaStream_t stream) {
     if (p.rows == 0)  // the sums over no rows
         return launch_column_sum(nullptr, 0, 2 * p.d, p.grad_weight, p.d, p.grad_bias, stream);
-    const Shape s = shape_of(p.d);
-    const unsigned grid = grid_of(s, p.rows);
-    float* part = nullptr;
-    cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * grid * 2 * p.d, stream);
-    if (e != cudaSuccess) return e;
-    e = p.in == InType::BF16 ? backward<__nv_bfloat16>(p, s, grid, part, stream)
-                             : backward<float>(p, s, grid, part, stream);
-    if (e == cudaSuccess)
-        e = launch_column_sum(part, grid, 2 * p.d, p.grad_weight, p.d, p.grad_bias, stream);
-    const cudaError_t f = cudaFreeAsync(part, stream);
-    return e != cudaSuccess ? e : f;
+    return p.in == InType::BF16 ? backward<__nv_bfloat16>(p, stream) : backward<float>(p, stream);
+}
+
+int read_and_clear_layer_norm_status() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_layer_norm_status, sizeof(int)) != cudaSuccess) return -1;
+    if (v != 0) {
+        const int zero = 0;
+        cudaMemcpyToSymbol(g_layer_norm_status, &zero, sizeof(int));
+    }
+    return v;
 }
 
 }  // namespace gdr

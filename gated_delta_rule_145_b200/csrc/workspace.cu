@@ -80,8 +80,9 @@ int read_and_clear_tc_status() {
     const int vst = read_and_clear_selftest_status();
     const int vcv = read_and_clear_conv_status();
     const int vrc = read_and_clear_recurrence_status();
-    if (v64 < 0 || vst < 0 || vcv < 0 || vrc < 0) return -1;
-    return v64 != 0 ? v64 : vst != 0 ? vst : vcv != 0 ? vcv : vrc;
+    const int vln = read_and_clear_layer_norm_status();
+    if (v64 < 0 || vst < 0 || vcv < 0 || vrc < 0 || vln < 0) return -1;
+    return v64 != 0 ? v64 : vst != 0 ? vst : vcv != 0 ? vcv : vrc != 0 ? vrc : vln;
 }
 
 }  // namespace gdr
