@@ -2,9 +2,11 @@
 // partial rows that a backward kernel left in the workspace.
 //
 // part [P][N] fp32 -> out0 [n0] (columns 0 .. n0 - 1) and out1 [N - n0] (the others).
-// The rows are added in a fixed order (thread row y takes rows y, y + 32, ...; then a tree
+// The rows are added in a fixed order (thread row y takes rows y, y + Y, ...; then a tree
 // over y), so a call's result does not depend on which CTA finished first, as it would with
-// atomic adds.  With P = 0 the sums are zero.
+// atomic adds.  With P = 0 the sums are zero.  A thread takes four columns; few blocks of
+// many rows (a norm's 128 columns) need all their loads in flight at once, many blocks of
+// few rows (a convolution's taps) need small blocks: Y = 128 above 128 rows, else 16.
 #include "gdr_internal.h"
 #include "tcgen05.cuh"
 
@@ -12,31 +14,43 @@ namespace gdr {
 
 namespace {
 
-constexpr int kSumX = 32, kSumY = 32;
+constexpr int kSumX = 8;  // threads across: 32 columns
 
-__global__ void __launch_bounds__(kSumX * kSumY)
+template <int Y>
+__global__ void __launch_bounds__(kSumX * Y)
 column_sum_kernel(const float* __restrict__ part, long long P, int N, float* __restrict__ out0,
                   int n0, float* __restrict__ out1) {
-    __shared__ float sm[kSumY][kSumX + 1];
+    __shared__ float4 sm[Y][kSumX];
+    const int x = threadIdx.x % kSumX, y = threadIdx.x / kSumX;
+    const int n = 4 * (blockIdx.x * kSumX + x);
     // launched while the kernel before it in the stream, which wrote part, may still run
     tc::grid_dep_wait();
-    const int x = threadIdx.x % kSumX, y = threadIdx.x / kSumX;
-    const int n = blockIdx.x * kSumX + x;
-    float s = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n < N) {
 #pragma unroll 8
-        for (long long p = y; p < P; p += kSumY) s += part[p * N + n];
+        for (long long p = y; p < P; p += Y) {
+            const float4 v = *reinterpret_cast<const float4*>(part + p * N + n);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
     }
     sm[y][x] = s;
     __syncthreads();
 #pragma unroll
-    for (int h = kSumY / 2; h > 0; h /= 2) {
-        if (y < h) sm[y][x] += sm[y + h][x];
+    for (int h = Y / 2; h > 0; h /= 2) {
+        if (y < h) {
+            const float4 v = sm[y + h][x];
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            sm[y][x] = s;
+        }
         __syncthreads();
     }
     if (y == 0 && n < N) {
-        float* out = n < n0 ? out0 : out1;
-        if (out) out[n < n0 ? n : n - n0] = sm[0][x];
+        const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float* out = n + e < n0 ? out0 : out1;
+            if (out) out[n + e < n0 ? n + e : n + e - n0] = v[e];
+        }
     }
 }
 
@@ -49,12 +63,13 @@ cudaError_t launch_column_sum(const float* part, long long P, int N, float* out0
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((N + kSumX - 1) / kSumX));
-    cfg.blockDim = dim3(kSumX * kSumY);
+    cfg.gridDim = dim3((unsigned)((N + 4 * kSumX - 1) / (4 * kSumX)));
+    cfg.blockDim = dim3(kSumX * (P > 128 ? 128 : 16));
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, column_sum_kernel, part, P, N, out0, n0, out1);
+    return cudaLaunchKernelEx(&cfg, P > 128 ? column_sum_kernel<128> : column_sum_kernel<16>, part,
+                              P, N, out0, n0, out1);
 }
 
 }  // namespace gdr

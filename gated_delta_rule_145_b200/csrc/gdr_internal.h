@@ -153,7 +153,8 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
 cudaError_t launch_gated_rmsnorm_backward(const NormGrads& p, cudaStream_t stream);
 
 // out0 [n0] and out1 [N - n0] = the column sums of part [P, N], rows added in a fixed order
-// (either output may be nullptr; P = 0 gives zeros); column_sum.cu.
+// (either output may be nullptr; P = 0 gives zeros); N a multiple of 4, part 16-byte aligned;
+// column_sum.cu.
 cudaError_t launch_column_sum(const float* part, long long P, int N, float* out0, int n0,
                               float* out1, cudaStream_t stream);
 

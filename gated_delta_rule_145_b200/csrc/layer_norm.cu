@@ -36,6 +36,7 @@ struct Raw<float> {
         b = *(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void pin() {}
     __device__ __forceinline__ void get(float2 (&v)[4]) const {
         v[0] = make_float2(a.x, a.y);
         v[1] = make_float2(a.z, a.w);
@@ -53,6 +54,11 @@ struct Raw<__nv_bfloat16> {
         u = *reinterpret_cast<const uint4*>(p);
     }
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    // What follows expands the packed values anew; the compiler would otherwise keep the
+    // expanded ones from one pass over them to the next, in twice the registers.
+    __device__ __forceinline__ void pin() {
+        asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
+    }
     __device__ __forceinline__ void get(float2 (&v)[4]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -83,6 +89,19 @@ __device__ __forceinline__ void load_param(const float* p, float2 (&v)[4]) {
 }
 __device__ __forceinline__ float2 bcast2(float v) { return make_float2(v, v); }
 
+// s / d from inv = 1 / d rounded: the product and one correction by its remainder (a row of one
+// value keeps that value as its mean), a third of a division's instructions.
+__device__ __forceinline__ float mean_of(float s, float d, float inv) {
+    const float q = s * inv;
+    return fabsf(q) < INFINITY ? fmaf(fmaf(-q, d, s), inv, q) : q;
+}
+// 1 / sqrt(v): the special-function unit's estimate and one Newton step (not where they meet 0
+// or infinity).
+__device__ __forceinline__ float inv_sqrt(float v) {
+    const float r = rsqrtf(v);
+    return v > 0.f && v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
+}
+
 // Sum over `lanes` adjacent lanes (a power of two).
 template <int lanes>
 __device__ __forceinline__ float lane_sum(float v) {
@@ -102,9 +121,9 @@ constexpr int kRawRegs = NV * (sizeof(Tin) == 2 ? 4 : 8);
 template <typename Tin, int NV>
 constexpr int kRowsAtOnce = kRawRegs<Tin, NV> <= 8 ? 4 : kRawRegs<Tin, NV> <= 16 ? 2 : 1;
 
-// blocks of 128 threads per SM whose registers hold the raw values and ~60 more
+// blocks of 128 threads per SM whose registers hold the raw values and ~32 more
 template <int raw>
-constexpr int kForwardBlocks = 512 / (raw + 60);
+constexpr int kForwardBlocks = 512 / (raw + 32);
 
 template <typename Tin, int NV, int L>
 __global__ void __launch_bounds__(128, kForwardBlocks<kRawRegs<Tin, NV> * kRowsAtOnce<Tin, NV>>)
@@ -113,8 +132,8 @@ layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* _
                   long long rows, int d, float eps) {
     constexpr int U = kRowsAtOnce<Tin, NV>;
     const int lane = threadIdx.x % L, per = blockDim.x / L;
-    // weight, then bias (zeros without one); Staged: then a row of x per warp
-    extern __shared__ __align__(128) float params[];
+    const float inv = 1.0f / (float)d;
+    extern __shared__ __align__(128) float params[];  // weight, then bias (zeros without one)
     for (int i = 4 * threadIdx.x; i < d; i += 4 * blockDim.x) {
         *reinterpret_cast<float4*>(params + i) = *reinterpret_cast<const float4*>(weight + i);
         *reinterpret_cast<float4*>(params + d + i) =
@@ -147,11 +166,12 @@ layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* _
                 raw[u][n].get(v);
                 s2 = __fadd2_rn(s2, __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3])));
             }
-            const float mean = lane_sum<L>(s2.x + s2.y) / (float)d;
+            const float mean = mean_of(lane_sum<L>(s2.x + s2.y), (float)d, inv);
             const float2 neg = bcast2(-mean);
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
                 float2 v[4];
+                raw[u][n].pin();
                 raw[u][n].get(v);
                 if (kVec * (lane + n * L) < d) {
 #pragma unroll
@@ -161,7 +181,7 @@ layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* _
                     }
                 }
             }
-            const float rstd = 1.0f / sqrtf(lane_sum<L>(q2.x + q2.y) / (float)d + eps);
+            const float rstd = inv_sqrt(fmaf(lane_sum<L>(q2.x + q2.y), inv, eps));
             if (row < rows && lane == 0) {
                 if (mean_out) mean_out[row] = mean;
                 if (rstd_out) rstd_out[row] = rstd;
@@ -173,6 +193,7 @@ layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* _
                 const int c = kVec * (lane + n * L);
                 if (row < rows && c < d) {
                     float2 v[4], w[4], b[4];
+                    raw[u][n].pin();
                     raw[u][n].get(v);
                     load_param(params + c, w);
                     load_param(params + d + c, b);
@@ -180,6 +201,123 @@ layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* _
                     for (int e = 0; e < 4; ++e)
                         v[e] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[e], neg), r2), w[e], b[e]);
                     store_vec(yp + n * L * kVec, v);
+                }
+            }
+        }
+    }
+}
+
+// Wide rows: a team of one to six warps (the block) per U rows, NV vectors per thread and row, so
+// that a thread's share stays small enough for many teams per SM and each load of the
+// parameters serves U rows.  (A warp per row: 64 us at [8192, 6144] bf16, with 12 warps per SM
+// and the parameters' loads twice the row's; its next row staged in shared memory: 72.)
+template <typename Tin>
+constexpr int kTeamRows = sizeof(Tin) == 2 ? 2 : 1;
+
+template <int U>
+__device__ __forceinline__ void team_sum(float (&v)[U], float (*sm)[U]) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, nw = blockDim.x / 32;
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = warp_sum(v[u]);
+    if (nw == 1) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) sm[warp][u] = v[u];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        v[u] = 0.f;
+        for (int w = 0; w < nw; ++w) v[u] += sm[w][u];
+    }
+}
+
+template <typename Tin, int NV>
+__global__ void __launch_bounds__(192, 4)
+layer_norm_team_kernel(const Tin* x, const float* __restrict__ weight,
+                       const float* __restrict__ bias, Tin* y, float* __restrict__ mean_out,
+                       float* __restrict__ rstd_out, long long rows, int d, float eps) {
+    constexpr int U = kTeamRows<Tin>;
+    __shared__ float sm[2][6][U];  // each sum has its own: one barrier per sum
+    const int tid = threadIdx.x, T = blockDim.x;
+    const float inv = 1.0f / (float)d;
+    for (long long row0 = (long long)blockIdx.x * U; row0 < rows; row0 += (long long)gridDim.x * U) {
+        Raw<Tin> raw[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int c = kVec * (tid + n * T);
+                if (row0 + u < rows && c < d)
+                    raw[u][n].load(x + (row0 + u) * d + c);
+                else
+                    raw[u][n].zero();
+            }
+        }
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float2 s2 = bcast2(0.f);
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                float2 v[4];
+                raw[u][n].get(v);
+                s2 = __fadd2_rn(s2, __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3])));
+            }
+            mean[u] = s2.x + s2.y;
+        }
+        team_sum<U>(mean, sm[0]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mean[u] = mean_of(mean[u], (float)d, inv);
+            const float2 neg = bcast2(-mean[u]);
+            float2 q2 = bcast2(0.f);
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                float2 v[4];
+                raw[u][n].pin();
+                raw[u][n].get(v);
+                if (kVec * (tid + n * T) < d) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = __fadd2_rn(v[e], neg);
+                        q2 = __ffma2_rn(v[e], v[e], q2);
+                    }
+                }
+            }
+            rstd[u] = q2.x + q2.y;
+        }
+        team_sum<U>(rstd, sm[1]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            rstd[u] = inv_sqrt(fmaf(rstd[u], inv, eps));
+            if (tid == u && row0 + u < rows) {
+                if (mean_out) mean_out[row0 + u] = mean[u];
+                if (rstd_out) rstd_out[row0 + u] = rstd[u];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = kVec * (tid + n * T);
+            if (c < d) {
+                float2 w[4], b[4];
+                load_param(weight + c, w);
+                if (bias) {
+                    load_param(bias + c, b);
+                } else {
+                    b[0] = b[1] = b[2] = b[3] = bcast2(0.f);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float2 v[4];
+                    raw[u][n].pin();
+                    raw[u][n].get(v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = __fmul2_rn(__fadd2_rn(v[e], bcast2(-mean[u])), bcast2(rstd[u]));
+                        v[e] = __ffma2_rn(v[e], w[e], b[e]);
+                    }
+                    if (row0 + u < rows) store_vec(y + (row0 + u) * d + c, v);
                 }
             }
         }
@@ -202,6 +340,7 @@ layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
                         float* __restrict__ rstd_out, long long rows, int d, float eps) {
     __shared__ float sm[2][32];  // each sum has its own: one barrier per sum
     const int tpr = blockDim.x;
+    const float inv = 1.0f / (float)d;
     for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
         Raw<Tin> raw[NV];
         float2 s2 = bcast2(0.f), q2 = s2;
@@ -216,11 +355,12 @@ layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
             raw[n].get(v);
             s2 = __fadd2_rn(s2, __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3])));
         }
-        const float mean = block_sum(s2.x + s2.y, sm[0]) / (float)d;
+        const float mean = mean_of(block_sum(s2.x + s2.y, sm[0]), (float)d, inv);
         const float2 neg = bcast2(-mean);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             float2 v[4];
+            raw[n].pin();
             raw[n].get(v);
             if (kVec * ((int)threadIdx.x + n * tpr) < d) {
 #pragma unroll
@@ -230,7 +370,7 @@ layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
                 }
             }
         }
-        const float rstd = 1.0f / sqrtf(block_sum(q2.x + q2.y, sm[1]) / (float)d + eps);
+        const float rstd = inv_sqrt(fmaf(block_sum(q2.x + q2.y, sm[1]), inv, eps));
         if (threadIdx.x == 0) {
             if (mean_out) mean_out[row] = mean;
             if (rstd_out) rstd_out[row] = rstd;
@@ -240,6 +380,7 @@ layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
             const int c = kVec * ((int)threadIdx.x + n * tpr);
             if (c < d) {
                 float2 v[4], w[4], b[4];
+                raw[n].pin();
                 raw[n].get(v);
                 load_param(weight + c, w);
                 if (bias) {
@@ -339,14 +480,14 @@ struct Ring {
 
 // ------------------------------------------------------------------------------ backward
 // part [gridDim.x][2 d]: each block's sums over its rows, dweight, then dbias.
-template <typename Tin, int NV>
-__global__ void __launch_bounds__(512)
+template <typename Tin, int NV, int Threads>
+__global__ void __launch_bounds__(Threads)
 layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ weight,
                            const float* __restrict__ mean, const float* __restrict__ rstd,
                            const Tin* dy, Tin* dx, float* __restrict__ part, long long rows, int d,
                            int stages, int group_rows) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ float sums[2][16][8];
+    __shared__ float sums[2][Threads / 32][8];
     __shared__ uint64_t full[8];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, nw = blockDim.x / 32;
     Ring<Tin, 2> ring(smem_raw, full, stages, group_rows, rows, d);
@@ -657,16 +798,13 @@ struct RingShape {
     }
 };
 
-// 16-byte loads of a row that one lane keeps: 128 registers.
-constexpr int kMaxWarpVecs = 32;
-
 template <typename Tin>
 cudaError_t forward(const LayerNormParams& p, cudaStream_t stream) {
     const Tin* x = static_cast<const Tin*>(p.x);
     Tin* y = static_cast<Tin*>(p.y);
     const int vecs = (p.d + kVec - 1) / kVec, sms = sm_count();
-    // a warp takes ~16 us for a row of 6144, a block 4: up to four rows per SM go to blocks
-    if (kVec * vecs * sizeof(Tin) > 32 * 16 * kMaxWarpVecs || (vecs > 128 && p.rows <= 4LL * sms)) {
+    // up to four rows per SM, and rows above 9216 columns: a block of up to 512 threads per row
+    if (vecs > 1152 || (vecs > 128 && p.rows <= 4LL * sms)) {
         const int nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;  // at most 512 threads, to d = 16384
         const int threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
         const unsigned grid = (unsigned)std::min<long long>(p.rows, sms * 2LL);
@@ -699,14 +837,19 @@ cudaError_t forward(const LayerNormParams& p, cudaStream_t stream) {
     if (vecs <= 32) return go(layer_norm_kernel<Tin, 1, 32>, 32, kRowsAtOnce<Tin, 1>);
     if (vecs <= 64) return go(layer_norm_kernel<Tin, 2, 32>, 32, kRowsAtOnce<Tin, 2>);
     if (vecs <= 128) return go(layer_norm_kernel<Tin, 4, 32>, 32, kRowsAtOnce<Tin, 4>);
-    if (vecs <= 256) return go(layer_norm_kernel<Tin, 8, 32>, 32, kRowsAtOnce<Tin, 8>);
-    if (vecs <= 384) return go(layer_norm_kernel<Tin, 12, 32>, 32, kRowsAtOnce<Tin, 12>);
-    if (sizeof(Tin) == 4 || vecs <= 512) return go(layer_norm_kernel<Tin, 16, 32>, 32, kRowsAtOnce<Tin, 16>);
-    if constexpr (sizeof(Tin) == 2) {
-        if (vecs <= 768) return go(layer_norm_kernel<Tin, 24, 32>, 32, kRowsAtOnce<Tin, 24>);
-        return go(layer_norm_kernel<Tin, 32, 32>, 32, kRowsAtOnce<Tin, 32>);
-    }
-    return cudaErrorNotSupported;
+    // teams of up to six warps, four to six vectors per thread
+    const int warps = (vecs + 191) / 192, nv = (vecs + 32 * warps - 1) / (32 * warps);
+    constexpr int U = kTeamRows<Tin>;
+    auto kernel = nv <= 4   ? layer_norm_team_kernel<Tin, 4>
+                  : nv == 5 ? layer_norm_team_kernel<Tin, 5>
+                            : layer_norm_team_kernel<Tin, 6>;
+    int blocks = 1;
+    const cudaError_t e =
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, 32 * warps, 0);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::min<long long>((p.rows + U - 1) / U, (long long)sms * std::max(1, blocks));
+    kernel<<<grid, 32 * warps, 0, stream>>>(x, p.weight, p.bias, y, p.mean, p.rstd, p.rows, p.d, p.eps);
+    return cudaGetLastError();
 }
 
 // Launches of the backward pass: how many blocks (= rows of partial sums) and on what.
@@ -731,8 +874,9 @@ struct BackwardPlan {
             grid = (unsigned)std::min<long long>(p.rows, std::max<long long>(1, 2 * sm_count() / across));
             return;
         }
-        // at most 512 threads of 8 to 32 columns; two slots of the most rows that fit
-        nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+        // threads of 8 columns up to 768 of them, then 512 of up to 32; two slots of the most rows
+        // that fit
+        nv = vecs <= 768 ? 1 : vecs <= 1024 ? 2 : 4;
         threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
         const size_t row = 2 * sizeof(Tin) * p.d;  // x and dy
         const RingShape ring(row, 1, 2);
@@ -774,9 +918,10 @@ cudaError_t backward(const LayerNormGrads& p, const BackwardPlan<Tin>& plan, flo
                                                                   p.rows, p.d);
         return cudaGetLastError();
     }
-    auto kernel = plan.nv == 1   ? layer_norm_backward_kernel<Tin, 1>
-                  : plan.nv == 2 ? layer_norm_backward_kernel<Tin, 2>
-                                 : layer_norm_backward_kernel<Tin, 4>;
+    auto kernel = plan.nv == 2   ? layer_norm_backward_kernel<Tin, 2, 512>
+                  : plan.nv == 4 ? layer_norm_backward_kernel<Tin, 4, 512>
+                  : plan.threads <= 512 ? layer_norm_backward_kernel<Tin, 1, 512>
+                                        : layer_norm_backward_kernel<Tin, 1, 768>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)plan.smem);
     if (e != cudaSuccess) return e;

@@ -48,97 +48,195 @@ __device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
 // ------------------------------------------------------------------------ conv + SiLU
 
 constexpr int kW = 4;
-constexpr int kGSeg = 64;     // tokens per warp
-constexpr int kGWarps = 8;    // segments per CTA
+constexpr int kGWarps = 8;    // segments of tokens per CTA, one per warp
 constexpr int kGCh = 128;     // channels per CTA: four per lane
+constexpr int kGBatch = 8;    // tokens whose loads a lane issues together
+constexpr int kGMinSeg = 32;  // tokens of a segment; three more on each side are read again
 
-// CTA -> (channel tile, group of 8 segments of the B * nseg segments); warp -> segment.
-// part [groups][5 C]: the taps' sums as [C][4], then the bias's.
-__global__ void __launch_bounds__(32 * kGWarps)
-conv_backward_kernel(ConvGrads p, int nct, int nseg, float* part) {
+__device__ __forceinline__ float2 bf2(uint32_t u) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+// Two adjacent channels walking along time: the taps, the three inputs and the three ds before
+// the current token, and the sums of the parameters' gradients.
+struct ConvLane {
+    float2 w[kW], bias;
+    float2 h0, h1, h2;  // x at t - 3, t - 2, t - 1
+    float2 d0, d1, d2;  // ds likewise
+    float2 sum_w[kW], sum_b;
+
+    // ds of the token with input v and output gradient g
+    __device__ __forceinline__ float2 slope(float2 v, float2 g) const {
+        float2 s = __ffma2_rn(w[0], h0, bias);
+        s = __ffma2_rn(w[1], h1, s);
+        s = __ffma2_rn(w[2], h2, s);
+        s = __ffma2_rn(w[3], v, s);
+        const float2 m = __fmul2_rn(s, splat(-1.4426950408889634f));
+        const float2 den = __fadd2_rn(make_float2(ex2g(m.x), ex2g(m.y)), splat(1.f));
+        const float2 r = make_float2(rcpg(den.x), rcpg(den.y));  // sigmoid(s), 0 for den = inf
+        const float2 c = __ffma2_rn(r, splat(-1.f), splat(1.f));
+        // at s = -inf, s (1 - r) r would be -inf * 0; SiLU is flat there
+        const float2 q = __ffma2_rn(s, c, splat(1.f));
+        const float2 rq = make_float2(r.x > 0.f ? r.x * q.x : 0.f, r.y > 0.f ? r.y * q.y : 0.f);
+        return __fmul2_rn(g, rq);
+    }
+    __device__ __forceinline__ void add(float2 v, float2 d) {
+        sum_w[0] = __ffma2_rn(d, h0, sum_w[0]);
+        sum_w[1] = __ffma2_rn(d, h1, sum_w[1]);
+        sum_w[2] = __ffma2_rn(d, h2, sum_w[2]);
+        sum_w[3] = __ffma2_rn(d, v, sum_w[3]);
+        sum_b = __fadd2_rn(sum_b, d);
+    }
+    // the gradient of the input three tokens back, which has all its terms with this token's d
+    __device__ __forceinline__ float2 out(float2 d) const {
+        float2 o = __fmul2_rn(w[3], d0);
+        o = __ffma2_rn(w[2], d1, o);
+        o = __ffma2_rn(w[1], d2, o);
+        return __ffma2_rn(w[0], d, o);
+    }
+    __device__ __forceinline__ void shift(float2 v, float2 d) {
+        h0 = h1; h1 = h2; h2 = v;
+        d0 = d1; d1 = d2; d2 = d;
+    }
+};
+
+// CTA -> (channel tile, group of 8 segments of the B * nseg segments); warp -> segment of
+// `seg` tokens, lane -> four channels, one token after the other.  Tokens whose outputs may
+// be the state's, or that lie past the segment, go one at a time; the others in batches
+// whose loads are issued together, without tests.  part [groups][5 C]: the taps' sums as
+// [C][4], then the bias's.
+__global__ void __launch_bounds__(32 * kGWarps, 2)
+conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, float* part) {
     __shared__ float sm[kGWarps][5][kGCh];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int ct = blockIdx.x % nct, group = blockIdx.x / nct;
     const int c = ct * kGCh + 4 * lane;
     const long long sid = (long long)group * kGWarps + warp;
     const bool live = c < p.C && sid < (long long)p.B * nseg;
-    float aw[kW][4] = {}, ab[4] = {};
+    const float2 zero = splat(0.f);
+    ConvLane a[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        a[k].sum_b = a[k].d0 = a[k].d1 = a[k].d2 = zero;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) a[k].sum_w[i] = zero;
+    }
     if (live) {
-        const int b = (int)(sid / nseg);
-        const int T = p.T, C = p.C;
-        const int t0 = (int)(sid % nseg) * kGSeg, t1 = min(T, t0 + kGSeg);
-        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + ((size_t)b * T) * C + c;
-        const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(p.grad_y) + ((size_t)b * T) * C + c;
-        __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(p.grad_x) + ((size_t)b * T) * C + c;
-        float w[4][kW], bs[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-#pragma unroll
-            for (int i = 0; i < kW; ++i) w[e][i] = p.weight[(size_t)(c + e) * kW + i];
-            bs[e] = p.bias ? p.bias[c + e] : 0.f;
-        }
+        const int b = (int)(sid / nseg), T = p.T, C = p.C;
+        const int t0 = (int)(sid % nseg) * seg, t1 = min(T, t0 + seg);
+        const size_t base = (size_t)b * T * C + c;
+        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + base;
+        const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(p.grad_y) + base;
+        __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(p.grad_x) + base;
         const size_t st = ((size_t)b * C + c) * 3;
-        float h[3][4], ds[3][4] = {};  // x at t - 3 .. t - 1; ds at t - 3 .. t - 1
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float4 u = *reinterpret_cast<const float4*>(p.weight + (size_t)(c + 2 * k) * kW);
+            const float4 v = *reinterpret_cast<const float4*>(p.weight + (size_t)(c + 2 * k + 1) * kW);
+            a[k].w[0] = make_float2(u.x, v.x);
+            a[k].w[1] = make_float2(u.y, v.y);
+            a[k].w[2] = make_float2(u.z, v.z);
+            a[k].w[3] = make_float2(u.w, v.w);
+            a[k].bias = p.bias ? make_float2(p.bias[c + 2 * k], p.bias[c + 2 * k + 1]) : zero;
+        }
+        // the three inputs before the segment: x, or the state (oldest first)
+        float2 h[3][2];
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             const int t = t0 - 3 + j;
+            h[j][0] = h[j][1] = zero;
             if (t >= 0) {
-                unpack4(*reinterpret_cast<const uint2*>(x + (size_t)t * C), h[j]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) h[j][e] = p.state_in ? p.state_in[st + 3 * e + t + 3] : 0.f;
+                const uint2 u = *reinterpret_cast<const uint2*>(x + (size_t)t * C);
+                h[j][0] = bf2(u.x);
+                h[j][1] = bf2(u.y);
+            } else if (p.state_in) {
+                const float* s = p.state_in + st + t + 3;
+                h[j][0] = make_float2(s[0], s[3]);
+                h[j][1] = make_float2(s[6], s[9]);
             }
         }
-        for (int t = t0; t < t1 + 3; ++t) {
-            float v[4] = {}, d[4] = {};
-            if (t < T) {
-                float g[4];
-                unpack4(__ldcs(reinterpret_cast<const uint2*>(x + (size_t)t * C)), v);
-                unpack4(__ldcs(reinterpret_cast<const uint2*>(dy + (size_t)t * C)), g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float s = bs[e] + w[e][0] * h[0][e] + w[e][1] * h[1][e] +
-                                    w[e][2] * h[2][e] + w[e][3] * v[e];
-                    const float sg = sigmoid_fast(s);
-                    d[e] = g[e] * sg * (1.f + s * (1.f - sg));
-                    if (t < t1) {
-                        aw[0][e] += d[e] * h[0][e];
-                        aw[1][e] += d[e] * h[1][e];
-                        aw[2][e] += d[e] * h[2][e];
-                        aw[3][e] += d[e] * v[e];
-                        ab[e] += d[e];
-                    }
+        for (int k = 0; k < 2; ++k) a[k].h0 = h[0][k], a[k].h1 = h[1][k], a[k].h2 = h[2][k];
+
+        auto single = [&](int t) {
+            float2 v[2] = {zero, zero}, d[2] = {zero, zero};
+            if (t < T) {
+                const uint2 ux = __ldcs(reinterpret_cast<const uint2*>(x + (size_t)t * C));
+                const uint2 ug = __ldcs(reinterpret_cast<const uint2*>(dy + (size_t)t * C));
+                v[0] = bf2(ux.x);
+                v[1] = bf2(ux.y);
+                d[0] = a[0].slope(v[0], bf2(ug.x));
+                d[1] = a[1].slope(v[1], bf2(ug.y));
+                if (t < t1) {
+                    a[0].add(v[0], d[0]);
+                    a[1].add(v[1], d[1]);
                 }
             }
-            // the input three tokens back has all four of its terms
             const int u = t - 3;
             if (u >= t0 || t0 == 0) {
-                float o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[e] = w[e][3] * ds[0][e] + w[e][2] * ds[1][e] + w[e][1] * ds[2][e] + w[e][0] * d[e];
-                    // the state after the call holds the inputs T - 3 .. T - 1
-                    if (p.grad_state_out && u >= T - 3) o[e] += p.grad_state_out[st + 3 * e + u - (T - 3)];
+                float2 o[2] = {a[0].out(d[0]), a[1].out(d[1])};
+                // the state after the call holds the inputs T - 3 .. T - 1
+                if (p.grad_state_out && u >= T - 3) {
+                    const float* s = p.grad_state_out + st + u - (T - 3);
+                    o[0] = __fadd2_rn(o[0], make_float2(s[0], s[3]));
+                    o[1] = __fadd2_rn(o[1], make_float2(s[6], s[9]));
                 }
                 if (u >= 0) {
-                    __stcs(reinterpret_cast<uint2*>(dx + (size_t)u * C), pack4(o));
+                    const float f[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
+                    __stcs(reinterpret_cast<uint2*>(dx + (size_t)u * C), pack4(f));
                 } else if (p.grad_state_in) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p.grad_state_in[st + 3 * e + u + 3] = o[e];
+                    float* s = p.grad_state_in + st + u + 3;
+                    s[0] = o[0].x;
+                    s[3] = o[0].y;
+                    s[6] = o[1].x;
+                    s[9] = o[1].y;
                 }
             }
+            a[0].shift(v[0], d[0]);
+            a[1].shift(v[1], d[1]);
+        };
+        int t = t0;
+#pragma unroll 1
+        for (; t < min(t0 + 3, t1 + 3); ++t) single(t);
+        const __nv_bfloat16* xp = x + (size_t)t * C;
+        const __nv_bfloat16* gp = dy + (size_t)t * C;
+        __nv_bfloat16* op = dx + ((ptrdiff_t)t - 3) * C;
+        const size_t step = (size_t)kGBatch * C;
+#pragma unroll 1
+        for (; t + kGBatch <= t1; t += kGBatch, xp += step, gp += step, op += step) {
+            uint2 ux[kGBatch], ug[kGBatch];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                h[0][e] = h[1][e]; h[1][e] = h[2][e]; h[2][e] = v[e];
-                ds[0][e] = ds[1][e]; ds[1][e] = ds[2][e]; ds[2][e] = d[e];
+            for (int i = 0; i < kGBatch; ++i) {
+                ux[i] = __ldcs(reinterpret_cast<const uint2*>(xp + (size_t)i * C));
+                ug[i] = __ldcs(reinterpret_cast<const uint2*>(gp + (size_t)i * C));
+            }
+#pragma unroll
+            for (int i = 0; i < kGBatch; ++i) {
+                const float2 v[2] = {bf2(ux[i].x), bf2(ux[i].y)};
+                const float2 d[2] = {a[0].slope(v[0], bf2(ug[i].x)), a[1].slope(v[1], bf2(ug[i].y))};
+                a[0].add(v[0], d[0]);
+                a[1].add(v[1], d[1]);
+                const float2 o[2] = {a[0].out(d[0]), a[1].out(d[1])};
+                const float f[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
+                __stcs(reinterpret_cast<uint2*>(op + (size_t)i * C), pack4(f));
+                a[0].shift(v[0], d[0]);
+                a[1].shift(v[1], d[1]);
             }
         }
+#pragma unroll 1
+        for (; t < t1 + 3; ++t) single(t);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int k = 0; k < 2; ++k) {
+        const int ch = 4 * lane + 2 * k;
 #pragma unroll
-        for (int i = 0; i < kW; ++i) sm[warp][i][4 * lane + e] = aw[i][e];
-        sm[warp][4][4 * lane + e] = ab[e];
+        for (int i = 0; i < kW; ++i) {
+            sm[warp][i][ch] = a[k].sum_w[i].x;
+            sm[warp][i][ch + 1] = a[k].sum_w[i].y;
+        }
+        sm[warp][4][ch] = a[k].sum_b.x;
+        sm[warp][4][ch + 1] = a[k].sum_b.y;
     }
     __syncthreads();
     float* row = part + (size_t)group * 5 * p.C;
@@ -267,14 +365,19 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
         }
         return launch_column_sum(nullptr, 0, 5 * p.C, p.grad_weight, 4 * p.C, p.grad_bias, stream);
     }
-    const int nseg = (p.T + kGSeg - 1) / kGSeg;
-    const long long groups = ((long long)p.B * nseg + kGWarps - 1) / kGWarps;
+    // segments such that about two waves of CTAs cover the tokens, a multiple of a batch long
     const int nct = (p.C + kGCh - 1) / kGCh;
+    const long long want = 2LL * 2 * sm_count() * kGWarps / nct + 1;  // segments in all
+    const long long per = ((long long)p.B * p.T + want - 1) / want;
+    const int seg = (int)std::min<long long>(
+        std::max<long long>(kGMinSeg, (per + kGBatch - 1) / kGBatch * kGBatch), 1 << 20);
+    const int nseg = (p.T + seg - 1) / seg;
+    const long long groups = ((long long)p.B * nseg + kGWarps - 1) / kGWarps;
     if (groups * nct > 0x7fffffffLL) return cudaErrorNotSupported;
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * groups * 5 * p.C, stream);
     if (e != cudaSuccess) return e;
-    conv_backward_kernel<<<(unsigned)(groups * nct), 32 * kGWarps, 0, stream>>>(p, nct, nseg, part);
+    conv_backward_kernel<<<(unsigned)(groups * nct), 32 * kGWarps, 0, stream>>>(p, nct, nseg, seg, part);
     e = cudaGetLastError();
     if (e == cudaSuccess)
         e = launch_column_sum(part, groups, 5 * p.C, p.grad_weight, 4 * p.C, p.grad_bias, stream);
