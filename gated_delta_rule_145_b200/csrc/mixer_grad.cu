@@ -50,7 +50,8 @@ __device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
 constexpr int kW = 4;
 constexpr int kGWarps = 8;    // segments of tokens per CTA, one per warp
 constexpr int kGCh = 128;     // channels per CTA: four per lane
-constexpr int kGBatch = 8;    // tokens whose loads a lane issues together
+constexpr int kGBatch = 8;    // tokens per batch of loads
+constexpr int kGRing = 3;     // batches in shared memory: one in use, two in flight
 constexpr int kGMinSeg = 32;  // tokens of a segment; three more on each side are read again
 
 __device__ __forceinline__ float2 bf2(uint32_t u) {
@@ -101,14 +102,32 @@ struct ConvLane {
     }
 };
 
+// Eight bytes global -> shared, zeros if not `in` (the source is not read then).
+__device__ __forceinline__ void copy8(uint2* dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(in ? 8 : 0)
+                 : "memory");
+}
+
+// x and dy of kGBatch tokens, one lane's eight bytes each: a lane reads only what it copied
+// itself, so the ring needs no barrier.
+struct ConvBatch {
+    uint2 x[kGBatch][32], g[kGBatch][32];
+};
+union ConvBackwardSmem {
+    ConvBatch ring[kGWarps][kGRing];
+    float sums[kGWarps][5][kGCh];
+};
+
 // CTA -> (channel tile, group of 8 segments of the B * nseg segments); warp -> segment of
-// `seg` tokens, lane -> four channels, one token after the other.  Tokens whose outputs may
-// be the state's, or that lie past the segment, go one at a time; the others in batches
-// whose loads are issued together, without tests.  part [groups][5 C]: the taps' sums as
-// [C][4], then the bias's.
+// `seg` tokens, lane -> four channels, one token after the other, its loads two batches
+// ahead (held in registers, one batch at a time, the loads' latency showed: 0.6 of HBM).
+// part [groups][5 C]: the taps' sums as [C][4], then the bias's.
 __global__ void __launch_bounds__(32 * kGWarps, 2)
 conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, float* part) {
-    __shared__ float sm[kGWarps][5][kGCh];
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    ConvBackwardSmem& smem = *reinterpret_cast<ConvBackwardSmem*>(smem_raw);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int ct = blockIdx.x % nct, group = blockIdx.x / nct;
     const int c = ct * kGCh + 4 * lane;
@@ -159,74 +178,85 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, float* part) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) a[k].h0 = h[0][k], a[k].h1 = h[1][k], a[k].h2 = h[2][k];
 
-        auto single = [&](int t) {
-            float2 v[2] = {zero, zero}, d[2] = {zero, zero};
-            if (t < T) {
-                const uint2 ux = __ldcs(reinterpret_cast<const uint2*>(x + (size_t)t * C));
-                const uint2 ug = __ldcs(reinterpret_cast<const uint2*>(dy + (size_t)t * C));
-                v[0] = bf2(ux.x);
-                v[1] = bf2(ux.y);
-                d[0] = a[0].slope(v[0], bf2(ug.x));
-                d[1] = a[1].slope(v[1], bf2(ug.y));
-                if (t < t1) {
-                    a[0].add(v[0], d[0]);
-                    a[1].add(v[1], d[1]);
-                }
-            }
-            const int u = t - 3;
-            if (u >= t0 || t0 == 0) {
-                float2 o[2] = {a[0].out(d[0]), a[1].out(d[1])};
-                // the state after the call holds the inputs T - 3 .. T - 1
-                if (p.grad_state_out && u >= T - 3) {
-                    const float* s = p.grad_state_out + st + u - (T - 3);
-                    o[0] = __fadd2_rn(o[0], make_float2(s[0], s[3]));
-                    o[1] = __fadd2_rn(o[1], make_float2(s[6], s[9]));
-                }
-                if (u >= 0) {
-                    const float f[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
-                    __stcs(reinterpret_cast<uint2*>(dx + (size_t)u * C), pack4(f));
-                } else if (p.grad_state_in) {
-                    float* s = p.grad_state_in + st + u + 3;
-                    s[0] = o[0].x;
-                    s[3] = o[0].y;
-                    s[6] = o[1].x;
-                    s[9] = o[1].y;
-                }
-            }
-            a[0].shift(v[0], d[0]);
-            a[1].shift(v[1], d[1]);
-        };
-        int t = t0;
-#pragma unroll 1
-        for (; t < min(t0 + 3, t1 + 3); ++t) single(t);
-        const __nv_bfloat16* xp = x + (size_t)t * C;
-        const __nv_bfloat16* gp = dy + (size_t)t * C;
-        __nv_bfloat16* op = dx + ((ptrdiff_t)t - 3) * C;
-        const size_t step = (size_t)kGBatch * C;
-#pragma unroll 1
-        for (; t + kGBatch <= t1; t += kGBatch, xp += step, gp += step, op += step) {
-            uint2 ux[kGBatch], ug[kGBatch];
-#pragma unroll
-            for (int i = 0; i < kGBatch; ++i) {
-                ux[i] = __ldcs(reinterpret_cast<const uint2*>(xp + (size_t)i * C));
-                ug[i] = __ldcs(reinterpret_cast<const uint2*>(gp + (size_t)i * C));
-            }
-#pragma unroll
-            for (int i = 0; i < kGBatch; ++i) {
-                const float2 v[2] = {bf2(ux[i].x), bf2(ux[i].y)};
-                const float2 d[2] = {a[0].slope(v[0], bf2(ug[i].x)), a[1].slope(v[1], bf2(ug[i].y))};
+        // one token: ds, the sums (`sum`), the input three tokens back
+        auto token = [&](uint2 ux, uint2 ug, bool sum) {
+            const float2 v[2] = {bf2(ux.x), bf2(ux.y)};
+            const float2 d[2] = {a[0].slope(v[0], bf2(ug.x)), a[1].slope(v[1], bf2(ug.y))};
+            if (sum) {
                 a[0].add(v[0], d[0]);
                 a[1].add(v[1], d[1]);
-                const float2 o[2] = {a[0].out(d[0]), a[1].out(d[1])};
-                const float f[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
-                __stcs(reinterpret_cast<uint2*>(op + (size_t)i * C), pack4(f));
-                a[0].shift(v[0], d[0]);
-                a[1].shift(v[1], d[1]);
+            }
+            const float4 o = make_float4(a[0].out(d[0]).x, a[0].out(d[0]).y, a[1].out(d[1]).x,
+                                         a[1].out(d[1]).y);
+            a[0].shift(v[0], d[0]);
+            a[1].shift(v[1], d[1]);
+            return o;
+        };
+        ConvBatch* ring = smem.ring[warp];
+        const int end = min(T, t1 + 3);  // tokens read: three past the segment
+        auto fetch = [&](int t, int slot) {
+            const __nv_bfloat16* xp = x + (size_t)t * C;
+            const __nv_bfloat16* gp = dy + (size_t)t * C;
+            if (t < end) {
+#pragma unroll
+                for (int i = 0; i < kGBatch; ++i) {
+                    const bool in = t + i < end;
+                    copy8(&ring[slot].x[i][lane], in ? xp + (size_t)i * C : x, in);
+                    copy8(&ring[slot].g[i][lane], in ? gp + (size_t)i * C : dy, in);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < kGRing - 1; ++k) fetch(t0 + k * kGBatch, k);
+        int slot = 0;
+#pragma unroll 1
+        for (int t = t0; t < t1 + 3; t += kGBatch) {
+            // the slot used last takes the batch two ahead; all but the newest two have landed
+            fetch(t + (kGRing - 1) * kGBatch, slot == 0 ? kGRing - 1 : slot - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kGRing - 1) : "memory");
+            const ConvBatch& now = ring[slot];
+            slot = slot + 1 == kGRing ? 0 : slot + 1;
+            __nv_bfloat16* op = dx + ((ptrdiff_t)t - 3) * C;
+            if (t > t0 && t + kGBatch <= t1) {
+#pragma unroll
+                for (int i = 0; i < kGBatch; ++i) {
+                    const float4 o = token(now.x[i][lane], now.g[i][lane], true);
+                    const float f[4] = {o.x, o.y, o.z, o.w};
+                    __stcs(reinterpret_cast<uint2*>(op + (size_t)i * C), pack4(f));
+                }
+                continue;
+            }
+            // the first batch, and those that reach the segment's end (past T: zeros)
+#pragma unroll 1
+            for (int i = 0; i < kGBatch; ++i) {
+                const int u = t + i - 3;
+                if (u >= t1) break;
+                uint2 ux = make_uint2(0, 0), ug = ux;
+                if (t + i < end) {
+                    ux = now.x[i][lane];
+                    ug = now.g[i][lane];
+                }
+                const float4 o = token(ux, ug, t + i < t1);
+                if (u < t0 && t0 > 0) continue;  // another segment's
+                float f[4] = {o.x, o.y, o.z, o.w};
+                // the state after the call holds the inputs T - 3 .. T - 1
+                if (p.grad_state_out && u >= T - 3) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] += p.grad_state_out[st + 3 * e + u - (T - 3)];
+                }
+                if (u >= 0) {
+                    __stcs(reinterpret_cast<uint2*>(op + (size_t)i * C), pack4(f));
+                } else if (p.grad_state_in) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p.grad_state_in[st + 3 * e + u + 3] = f[e];
+                }
             }
         }
-#pragma unroll 1
-        for (; t < t1 + 3; ++t) single(t);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    __syncthreads();  // the ring is done with: its memory takes the sums
+    float(*sm)[5][kGCh] = smem.sums;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int ch = 4 * lane + 2 * k;
@@ -365,20 +395,33 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
         }
         return launch_column_sum(nullptr, 0, 5 * p.C, p.grad_weight, 4 * p.C, p.grad_bias, stream);
     }
-    // segments such that about two waves of CTAs cover the tokens, a multiple of a batch long
+    // Segments: for one to eight waves of CTAs, the most segments that they hold, and of these
+    // the number that takes the fewest token steps (a segment costs some 24 beside its own).
     const int nct = (p.C + kGCh - 1) / kGCh;
-    const long long want = 2LL * 2 * sm_count() * kGWarps / nct + 1;  // segments in all
-    const long long per = ((long long)p.B * p.T + want - 1) / want;
-    const int seg = (int)std::min<long long>(
-        std::max<long long>(kGMinSeg, (per + kGBatch - 1) / kGBatch * kGBatch), 1 << 20);
-    const int nseg = (p.T + seg - 1) / seg;
+    const long long slots = 2LL * sm_count();
+    int seg = 0, nseg = 0;
+    long long best = 0;
+    for (int waves = 1; waves <= 8; ++waves) {
+        const long long most = std::max<long long>(1, waves * slots / nct * kGWarps / p.B);
+        const long long len = std::max<long long>(
+            kGMinSeg, ((p.T + most - 1) / most + kGBatch - 1) / kGBatch * kGBatch);
+        const long long n = (p.T + len - 1) / len;
+        const long long ctas = (p.B * n + kGWarps - 1) / kGWarps * nct;
+        const long long cost = (ctas + slots - 1) / slots * (std::min<long long>(len, p.T) + 24);
+        if (!seg || cost < best) seg = (int)len, nseg = (int)n, best = cost;
+    }
     const long long groups = ((long long)p.B * nseg + kGWarps - 1) / kGWarps;
     if (groups * nct > 0x7fffffffLL) return cudaErrorNotSupported;
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * groups * 5 * p.C, stream);
     if (e != cudaSuccess) return e;
-    conv_backward_kernel<<<(unsigned)(groups * nct), 32 * kGWarps, 0, stream>>>(p, nct, nseg, seg, part);
-    e = cudaGetLastError();
+    e = cudaFuncSetAttribute(conv_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(ConvBackwardSmem));
+    if (e == cudaSuccess) {
+        conv_backward_kernel<<<(unsigned)(groups * nct), 32 * kGWarps, sizeof(ConvBackwardSmem),
+                               stream>>>(p, nct, nseg, seg, part);
+        e = cudaGetLastError();
+    }
     if (e == cudaSuccess)
         e = launch_column_sum(part, groups, 5 * p.C, p.grad_weight, 4 * p.C, p.grad_bias, stream);
     const cudaError_t f = cudaFreeAsync(part, stream);
