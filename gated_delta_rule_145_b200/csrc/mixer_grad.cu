@@ -30,6 +30,13 @@ __device__ __forceinline__ float rcpg(float x) {
     return y;
 }
 
+// The larger value; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // sigmoid(v) by 1 / (1 + 2^(-v log2 e)): relative error ~1e-6, 0 where the power is +inf
 __device__ __forceinline__ float sigmoid_fast(float v) {
     return rcpg(1.0f + ex2g(v * -1.4426950408889634f));
@@ -73,14 +80,15 @@ struct ConvLane {
         s = __ffma2_rn(w[1], h1, s);
         s = __ffma2_rn(w[2], h2, s);
         s = __ffma2_rn(w[3], v, s);
+        // SiLU'(s) = r (1 + s (1 - r)), r = sigmoid(s) = 1 / den.  Below -41 it is under 2^-53 in
+        // magnitude; there s is taken as -41, so that the two channels' den stay finite when
+        // multiplied: one reciprocal, the pass's scarcest instruction, serves both.  NaN stays.
+        s = make_float2(max_nan(s.x, -41.f), max_nan(s.y, -41.f));
         const float2 m = __fmul2_rn(s, splat(-1.4426950408889634f));
         const float2 den = __fadd2_rn(make_float2(ex2g(m.x), ex2g(m.y)), splat(1.f));
-        const float2 r = make_float2(rcpg(den.x), rcpg(den.y));  // sigmoid(s), 0 for den = inf
-        const float2 c = __ffma2_rn(r, splat(-1.f), splat(1.f));
-        // at s = -inf, s (1 - r) r would be -inf * 0; SiLU is flat there
-        const float2 q = __ffma2_rn(s, c, splat(1.f));
-        const float2 rq = make_float2(r.x > 0.f ? r.x * q.x : 0.f, r.y > 0.f ? r.y * q.y : 0.f);
-        return __fmul2_rn(g, rq);
+        const float2 r = __fmul2_rn(splat(rcpg(den.x * den.y)), make_float2(den.y, den.x));
+        const float2 q = __ffma2_rn(s, __ffma2_rn(r, splat(-1.f), splat(1.f)), splat(1.f));
+        return __fmul2_rn(g, __fmul2_rn(r, q));
     }
     __device__ __forceinline__ void add(float2 v, float2 d) {
         sum_w[0] = __ffma2_rn(d, h0, sum_w[0]);
