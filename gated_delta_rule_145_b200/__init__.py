@@ -133,27 +133,20 @@ def gdr_release_workspace() -> None:
     library().gdr_release_workspace()
 
 
-def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return _P(x)
-    return _P(x.data_ptr())
-
-
 def _stream(s):
     if s is None:
         import torch
 
-        return _P(torch.cuda.current_stream().cuda_stream)
-    if isinstance(s, int):
-        return _P(s)
-    return _P(s.cuda_stream)
+        # torch.cuda.current_stream() makes a Stream object (1.3 us) around this integer
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+    return s if isinstance(s, int) else s.cuda_stream
 
 
 def _call(name, ptrs, ints, stream, check):
-    fn = getattr(library(), name)
-    status = fn(*[_ptr(p) for p in ptrs], *[int(i) for i in ints], _stream(stream))
+    fn = getattr(_lib or library(), name)
+    status = fn(*[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs],
+                *map(int, ints), _stream(stream))
     if check and status != GDR_OK:
         raise GdrError(name, status)
     return status
@@ -286,8 +279,9 @@ def gdr_short_conv_silu(x, weight, bias, conv_state_in, conv_state_out, y, B, T,
 
 def _rows_call(name, ptrs, rows, d, rest, stream, check):
     """A row-wise call: pointers, then rows, d and what follows them (eps)."""
-    status = getattr(library(), name)(*[_ptr(p) for p in ptrs], int(rows), int(d), *rest,
-                                      _stream(stream))
+    status = getattr(_lib or library(), name)(
+        *[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs], int(rows), int(d),
+        *rest, _stream(stream))
     if check and status != GDR_OK:
         raise GdrError(name, status)
     return status
@@ -460,20 +454,21 @@ def decode_step(q, k, v, a, b, A_log, dt_bias, state, out=None, stream=None, era
     return out
 
 
-def _check_arg(name, t, dtype, shape, like=None, rows=False):
-    """`t` is a CUDA tensor of this type and shape (None passes), on `like`'s device and
-    contiguous; ``rows``: only its last dimension has to be."""
-    if t is None:
-        return
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if not rows and not t.is_contiguous():
+def _check(device, *specs):
+    """Every (name, tensor, dtype, shape, dense) of `specs` is a CUDA tensor on `device` of this
+    type and shape, contiguous if `dense`; None passes."""
+    for name, t, dtype, shape, dense in specs:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and
+                         t.is_cuda and (not dense or t.is_contiguous())):
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -482,30 +477,46 @@ def _token_stride(tensors, B, T, C):
     or slices of the last dimension of a wider dense tensor."""
     if B * T * C == 0:
         return max(C, 1)
-    first = next(iter(tensors.values()))
-    ld = first.stride(1) if T > 1 else first.stride(0) if B > 1 else C
-    for name, t in tensors.items():
-        if ((C > 1 and t.stride(2) != 1) or (T > 1 and t.stride(1) != ld) or
-                (B > 1 and t.stride(0) != T * ld)):
-            raise ValueError(f"{name}: x, a, b need one layout, dense or slices of the last "
-                             f"dimension of a dense tensor; got strides {t.stride()}")
+    first = tensors[0].stride()
+    ld = first[1] if T > 1 else first[0] if B > 1 else C
+    for t in tensors:
+        sb, st, sc = t.stride()
+        if (C > 1 and sc != 1) or (T > 1 and st != ld) or (B > 1 and sb != T * ld):
+            raise ValueError("x, a, b (and their gradients) need one layout, dense or slices of "
+                             f"the last dimension of a dense tensor; got strides {t.stride()}")
     return ld
 
 
 def _input_type(x, name):
     import torch
 
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
         raise ValueError(f"{name} must be bf16 or fp32, got {x.dtype}")
     return x.dtype
 
 
-def _on_device(t, stream):
-    """Context that makes t's device current, and the stream to use on it."""
+def _on_device(t, stream, fn, *args):
+    """fn(*args) on `stream` (None: the current one) of t's device, that device current."""
     import torch
 
-    ctx = torch.cuda.device(t.device)
-    return ctx, (torch.cuda.current_stream(t.device) if stream is None else stream)
+    index = t.get_device()
+    if index == torch.cuda.current_device():
+        return fn(*args, stream=stream)
+    with torch.cuda.device(index):
+        return fn(*args, stream=stream)
+
+
+def _empty(t, stream, *specs):
+    """Uninitialised tensors of (shape, dtype) on t's device, allocated for use on `stream`: memory
+    of the current stream's pool could still be in use by work queued there."""
+    if stream is None:
+        return [t.new_empty(shape, dtype=dtype) for shape, dtype in specs]
+    import torch
+
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    with torch.cuda.stream(stream):
+        return [t.new_empty(shape, dtype=dtype) for shape, dtype in specs]
 
 
 def _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens):
@@ -514,20 +525,18 @@ def _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens):
     dtype = _input_type(x, "x")
     if x.dim() != 3:
         raise ValueError(f"x must be [B, T, C], got shape {tuple(x.shape)}")
-    B, T, C = x.shape
+    B, T, C = shape = x.shape
     f32 = torch.float32
-    for name, t in dict(x=x, a=a, b=b).items():
-        _check_arg(name, t, dtype, (B, T, C), x, rows=True)
     nseq = B
     if cu_seqlens is not None:
         if B != 1:
             raise ValueError("packed sequences need B == 1")
         nseq = cu_seqlens.numel() - 1
-        _check_arg("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), x)
-    _check_arg("A_log", A_log, f32, (C,), x)
-    _check_arg("dt_bias", dt_bias, f32, (C,), x)
-    _check_arg("init_state", init_state, f32, (nseq, C), x)
-    return dtype, nseq, T, C, _token_stride(dict(x=x, a=a, b=b), B, T, C)
+    _check(x.device, ("x", x, dtype, shape, False), ("a", a, dtype, shape, False),
+           ("b", b, dtype, shape, False), ("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), True),
+           ("A_log", A_log, f32, (C,), True), ("dt_bias", dt_bias, f32, (C,), True),
+           ("init_state", init_state, f32, (nseq, C), True))
+    return dtype, nseq, T, C, _token_stride((x, a, b), B, T, C)
 
 
 def linear_recurrence(x, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None, out=None,
@@ -543,16 +552,14 @@ def linear_recurrence(x, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None,
     dtype, nseq, T, C, ld = _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens)
     f32 = torch.float32
     if out is None:
-        out = torch.empty(x.shape, device=x.device, dtype=f32)
+        out, = _empty(x, stream, (x.shape, f32))
     if final_state is None:
-        final_state = torch.empty((nseq, C), device=x.device, dtype=f32)
-    _check_arg("out", out, f32, x.shape, x)
-    _check_arg("final_state", final_state, f32, (nseq, C), x)
-    ctx, stream = _on_device(x, stream)
-    with ctx:
-        fn = gdr_linear_recurrence_f32 if dtype == f32 else gdr_linear_recurrence
-        fn(x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens, nseq, T, C, ld,
-           stream=stream)
+        final_state, = _empty(x, stream, ((nseq, C), f32))
+    _check(x.device, ("out", out, f32, x.shape, True),
+           ("final_state", final_state, f32, (nseq, C), True))
+    fn = gdr_linear_recurrence_f32 if dtype == f32 else gdr_linear_recurrence
+    _on_device(x, stream, fn, x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens,
+               nseq, T, C, ld)
     return out, final_state
 
 
@@ -568,28 +575,23 @@ def linear_recurrence_backward(x, a, b, A_log, dt_bias, out, grad_out, grad_fina
 
     dtype, nseq, T, C, ld = _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens)
     f32 = torch.float32
-    _check_arg("out", out, f32, x.shape, x)
-    _check_arg("grad_out", grad_out, f32, x.shape, x)
-    _check_arg("grad_final_state", grad_final_state, f32, (nseq, C), x)
-    grads = dict(grad_x=grad_x, grad_a=grad_a, grad_b=grad_b)
-    if any(g is None for g in grads.values()):
-        if any(g is not None for g in grads.values()):
+    grads = (grad_x, grad_a, grad_b)
+    if grad_x is None or grad_a is None or grad_b is None:
+        if any(g is not None for g in grads):
             raise ValueError("give grad_x, grad_a and grad_b together, or none of them")
-        grads = {k: torch.empty(x.shape, device=x.device, dtype=dtype) for k in grads}
-    for name, t in grads.items():
-        _check_arg(name, t, dtype, x.shape, x, rows=True)
+        grads = _empty(x, stream, *[(x.shape, dtype)] * 3)
+    _check(x.device, ("out", out, f32, x.shape, True), ("grad_out", grad_out, f32, x.shape, True),
+           ("grad_final_state", grad_final_state, f32, (nseq, C), True),
+           *[(n, g, dtype, x.shape, False) for n, g in zip(("grad_x", "grad_a", "grad_b"), grads)])
     ld_grad = _token_stride(grads, x.shape[0], T, C)
-    grad_A_log, grad_dt_bias = torch.empty((2, C), device=x.device, dtype=f32)
-    grad_init = torch.empty((nseq, C), device=x.device, dtype=f32)
-    ctx, stream = _on_device(x, stream)
-    with ctx:
-        fn = (gdr_linear_recurrence_backward_f32 if dtype == f32 else
-              gdr_linear_recurrence_backward)
-        fn(x, a, b, A_log, dt_bias, init_state, out, grad_out, grad_final_state,
-           grads["grad_x"], grads["grad_a"], grads["grad_b"], grad_A_log, grad_dt_bias, grad_init,
-           cu_seqlens, nseq, T, C, ld, ld_grad, stream=stream)
-    return (grads["grad_x"], grads["grad_a"], grads["grad_b"], grad_A_log, grad_dt_bias,
-            grad_init)
+    grad_A_log, grad_dt_bias, grad_init = _empty(x, stream, ((C,), f32), ((C,), f32),
+                                                 ((nseq, C), f32))
+    fn = (gdr_linear_recurrence_backward_f32 if dtype == f32 else
+          gdr_linear_recurrence_backward)
+    _on_device(x, stream, fn, x, a, b, A_log, dt_bias, init_state, out, grad_out,
+               grad_final_state, *grads, grad_A_log, grad_dt_bias, grad_init, cu_seqlens, nseq, T,
+               C, ld, ld_grad)
+    return (*grads, grad_A_log, grad_dt_bias, grad_init)
 
 
 def _row_args(x):
@@ -606,16 +608,13 @@ def layer_norm(x, weight, bias=None, eps=1e-5, y=None, stream=None):
 
     dtype, f32 = _input_type(x, "x"), torch.float32
     rows, d = _row_args(x)
-    _check_arg("x", x, dtype, x.shape)
-    _check_arg("weight", weight, f32, (d,), x)
-    _check_arg("bias", bias, f32, (d,), x)
-    y = torch.empty_like(x) if y is None else y
-    _check_arg("y", y, dtype, x.shape, x)
-    mean, rstd = torch.empty((2,) + tuple(x.shape[:-1]), device=x.device, dtype=f32)
-    ctx, stream = _on_device(x, stream)
-    with ctx:
-        fn = gdr_layer_norm_f32 if dtype == f32 else gdr_layer_norm
-        fn(x, weight, bias, y, mean, rstd, rows, d, eps, stream=stream)
+    _check(x.device, ("x", x, dtype, x.shape, True), ("weight", weight, f32, (d,), True),
+           ("bias", bias, f32, (d,), True), ("y", y, dtype, x.shape, True))
+    mean, rstd = _empty(x, stream, (x.shape[:-1], f32), (x.shape[:-1], f32))
+    if y is None:
+        y, = _empty(x, stream, (x.shape, dtype))
+    fn = gdr_layer_norm_f32 if dtype == f32 else gdr_layer_norm
+    _on_device(x, stream, fn, x, weight, bias, y, mean, rstd, rows, d, eps)
     return y, mean, rstd
 
 
@@ -626,18 +625,15 @@ def layer_norm_backward(x, weight, mean, rstd, grad_y, grad_x=None, stream=None)
 
     dtype, f32 = _input_type(x, "x"), torch.float32
     rows, d = _row_args(x)
-    _check_arg("x", x, dtype, x.shape)
-    _check_arg("weight", weight, f32, (d,), x)
-    for name, t in dict(mean=mean, rstd=rstd).items():
-        _check_arg(name, t, f32, x.shape[:-1], x)
-    _check_arg("grad_y", grad_y, dtype, x.shape, x)
-    grad_x = torch.empty_like(x) if grad_x is None else grad_x
-    _check_arg("grad_x", grad_x, dtype, x.shape, x)
-    grad_weight, grad_bias = torch.empty((2, d), device=x.device, dtype=f32)
-    ctx, stream = _on_device(x, stream)
-    with ctx:
-        fn = gdr_layer_norm_backward_f32 if dtype == f32 else gdr_layer_norm_backward
-        fn(x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias, rows, d, stream=stream)
+    _check(x.device, ("x", x, dtype, x.shape, True), ("weight", weight, f32, (d,), True),
+           ("mean", mean, f32, x.shape[:-1], True), ("rstd", rstd, f32, x.shape[:-1], True),
+           ("grad_y", grad_y, dtype, x.shape, True), ("grad_x", grad_x, dtype, x.shape, True))
+    if grad_x is None:
+        grad_x, = _empty(x, stream, (x.shape, dtype))
+    grad_weight, grad_bias = _empty(x, stream, ((d,), f32), ((d,), f32))
+    fn = gdr_layer_norm_backward_f32 if dtype == f32 else gdr_layer_norm_backward
+    _on_device(x, stream, fn, x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias, rows,
+               d)
     return grad_x, grad_weight, grad_bias
 
 
@@ -652,21 +648,14 @@ def short_conv_silu_backward(x, weight, grad_y, bias=None, conv_state_in=None,
     if x.dim() != 3:
         raise ValueError(f"x must be [B, T, C], got shape {tuple(x.shape)}")
     B, T, C = x.shape
-    _check_arg("x", x, bf16, x.shape)
-    _check_arg("weight", weight, f32, (C, 4), x)
-    _check_arg("grad_y", grad_y, bf16, x.shape, x)
-    _check_arg("bias", bias, f32, (C,), x)
-    _check_arg("conv_state_in", conv_state_in, f32, (B, C, 3), x)
-    _check_arg("grad_conv_state_out", grad_conv_state_out, f32, (B, C, 3), x)
-    grad_x = torch.empty_like(x)
-    grad_weight = torch.empty_like(weight)
-    grad_bias = torch.empty((C,), device=x.device, dtype=f32)
-    grad_state = torch.empty((B, C, 3), device=x.device, dtype=f32)
-    ctx, stream = _on_device(x, stream)
-    with ctx:
-        gdr_short_conv_silu_backward(x, weight, bias, conv_state_in, grad_y, grad_conv_state_out,
-                                     grad_x, grad_weight, grad_bias, grad_state, B, T, C,
-                                     stream=stream)
+    _check(x.device, ("x", x, bf16, x.shape, True), ("weight", weight, f32, (C, 4), True),
+           ("grad_y", grad_y, bf16, x.shape, True), ("bias", bias, f32, (C,), True),
+           ("conv_state_in", conv_state_in, f32, (B, C, 3), True),
+           ("grad_conv_state_out", grad_conv_state_out, f32, (B, C, 3), True))
+    grad_x, grad_weight, grad_bias, grad_state = _empty(
+        x, stream, (x.shape, bf16), ((C, 4), f32), ((C,), f32), ((B, C, 3), f32))
+    _on_device(x, stream, gdr_short_conv_silu_backward, x, weight, bias, conv_state_in, grad_y,
+               grad_conv_state_out, grad_x, grad_weight, grad_bias, grad_state, B, T, C)
     return grad_x, grad_weight, grad_bias, grad_state
 
 
@@ -678,13 +667,9 @@ def gated_rmsnorm_backward(o, z, weight, grad_y, eps=1e-6, stream=None):
     f32 = torch.float32
     dtype = _input_type(z, "z")
     rows, d = _row_args(o)
-    _check_arg("o", o, f32, o.shape)
-    _check_arg("z", z, dtype, o.shape, o)
-    _check_arg("weight", weight, f32, (d,), o)
-    _check_arg("grad_y", grad_y, f32, o.shape, o)
-    grad_o, grad_z, grad_weight = torch.empty_like(o), torch.empty_like(z), torch.empty_like(weight)
-    ctx, stream = _on_device(o, stream)
-    with ctx:
-        fn = gdr_gated_rmsnorm_backward_f32 if dtype == f32 else gdr_gated_rmsnorm_backward
-        fn(o, z, weight, grad_y, grad_o, grad_z, grad_weight, rows, d, eps, stream=stream)
+    _check(o.device, ("o", o, f32, o.shape, True), ("z", z, dtype, o.shape, True),
+           ("weight", weight, f32, (d,), True), ("grad_y", grad_y, f32, o.shape, True))
+    grad_o, grad_z, grad_weight = _empty(o, stream, (o.shape, f32), (z.shape, dtype), ((d,), f32))
+    fn = gdr_gated_rmsnorm_backward_f32 if dtype == f32 else gdr_gated_rmsnorm_backward
+    _on_device(o, stream, fn, o, z, weight, grad_y, grad_o, grad_z, grad_weight, rows, d, eps)
     return grad_o, grad_z, grad_weight

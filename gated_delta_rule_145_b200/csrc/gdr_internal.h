@@ -171,6 +171,13 @@ cudaError_t launch_segment_bounds(int32_t* cu, int G, int L, int T, cudaStream_t
 cudaError_t launch_prefill_host(const FwdParams& host_params, int seg, cudaStream_t stream,
                                 int (*prefill)(const FwdParams&, cudaStream_t), int* status);
 
+// Multiprocessors of the current device, asked once per device; workspace.cu.
+int device_sms();
+
+// Allows `kernel` this much dynamic shared memory on the current device; the runtime is asked
+// once per kernel, device and size above the last one.
+cudaError_t allow_smem(const void* kernel, size_t bytes);
+
 // The library's stream-ordered workspace pool (workspace.cu).
 cudaError_t workspace_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 

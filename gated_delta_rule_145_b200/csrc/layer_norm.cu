@@ -122,11 +122,11 @@ template <typename Tin, int NV>
 constexpr int kRowsAtOnce = kRawRegs<Tin, NV> <= 8 ? 4 : kRawRegs<Tin, NV> <= 16 ? 2 : 1;
 
 // blocks of 128 threads per SM whose registers hold the raw values and ~32 more
-template <int raw>
-constexpr int kForwardBlocks = 512 / (raw + 32);
+template <typename Tin, int NV>
+constexpr int kForwardBlocks = 512 / (kRawRegs<Tin, NV> * kRowsAtOnce<Tin, NV> + 32);
 
 template <typename Tin, int NV, int L>
-__global__ void __launch_bounds__(128, kForwardBlocks<kRawRegs<Tin, NV> * kRowsAtOnce<Tin, NV>>)
+__global__ void __launch_bounds__(128, kForwardBlocks<Tin, NV>)
 layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* __restrict__ bias,
                   Tin* y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
                   long long rows, int d, float eps) {
@@ -775,14 +775,6 @@ layer_norm_backward_wide_kernel(const Tin* __restrict__ x, const float* __restri
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        n = 148;
-    return n;
-}
-
 // Shared memory for rings, per SM; beside it each block needs its sums and barriers.
 constexpr size_t kRoom = 216 * 1024;
 
@@ -802,7 +794,7 @@ template <typename Tin>
 cudaError_t forward(const LayerNormParams& p, cudaStream_t stream) {
     const Tin* x = static_cast<const Tin*>(p.x);
     Tin* y = static_cast<Tin*>(p.y);
-    const int vecs = (p.d + kVec - 1) / kVec, sms = sm_count();
+    const int vecs = (p.d + kVec - 1) / kVec, sms = device_sms();
     // up to four rows per SM, and rows above 9216 columns: a block of up to 512 threads per row
     if (vecs > 1152 || (vecs > 128 && p.rows <= 4LL * sms)) {
         const int nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;  // at most 512 threads, to d = 16384
@@ -815,39 +807,32 @@ cudaError_t forward(const LayerNormParams& p, cudaStream_t stream) {
                                              p.eps);
         return cudaGetLastError();
     }
-    auto go = [&](auto kernel, int L, int U) {
+    auto go = [&](auto kernel, int L, int U, int blocks) {
         // few rows: one warp per block, to use more SMs
         const int threads = p.rows * L <= 128LL * sms * U ? 32 : 128;
         const long long per = (long long)threads / L * U, need = (p.rows + per - 1) / per;
-        const size_t smem = 2 * sizeof(float) * p.d;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        int blocks = 1;  // of the grid-stride pass, per SM
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem);
-        if (e != cudaSuccess) return e;
-        const unsigned grid = (unsigned)std::min<long long>(need, (long long)sms * std::max(1, blocks));
+        const size_t smem = 2 * sizeof(float) * p.d;  // 8 KB at most
+        const unsigned grid =  // as many blocks as the SMs' registers hold, grid-stride
+            (unsigned)std::min<long long>(need, (long long)sms * std::min(32, blocks * 128 / threads));
         kernel<<<grid, threads, smem, stream>>>(x, p.weight, p.bias, y, p.mean, p.rstd, p.rows, p.d,
                                                 p.eps);
         return cudaGetLastError();
     };
-    if (vecs <= 1) return go(layer_norm_kernel<Tin, 1, 1>, 1, kRowsAtOnce<Tin, 1>);
-    if (vecs <= 4) return go(layer_norm_kernel<Tin, 1, 4>, 4, kRowsAtOnce<Tin, 1>);
-    if (vecs <= 8) return go(layer_norm_kernel<Tin, 1, 8>, 8, kRowsAtOnce<Tin, 1>);
-    if (vecs <= 16) return go(layer_norm_kernel<Tin, 1, 16>, 16, kRowsAtOnce<Tin, 1>);
-    if (vecs <= 32) return go(layer_norm_kernel<Tin, 1, 32>, 32, kRowsAtOnce<Tin, 1>);
-    if (vecs <= 64) return go(layer_norm_kernel<Tin, 2, 32>, 32, kRowsAtOnce<Tin, 2>);
-    if (vecs <= 128) return go(layer_norm_kernel<Tin, 4, 32>, 32, kRowsAtOnce<Tin, 4>);
+    if (vecs <= 1) return go(layer_norm_kernel<Tin, 1, 1>, 1, kRowsAtOnce<Tin, 1>, kForwardBlocks<Tin, 1>);
+    if (vecs <= 4) return go(layer_norm_kernel<Tin, 1, 4>, 4, kRowsAtOnce<Tin, 1>, kForwardBlocks<Tin, 1>);
+    if (vecs <= 8) return go(layer_norm_kernel<Tin, 1, 8>, 8, kRowsAtOnce<Tin, 1>, kForwardBlocks<Tin, 1>);
+    if (vecs <= 16) return go(layer_norm_kernel<Tin, 1, 16>, 16, kRowsAtOnce<Tin, 1>, kForwardBlocks<Tin, 1>);
+    if (vecs <= 32) return go(layer_norm_kernel<Tin, 1, 32>, 32, kRowsAtOnce<Tin, 1>, kForwardBlocks<Tin, 1>);
+    if (vecs <= 64) return go(layer_norm_kernel<Tin, 2, 32>, 32, kRowsAtOnce<Tin, 2>, kForwardBlocks<Tin, 2>);
+    if (vecs <= 128) return go(layer_norm_kernel<Tin, 4, 32>, 32, kRowsAtOnce<Tin, 4>, kForwardBlocks<Tin, 4>);
     // teams of up to six warps, four to six vectors per thread
     const int warps = (vecs + 191) / 192, nv = (vecs + 32 * warps - 1) / (32 * warps);
     constexpr int U = kTeamRows<Tin>;
     auto kernel = nv <= 4   ? layer_norm_team_kernel<Tin, 4>
                   : nv == 5 ? layer_norm_team_kernel<Tin, 5>
                             : layer_norm_team_kernel<Tin, 6>;
-    int blocks = 1;
-    const cudaError_t e =
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, 32 * warps, 0);
-    if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::min<long long>((p.rows + U - 1) / U, (long long)sms * std::max(1, blocks));
+    const unsigned grid =  // at most 85 registers a thread: 768 threads per SM, grid-stride
+        (unsigned)std::min<long long>((p.rows + U - 1) / U, (long long)sms * (768 / (32 * warps)));
     kernel<<<grid, 32 * warps, 0, stream>>>(x, p.weight, p.bias, y, p.mean, p.rstd, p.rows, p.d, p.eps);
     return cudaGetLastError();
 }
@@ -865,13 +850,13 @@ struct BackwardPlan {
         if (narrow) {
             L = vecs <= 1 ? 1 : vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
             const long long per = (long long)kNarrowThreads / L * kNarrowRows;
-            grid = (unsigned)std::min<long long>((p.rows + per - 1) / per, (long long)sm_count() * 4);
+            grid = (unsigned)std::min<long long>((p.rows + per - 1) / per, (long long)device_sms() * 4);
             return;
         }
         wide = p.d > kRingMaxD || RingShape(2 * sizeof(Tin) * p.d, 1, 2).stages < 2;
         if (wide) {  // slices of rows, for two blocks per SM
             const long long across = (vecs + 127) / 128;
-            grid = (unsigned)std::min<long long>(p.rows, std::max<long long>(1, 2 * sm_count() / across));
+            grid = (unsigned)std::min<long long>(p.rows, std::max<long long>(1, 2 * device_sms() / across));
             return;
         }
         // threads of 8 columns up to 768 of them, then 512 of up to 32; two slots of the most rows
@@ -886,7 +871,7 @@ struct BackwardPlan {
         const long long groups = (p.rows + group_rows - 1) / group_rows;
         const long long blocks = std::max<long long>(
             1, std::min<long long>((long long)(kRoom / (smem + 2048)), 1024 / threads));
-        grid = (unsigned)std::min<long long>(groups, blocks * sm_count());
+        grid = (unsigned)std::min<long long>(groups, blocks * device_sms());
     }
 };
 
@@ -913,7 +898,7 @@ cudaError_t backward(const LayerNormGrads& p, const BackwardPlan<Tin>& plan, flo
     if (plan.wide) {
         const dim3 grid((unsigned)((p.d + 128 * kVec - 1) / (128 * kVec)), plan.grid);
         layer_norm_columns_kernel<Tin><<<grid, 128, 0, stream>>>(x, p.mean, p.rstd, dy, part, p.rows, p.d);
-        layer_norm_backward_wide_kernel<Tin><<<(unsigned)std::min<long long>(p.rows, 2LL * sm_count()),
+        layer_norm_backward_wide_kernel<Tin><<<(unsigned)std::min<long long>(p.rows, 2LL * device_sms()),
                                                1024, 0, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx,
                                                                   p.rows, p.d);
         return cudaGetLastError();
@@ -922,8 +907,7 @@ cudaError_t backward(const LayerNormGrads& p, const BackwardPlan<Tin>& plan, flo
                   : plan.nv == 4 ? layer_norm_backward_kernel<Tin, 4, 512>
                   : plan.threads <= 512 ? layer_norm_backward_kernel<Tin, 1, 512>
                                         : layer_norm_backward_kernel<Tin, 1, 768>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)plan.smem);
+    const cudaError_t e = allow_smem((const void*)kernel, plan.smem);
     if (e != cudaSuccess) return e;
     kernel<<<plan.grid, plan.threads, plan.smem, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx, part,
                                                            p.rows, p.d, plan.stages, plan.group_rows);

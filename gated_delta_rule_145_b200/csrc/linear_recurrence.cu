@@ -10,6 +10,7 @@
 // Both are bound by memory: forward reads x, a, b and writes h, backward reads x, a, b, h
 // and dout and writes dx, da, db, each once.
 #include <algorithm>
+#include <atomic>
 
 #include "gdr_common.cuh"
 #include "gdr_internal.h"
@@ -729,14 +730,6 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
 // Rows of CTAs of the sequential form: the partial sums have one row each.
 int seq_rows(int nseq) { return std::min(nseq, 64); }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        n = 148;
-    return n;
-}
-
 // The tokens of a call's mean sequence; the host does not know packed sequences' lengths.
 int mean_length(const RecurrenceParams& p) {
     return p.cu_seqlens ? (p.T + p.nseq - 1) / p.nseq : p.T;
@@ -758,34 +751,47 @@ template <typename Kernel>
 cudaError_t cluster_of(Kernel kernel, int threads, size_t smem, long long units, int tiles, int* K) {
     *K = 1;
     const int most = (int)std::min<long long>({(long long)kMaxCluster, (long long)tiles,
-                                               sm_count() / units});
+                                               device_sms() / units});
     if (most < 2) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    for (int k = most; e == cudaSuccess && k > 1; --k) {
-        cudaLaunchAttribute attr = {};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = (unsigned)k;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(units * k));
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int fit = 0;
-        e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
-        if (e == cudaSuccess && fit >= units) {
+    // clusters of k CTAs that the current device holds at once; asked once per kernel and device
+    struct Held {
+        std::atomic<int> fit[kMaxCluster + 1];
+    };
+    static Held held[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+    if (e != cudaSuccess) return e;
+    for (int k = most; k > 1; --k) {
+        int fit = held[dev].fit[k].load();
+        if (fit == 0) {
+            cudaLaunchAttribute attr = {};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)k;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)k);
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = allow_smem((const void*)kernel, smem);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+            held[dev].fit[k].store(std::max(fit, 1));
+        }
+        if (fit >= units) {
             *K = k;
             break;
         }
     }
-    return e;
+    return cudaSuccess;
 }
 
 template <typename Kernel, typename... Args>
 cudaError_t launch_tiles(Kernel kernel, long long grid, int threads, int K, size_t smem,
                          cudaStream_t stream, Args... args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem((const void*)kernel, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);

@@ -370,14 +370,6 @@ gated_rmsnorm_backward_kernel(NormGrads p, float* part) {
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        n = 148;
-    return n;
-}
-
 template <typename Tz>
 cudaError_t norm_backward(const NormGrads& p, unsigned grid, float* part, cudaStream_t stream) {
     switch (p.d) {
@@ -406,7 +398,7 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
     // Segments: for one to eight waves of CTAs, the most segments that they hold, and of these
     // the number that takes the fewest token steps (a segment costs some 24 beside its own).
     const int nct = (p.C + kGCh - 1) / kGCh;
-    const long long slots = 2LL * sm_count();
+    const long long slots = 2LL * device_sms();
     int seg = 0, nseg = 0;
     long long best = 0;
     for (int waves = 1; waves <= 8; ++waves) {
@@ -423,8 +415,7 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * groups * 5 * p.C, stream);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(conv_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(ConvBackwardSmem));
+    e = allow_smem((const void*)conv_backward_kernel, sizeof(ConvBackwardSmem));
     if (e == cudaSuccess) {
         conv_backward_kernel<<<(unsigned)(groups * nct), 32 * kGWarps, sizeof(ConvBackwardSmem),
                                stream>>>(p, nct, nseg, seg, part);
@@ -439,7 +430,7 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
 cudaError_t launch_gated_rmsnorm_backward(const NormGrads& p, cudaStream_t stream) {
     if (p.rows == 0) return launch_column_sum(nullptr, 0, p.d, p.grad_weight, p.d, nullptr, stream);
     const long long rpb = kNThreads / (p.d / 4);
-    const unsigned grid = (unsigned)std::min<long long>((p.rows + rpb - 1) / rpb, (long long)sm_count() * 8);
+    const unsigned grid = (unsigned)std::min<long long>((p.rows + rpb - 1) / rpb, (long long)device_sms() * 8);
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * grid * p.d, stream);
     if (e != cudaSuccess) return e;

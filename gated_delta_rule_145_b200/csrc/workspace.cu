@@ -4,6 +4,7 @@
 // (64-token block, value head) in a workspace: taken per call from a private
 // stream-ordered pool of the current device (this file), or from a caller's memory
 // (the no-allocation and host-buffer entry points).
+#include <atomic>
 #include <mutex>
 
 #include "gdr_internal.h"
@@ -29,6 +30,45 @@ bool tc_shape(const FwdParams& p) {
 }
 
 }  // namespace
+
+int device_sms() {
+    static std::atomic<int> counts[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    n = counts[dev].load();
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            return 148;
+        counts[dev].store(n);
+    }
+    return n;
+}
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;  // every kernel's from the start
+    struct Entry {
+        int dev;
+        const void* kernel;
+        size_t bytes;
+    };
+    constexpr int kEntries = 256;  // beyond them the runtime is asked every time
+    static std::mutex mu;
+    static Entry table[kEntries];
+    static int used = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    Entry* at = nullptr;
+    for (int i = 0; i < used && !at; ++i)
+        if (table[i].kernel == kernel && table[i].dev == dev) at = &table[i];
+    if (at && at->bytes >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    if (!at && used < kEntries) at = &table[used++];
+    if (at) *at = {dev, kernel, bytes};
+    return cudaSuccess;
+}
 
 cudaError_t workspace_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
     int dev = 0;
