@@ -240,14 +240,17 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
 // W does not.  A factor below 2^-0.5 acts as P itself: there S + W S would cancel, and a
 // large forgotten state would leave its rounding error in a small new one.
 constexpr int kStrip = 64;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 12;  // above 8 where the device allows it
 
 // Shared memory of a CTA: per slot the x, a, b tiles, and for the backward pass dout's.
-template <typename Tin_, int WARPS_, int TOK_, int STAGES_, bool Grad>
+// PEERS: CTAs per cluster at most (1: none); Pipe: a step's exchange overlaps the next step's
+// tile, at the price of both steps' tokens in registers.
+template <typename Tin_, int WARPS_, int TOK_, int STAGES_, int PEERS_, bool Pipe_, bool Grad>
 struct alignas(128) TileSmem {
     using Tin = Tin_;
     static constexpr int WARPS = WARPS_, TOK = TOK_, STAGES = STAGES_, kRows = WARPS * TOK;
-    static_assert(WARPS >= kMaxCluster, "warp w sends to peer w");
+    static constexpr int PEERS = PEERS_;
+    static constexpr bool Cluster = PEERS > 1, Pipe = Pipe_;
     struct alignas(128) Slot {
         Tin in[3][kRows][kStrip];
         float dout[Grad ? kRows : 1][Grad ? kStrip : 4];
@@ -258,8 +261,9 @@ struct alignas(128) TileSmem {
     // The cluster's tiles: coded factor pair, H pair; by step modulo 4.  A CTA publishes step
     // s + 4 only once it has every peer's step s + 2, which a peer publishes after all its
     // warps are done with step s: nothing still unread is overwritten.
-    float4 peer[4][kMaxCluster][32];
+    float4 peer[4][PEERS][32];
     uint64_t full[STAGES], peers_in[4];
+    int ticket;
 };
 
 // The factor 2^y, y <= 0, coded for carry(): for y > -0.5, W = expm1(y ln 2) with its sign
@@ -340,6 +344,7 @@ __device__ __noinline__ void wait_in_flight(uint64_t* full, int stages, int issu
 struct Joined {
     float2 P, H;
     float4 all;
+    int step;
 };
 
 // Composes the warps' pairs in sm.part (after the barrier behind their stores) and, in a
@@ -360,6 +365,7 @@ __device__ __forceinline__ Joined publish(Smem& sm, int step, int warp, int lane
         G = __fadd2_rn(G, sm.log_part[buf][w][lane]);
     }
     Joined j;
+    j.step = step;
     j.P = ex2f2(Gp);
     j.H = Hp;
     j.all = make_float4(code_factor(G.x), code_factor(G.y), H.x, H.y);
@@ -367,15 +373,17 @@ __device__ __forceinline__ Joined publish(Smem& sm, int step, int warp, int lane
         uint64_t* bar = &sm.peers_in[step & 3];
         const uint32_t K = cluster_size();
         if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(bar, K * (uint32_t)sizeof(sm.peer[0][0]));
-        if (warp < K) store_peer(&sm.peer[step & 3][cluster_rank()][lane], bar, warp, j.all);
+        for (uint32_t k = warp; k < K; k += Smem::WARPS)
+            store_peer(&sm.peer[step & 3][cluster_rank()][lane], bar, k, j.all);
     }
     return j;
 }
 
 // The state before this warp's tokens of the step; S moves from before the step to behind it.
 template <bool Cluster, typename Smem>
-__device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int step, int lane,
-                                              float2& S, bool& dead) {
+__device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int lane, float2& S,
+                                              bool& dead) {
+    const int step = j.step;
     float2 in = S;
     if constexpr (Cluster) {
         if (!dead && !tc::mbar_wait(&sm.peers_in[step & 3], (uint32_t)(step >> 2) & 1u)) {
@@ -395,20 +403,96 @@ __device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int ste
     return __ffma2_rn(j.P, in, j.H);
 }
 
-// What the CTAs of both tiled kernels share: their place, their tokens, their barriers.
+// How a grid's clusters share the units' steps.  Plain (span == 0): cluster i takes unit i from end
+// to end.  Split: the units' steps, all of one number, are laid end to end and cluster i takes
+// `span` of them, at least a unit's; a unit cut by the border between i and i + 1 has its
+// first steps in i and the rest in i + 1.  Every cluster takes its units from the last to
+// the first, so it starts with the first steps of a cut unit, which wait for nothing, and
+// ends with the last steps of another, whose state the cluster before it handed over long
+// ago.  No SM idles for want of whole units: 96 units on 74 clusters of two.  Clusters are
+// numbered in the order in which they start, so the one waited for always runs.
+struct Schedule {
+    int span, steps, total;
+    int* ticket;       // clusters started; zero at launch
+    uint32_t* ready;   // [clusters], zero at launch: states[i] is there
+    float* states;     // [clusters][kStrip]
+};
+
+// A unit's part: steps [s0, s1) of `steps`.
+struct Part {
+    int unit, s0, s1;
+};
+struct Parts {
+    int first, last, lo, hi, index;
+};
+template <bool Cluster, typename Smem>
+__device__ __forceinline__ Parts parts_of(Smem& sm, const Schedule& s) {
+    Parts p;
+    p.lo = p.hi = 0;
+    p.index = blockIdx.x / (Cluster ? (int)cluster_size() : 1);
+    p.first = p.last = p.index;
+    if (Cluster && s.span) {
+        uint32_t a;  // rank 0 drew it
+        int t;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_u32(&sm.ticket)));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(t) : "r"(a) : "memory");
+        p.index = t;
+        p.lo = t * s.span;
+        p.hi = min(s.total, p.lo + s.span);
+        p.first = p.lo / s.steps;
+        p.last = p.lo < p.hi ? (p.hi - 1) / s.steps : p.first - 1;
+    }
+    return p;
+}
+template <bool Cluster>
+__device__ __forceinline__ Part part_of(const Parts& p, const Schedule& s, int unit, int steps) {
+    if (!Cluster || !s.span) return {unit, 0, steps};
+    return {unit, max(0, p.lo - unit * s.steps), min(s.steps, p.hi - unit * s.steps)};
+}
+
+// Hands the state behind a cut unit's first steps to the next cluster (one warp) ...
+__device__ __forceinline__ void hand_over(const Schedule& s, int index, int lane, float2 S) {
+    __stcg(reinterpret_cast<float2*>(s.states + (size_t)index * kStrip + 2 * lane), S);
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) asm volatile("st.release.gpu.u32 [%0], %1;" ::"l"(s.ready + index), "r"(1u) : "memory");
+}
+// ... and takes it there (every warp); false if it did not come within the wait's limit.
+__device__ __noinline__ bool wait_ready(const uint32_t* flag) {
+    const uint64_t t0 = tc::globaltimer();
+    for (;;) {
+        uint32_t v;
+        asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+        if (v) return true;
+        if (tc::globaltimer() - t0 > tc::kWaitLimitNs) return false;
+        __nanosleep(100);
+    }
+}
+__device__ __forceinline__ float2 take_over(const Schedule& s, int index, int lane, bool& dead) {
+    int ok = 1;
+    if (lane == 0 && !dead) ok = wait_ready(s.ready + index);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) {
+        dead = true;
+        if (lane == 0) atomicExch(&g_recurrence_status, 1);
+    }
+    __syncwarp();
+    return __ldcg(reinterpret_cast<const float2*>(s.states + (size_t)index * kStrip + 2 * lane));
+}
+
+// What the CTAs of both tiled kernels share: their place in a unit, and its tokens.
 struct Place {
     int warp, lane, K, rank, seq, c0, c, tiles, steps;
     long long t0, t1;
     bool in_c;
 };
 template <bool Cluster>
-__device__ __forceinline__ Place place_of(const RecurrenceParams& p, int strips, int rows) {
+__device__ __forceinline__ Place place_of(const RecurrenceParams& p, int unit, int strips, int rows) {
     Place w;
     w.warp = threadIdx.x / 32;
     w.lane = threadIdx.x % 32;
     w.K = Cluster ? (int)cluster_size() : 1;
     w.rank = Cluster ? (int)cluster_rank() : 0;
-    const int unit = blockIdx.x / w.K;
     w.seq = unit / strips;
     w.c0 = unit % strips * kStrip;
     w.c = w.c0 + 2 * w.lane;
@@ -418,137 +502,157 @@ __device__ __forceinline__ Place place_of(const RecurrenceParams& p, int strips,
     w.steps = (w.tiles + w.K - 1) / w.K;
     return w;
 }
+// One thread: barriers, and the cluster's number where it is drawn.
 template <typename Smem>
-__device__ __forceinline__ void init_barriers(Smem& sm) {
+__device__ __forceinline__ void init_cta(Smem& sm, const Schedule& s, int rank) {
     for (int i = 0; i < Smem::STAGES; ++i) tc::mbar_init(&sm.full[i], 1);
     for (int i = 0; i < 4; ++i) tc::mbar_init(&sm.peers_in[i], 1);
     tc::mbar_init_fence();
+    if (Smem::Cluster && s.span && rank == 0) sm.ticket = atomicAdd(s.ticket, 1);
 }
 
-template <typename Smem, int Blocks, bool Cluster>
+template <typename Smem, int Blocks>
 __global__ void __launch_bounds__(32 * Smem::WARPS, Blocks)
-recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, int strips) {
+recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, int strips,
+                       Schedule sched) {
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
+    constexpr bool Cluster = Smem::Cluster;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-    const Place w = place_of<Cluster>(p, strips, kRows);
-    Channels ch = {};
-    if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
-    const size_t at = (size_t)w.seq * p.C + w.c;
-    float2 S = w.in_c && p.init_state ? *reinterpret_cast<const float2*>(p.init_state + at)
-                                      : make_float2(0.f, 0.f);
-    int issued = 0;
-    if (threadIdx.x == 0) {
-        init_barriers(sm);
-        for (; issued < STAGES && issued * w.K + w.rank < w.tiles; ++issued)
-            load_tile<false>(sm, issued, maps, w.c0,
-                             (int)(w.t0 + (long long)(issued * w.K + w.rank) * kRows));
-    }
-    // the barriers are set up; in a cluster, every CTA has started and has read its state
+    if (threadIdx.x == 0) init_cta(sm, sched, Cluster ? (int)cluster_rank() : 0);
+    // the barriers are set up; in a cluster, every CTA has started
     if constexpr (Cluster) cluster_barrier(); else __syncthreads();
-    bool dead = false;
+    const Parts parts = parts_of<Cluster>(sm, sched);
     struct Held {
         float2 lam[TOK], u[TOK];
         Joined j;
     };
-    // tokens of this warp in a step: the first one, and how many are within the sequence
-    auto first_of = [&](int step) {
-        return w.t0 + (long long)(step * w.K + w.rank) * kRows + w.warp * TOK;
-    };
-    auto live_of = [&](long long first) { return (int)min((long long)TOK, max(0LL, w.t1 - first)); };
-    // the run from zero, up to the exchange
-    auto read_tile = [&](int step, Held& k) {
-        const int st = step % STAGES, buf = step & 1, live = live_of(first_of(step));
-        if (step * w.K + w.rank < w.tiles && !dead &&
-            !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
-            dead = true;
-            if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
-        }
-        __syncwarp();
-        float2 G = make_float2(0.f, 0.f), H = G;
-        const auto* row = &sm.slot[st].in[0][w.warp * TOK][2 * w.lane];
-        auto gates = [&](int i) {
-            const float2 xv = smem_pair(row + i * kStrip);
-            const float2 av = smem_pair(row + (kRows + i) * kStrip);
-            const float2 bv = smem_pair(row + (2 * kRows + i) * kStrip);
-            const float2 y = decay_gate(av, ch).y;
-            k.lam[i] = ex2f2(y);
-            k.u[i] = gated_input(xv, bv);
-            G = __fadd2_rn(G, y);
-            H = __ffma2_rn(k.lam[i], H, k.u[i]);
+    bool dead = false;
+    int issued = 0, taken = 0, turn = 0;  // tiles copied, tiles waited for, steps begun
+    for (int unit = parts.last; unit >= parts.first; --unit) {  // without a cluster: once
+        const Place w = place_of<Cluster>(p, Cluster ? unit : (int)blockIdx.x, strips, kRows);
+        const Part part = part_of<Cluster>(parts, sched, unit, w.steps);
+        Channels ch = {};
+        if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
+        const size_t at = (size_t)w.seq * p.C + w.c;
+        float2 S = w.in_c && p.init_state && part.s0 == 0
+                       ? *reinterpret_cast<const float2*>(p.init_state + at)
+                       : make_float2(0.f, 0.f);
+        // tokens of this warp in a step: the first one, and how many are within the sequence
+        auto first_of = [&](int step) {
+            return w.t0 + (long long)(step * w.K + w.rank) * kRows + w.warp * TOK;
         };
-        if (live == TOK) {
-#pragma unroll
-            for (int i = 0; i < TOK; ++i) gates(i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < TOK; ++i) {
-                if (i < live) {
-                    gates(i);
-                } else {
-                    k.lam[i] = make_float2(1.f, 1.f);
-                    k.u[i] = make_float2(0.f, 0.f);
-                }
-            }
-        }
-        sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
-        sm.log_part[buf][w.warp][w.lane] = G;
-        __syncthreads();
-        // every warp has read the tile: its slot takes the tile STAGES steps ahead
-        if (threadIdx.x == 0 && !dead && issued * w.K + w.rank < w.tiles) {
-            load_tile<false>(sm, st, maps, w.c0,
-                             (int)(w.t0 + (long long)(issued * w.K + w.rank) * kRows));
+        auto live_of = [&](long long first) {
+            return (int)min((long long)TOK, max(0LL, w.t1 - first));
+        };
+        int to_load = part.s0;  // one thread: the step whose tile is copied next
+        auto load_next = [&]() {
+            const int tile = to_load * w.K + w.rank;
+            if (to_load >= part.s1 || tile >= w.tiles) return;
+            load_tile<false>(sm, issued % STAGES, maps, w.c0, (int)(w.t0 + (long long)tile * kRows));
+            ++to_load;
             ++issued;
-        }
-        k.j = publish<Cluster>(sm, step, w.warp, w.lane);
-    };
-    // the run from the true start state
-    auto write_tile = [&](int step, const Held& k) {
-        float2 h = start_state<Cluster>(sm, k.j, step, w.lane, S, dead);
-        const long long first = first_of(step);
-        const int live = live_of(first);
-        float* out = p.out + first * p.C + w.c;
-        if (w.in_c) {
+        };
+        if (Cluster) __syncthreads();  // the part before is done with its tiles
+        if (threadIdx.x == 0 && !dead)
+            for (int i = 0; i < STAGES; ++i) load_next();
+        // the run from zero, up to the exchange
+        auto read_tile = [&](int step, Held& k) {
+            const int st = taken % STAGES, buf = turn & 1, live = live_of(first_of(step));
+            if (step * w.K + w.rank < w.tiles) {
+                if (!dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(taken / STAGES) & 1u)) {
+                    dead = true;
+                    if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
+                }
+                ++taken;
+            }
+            __syncwarp();
+            float2 G = make_float2(0.f, 0.f), H = G;
+            const auto* row = &sm.slot[st].in[0][w.warp * TOK][2 * w.lane];
+            auto gates = [&](int i) {
+                const float2 xv = smem_pair(row + i * kStrip);
+                const float2 av = smem_pair(row + (kRows + i) * kStrip);
+                const float2 bv = smem_pair(row + (2 * kRows + i) * kStrip);
+                const float2 y = decay_gate(av, ch).y;
+                k.lam[i] = ex2f2(y);
+                k.u[i] = gated_input(xv, bv);
+                G = __fadd2_rn(G, y);
+                H = __ffma2_rn(k.lam[i], H, k.u[i]);
+            };
             if (live == TOK) {
 #pragma unroll
-                for (int i = 0; i < TOK; ++i) {
-                    h = __ffma2_rn(k.lam[i], h, k.u[i]);
-                    store_pair(out + (size_t)i * p.C, h);
-                }
+                for (int i = 0; i < TOK; ++i) gates(i);
             } else {
 #pragma unroll
                 for (int i = 0; i < TOK; ++i) {
-                    h = __ffma2_rn(k.lam[i], h, k.u[i]);
-                    if (i < live) store_pair(out + (size_t)i * p.C, h);
+                    if (i < live) {
+                        gates(i);
+                    } else {
+                        k.lam[i] = make_float2(1.f, 1.f);
+                        k.u[i] = make_float2(0.f, 0.f);
+                    }
                 }
             }
-            // the warp with the sequence's last token: its h, so that the two agree
-            if (live > 0 && first + live == w.t1 && p.final_state)
-                *reinterpret_cast<float2*>(p.final_state + at) = h;
-        }
-        __syncwarp();
-    };
-    if constexpr (Cluster) {
-        // a step's exchange runs while the next step's tile is read
-        Held even, odd;
-        if (w.steps > 0) read_tile(0, even);
-        for (int step = 0; step < w.steps; step += 2) {
-            if (step + 1 < w.steps) read_tile(step + 1, odd);
-            write_tile(step, even);
-            if (step + 1 < w.steps) {
-                if (step + 2 < w.steps) read_tile(step + 2, even);
-                write_tile(step + 1, odd);
+            sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
+            sm.log_part[buf][w.warp][w.lane] = G;
+            __syncthreads();
+            // every warp has read the tile: its slot takes another
+            if (threadIdx.x == 0 && !dead) load_next();
+            k.j = publish<Cluster>(sm, turn++, w.warp, w.lane);
+        };
+        // the run from the true start state
+        auto write_tile = [&](int step, const Held& k) {
+            float2 h = start_state<Cluster>(sm, k.j, w.lane, S, dead);
+            const long long first = first_of(step);
+            const int live = live_of(first);
+            float* out = p.out + first * p.C + w.c;
+            if (w.in_c) {
+                if (live == TOK) {
+#pragma unroll
+                    for (int i = 0; i < TOK; ++i) {
+                        h = __ffma2_rn(k.lam[i], h, k.u[i]);
+                        store_pair(out + (size_t)i * p.C, h);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < TOK; ++i) {
+                        h = __ffma2_rn(k.lam[i], h, k.u[i]);
+                        if (i < live) store_pair(out + (size_t)i * p.C, h);
+                    }
+                }
+                // the warp with the sequence's last token: its h, so that the two agree
+                if (live > 0 && first + live == w.t1 && p.final_state)
+                    *reinterpret_cast<float2*>(p.final_state + at) = h;
+            }
+            __syncwarp();
+        };
+        if constexpr (Smem::Pipe) {
+            // a step's exchange runs while the next step's tile is read
+            Held even, odd;
+            if (part.s0 < part.s1) read_tile(part.s0, even);
+            if (part.s0 > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
+            for (int step = part.s0; step < part.s1; step += 2) {
+                if (step + 1 < part.s1) read_tile(step + 1, odd);
+                write_tile(step, even);
+                if (step + 1 < part.s1) {
+                    if (step + 2 < part.s1) read_tile(step + 2, even);
+                    write_tile(step + 1, odd);
+                }
+            }
+        } else {
+            Held k;
+            for (int step = part.s0; step < part.s1; ++step) {
+                read_tile(step, k);
+                if (Cluster && step == part.s0 && step > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
+                write_tile(step, k);
             }
         }
-    } else {
-        Held k;
-        for (int step = 0; step < w.steps; ++step) {
-            read_tile(step, k);
-            write_tile(step, k);
-        }
+        if (Cluster && part.s1 < w.steps && w.rank == 0 && w.warp == 0)
+            hand_over(sched, parts.index, w.lane, S);
+        if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && p.final_state)
+            *reinterpret_cast<float2*>(p.final_state + at) = S;
+        if (!Cluster) break;
     }
-    if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && p.final_state)
-        *reinterpret_cast<float2*>(p.final_state + at) = S;
     if (dead && threadIdx.x == 0) wait_in_flight(sm.full, STAGES, issued);
     // no CTA leaves while a peer may still store to it
     if constexpr (Cluster) cluster_barrier();
@@ -559,169 +663,194 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
 // warp's pair is (P, H) of E.  Tiles are counted from the sequence's end.  Everything that
 // multiplies D is formed while the tile is read, so that the second run over a warp's tokens,
 // after the join, is short.  h comes by plain loads, one step ahead.
-// part [units * K][2 C]: each CTA's sums for A_log and dt_bias.
-template <typename Smem, int Blocks, bool Cluster>
+// partial [rows][2 C]: each CTA's sums for A_log and dt_bias, one row per (sequence, rank), and
+// under a split schedule as many rows again for the units' later parts.
+template <typename Smem, int Blocks>
 __global__ void __launch_bounds__(32 * Smem::WARPS, Blocks)
 recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrenceParams p,
-                                RecurrenceGrads r, float* part, int strips) {
+                                RecurrenceGrads r, float* partial, int strips, Schedule sched) {
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
+    constexpr bool Cluster = Smem::Cluster;
     using Tin = typename Smem::Tin;
     // steps after which a tile's dout is no longer needed: the exchange takes one of two
-    constexpr int kHeld = Cluster ? 2 : 1;
+    constexpr int kHeld = Smem::Pipe ? 2 : 1;
     static_assert(STAGES > kHeld, "a slot has to be free for the next tile");
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-    const Place w = place_of<Cluster>(p, strips, kRows);
-    Channels ch = {};
-    if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
-    const size_t at = (size_t)w.seq * p.C + w.c;
-    const float2 zero = make_float2(0.f, 0.f);
-    float2 S = w.in_c && r.grad_final ? *reinterpret_cast<const float2*>(r.grad_final + at) : zero;
-    int issued = 0;
-    // a sequence's first tile may start before it, at a negative row even
-    auto first_row = [&](int step) {
-        return (int)(w.t1 - (long long)(step * w.K + w.rank + 1) * kRows);
-    };
-    if (threadIdx.x == 0) {
-        init_barriers(sm);
-        for (; issued < STAGES && issued * w.K + w.rank < w.tiles; ++issued)
-            load_tile<true>(sm, issued, maps, w.c0, first_row(issued));
-    }
-    // the states before a step's tokens of this warp: last, last - 1, ...
-    float2 prev[TOK];
-    auto load_prev = [&](int step) {
-        const long long last = w.t1 - (long long)(step * w.K + w.rank) * kRows - w.warp * TOK - 1;
-        const float* h = p.out + (last - 1) * p.C + w.c;
-        if (last - TOK >= w.t0 && w.in_c) {
-#pragma unroll
-            for (int i = 0; i < TOK; ++i) prev[i] = load_pair(h - (size_t)i * p.C);
-        } else {
-#pragma unroll
-            for (int i = 0; i < TOK; ++i) {
-                prev[i] = zero;
-                if (w.in_c && last - i > w.t0) prev[i] = load_pair(h - (size_t)i * p.C);
-                if (w.in_c && last - i == w.t0 && p.init_state)
-                    prev[i] = *reinterpret_cast<const float2*>(p.init_state + at);
-            }
-        }
-    };
-    load_prev(0);
+    if (threadIdx.x == 0) init_cta(sm, sched, Cluster ? (int)cluster_rank() : 0);
     if constexpr (Cluster) cluster_barrier(); else __syncthreads();
-    float2 acc_A = zero, acc_bias = zero;
-    bool dead = false;
+    const Parts parts = parts_of<Cluster>(sm, sched);
+    const float2 zero = make_float2(0.f, 0.f);
     struct Held {
         GradFactors f[TOK];
         Joined j;
+        int slot;
     };
-    auto last_of = [&](int step) {
-        return w.t1 - (long long)(step * w.K + w.rank) * kRows - w.warp * TOK - 1;
-    };
-    auto live_of = [&](long long last) {
-        return (int)min((long long)TOK, max(0LL, last + 1 - w.t0));
-    };
-    auto read_tile = [&](int step, Held& k) {
-        const int st = step % STAGES, buf = step & 1, live = live_of(last_of(step));
-        if (step * w.K + w.rank < w.tiles && !dead &&
-            !tc::mbar_wait(&sm.full[st], (uint32_t)(step / STAGES) & 1u)) {
-            dead = true;
-            if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
-        }
-        __syncwarp();
-        float2 G = zero, H = zero;
-        const auto* row = &sm.slot[st].in[0][kRows - 1 - w.warp * TOK][2 * w.lane];
-        const float* dout = &sm.slot[st].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
-        auto gates = [&](int i) {
-            float2 y;
-            k.f[i] = grad_factors(smem_pair(row - i * kStrip), smem_pair(row + (kRows - i) * kStrip),
-                                  smem_pair(row + (2 * kRows - i) * kStrip), prev[i], ch, y);
-            G = __fadd2_rn(G, y);
-            H = __fmul2_rn(k.f[i].lam, __fadd2_rn(smem_pair(dout - i * kStrip), H));
+    bool dead = false;
+    int issued = 0, taken = 0, turn = 0;  // tiles copied, tiles waited for, steps begun
+    for (int unit = parts.last; unit >= parts.first; --unit) {  // without a cluster: once
+        const Place w = place_of<Cluster>(p, Cluster ? unit : (int)blockIdx.x, strips, kRows);
+        const Part part = part_of<Cluster>(parts, sched, unit, w.steps);
+        Channels ch = {};
+        if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
+        const size_t at = (size_t)w.seq * p.C + w.c;
+        float2 S = w.in_c && r.grad_final && part.s0 == 0
+                       ? *reinterpret_cast<const float2*>(r.grad_final + at) : zero;
+        auto last_of = [&](int step) {
+            return w.t1 - (long long)(step * w.K + w.rank) * kRows - w.warp * TOK - 1;
         };
-        if (live == TOK) {
-#pragma unroll
-            for (int i = 0; i < TOK; ++i) gates(i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < TOK; ++i) {
-                if (i < live) gates(i);
-            }
-        }
-        if (step + 1 < w.steps) load_prev(step + 1);
-        sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
-        sm.log_part[buf][w.warp][w.lane] = G;
-        __syncthreads();
-        // every warp is done with step - kHeld: its slot takes the tile STAGES steps later
-        if (threadIdx.x == 0 && !dead && step >= kHeld && issued * w.K + w.rank < w.tiles) {
-            load_tile<true>(sm, issued % STAGES, maps, w.c0, first_row(issued));
+        auto live_of = [&](long long last) {
+            return (int)min((long long)TOK, max(0LL, last + 1 - w.t0));
+        };
+        int to_load = part.s0;  // one thread: the step whose tile is copied next
+        auto load_next = [&]() {
+            const int tile = to_load * w.K + w.rank;
+            if (to_load >= part.s1 || tile >= w.tiles) return;
+            // a sequence's first tile may start before it, at a negative row even
+            load_tile<true>(sm, issued % STAGES, maps, w.c0,
+                            (int)(w.t1 - (long long)(tile + 1) * kRows));
+            ++to_load;
             ++issued;
-        }
-        k.j = publish<Cluster>(sm, step, w.warp, w.lane);
-    };
-    auto write_tile = [&](int step, const Held& k) {
-        float2 E = start_state<Cluster>(sm, k.j, step, w.lane, S, dead);
-        const long long last = last_of(step);
-        const int live = live_of(last);
-        const float* dout =
-            &sm.slot[step % STAGES].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
-        if (w.in_c) {
-            Tin* dx = static_cast<Tin*>(r.grad_x) + last * r.ld_grad + w.c;
-            Tin* da = static_cast<Tin*>(r.grad_a) + last * r.ld_grad + w.c;
-            Tin* db = static_cast<Tin*>(r.grad_b) + last * r.ld_grad + w.c;
-            auto token = [&](int i) {
-                const float2 D = __fadd2_rn(smem_pair(dout - i * kStrip), E);
-                const long long o = i * r.ld_grad;
-                store_grads(k.f[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
-                E = __fmul2_rn(k.f[i].lam, D);
-            };
-            if (live == TOK) {
+        };
+        if (Cluster) __syncthreads();  // the part before is done with its tiles
+        if (threadIdx.x == 0 && !dead)
+            for (int i = 0; i < STAGES; ++i) load_next();
+        // the states before a step's tokens of this warp: last, last - 1, ...
+        float2 prev[TOK];
+        auto load_prev = [&](int step) {
+            const long long last = last_of(step);
+            const float* h = p.out + (last - 1) * p.C + w.c;
+            if (last - TOK >= w.t0 && w.in_c) {
 #pragma unroll
-                for (int i = 0; i < TOK; ++i) token(i);
+                for (int i = 0; i < TOK; ++i) prev[i] = load_pair(h - (size_t)i * p.C);
             } else {
 #pragma unroll
                 for (int i = 0; i < TOK; ++i) {
-                    if (i < live) token(i);
+                    prev[i] = zero;
+                    if (w.in_c && last - i > w.t0) prev[i] = load_pair(h - (size_t)i * p.C);
+                    if (w.in_c && last - i == w.t0 && p.init_state)
+                        prev[i] = *reinterpret_cast<const float2*>(p.init_state + at);
                 }
             }
-            // the warp with the sequence's first token
-            if (live > 0 && last + 1 - live == w.t0 && r.grad_init)
-                *reinterpret_cast<float2*>(r.grad_init + at) = E;
-        }
-        __syncwarp();
-    };
-    if constexpr (Cluster) {
-        // a step's exchange runs while the next step's tile is read
-        Held even, odd;
-        if (w.steps > 0) read_tile(0, even);
-        for (int step = 0; step < w.steps; step += 2) {
-            if (step + 1 < w.steps) read_tile(step + 1, odd);
-            write_tile(step, even);
-            if (step + 1 < w.steps) {
-                if (step + 2 < w.steps) read_tile(step + 2, even);
-                write_tile(step + 1, odd);
+        };
+        if (part.s0 < part.s1) load_prev(part.s0);
+        float2 acc_A = zero, acc_bias = zero;
+        auto read_tile = [&](int step, Held& k) {
+            const int st = taken % STAGES, buf = turn & 1, live = live_of(last_of(step));
+            k.slot = st;
+            if (step * w.K + w.rank < w.tiles) {
+                if (!dead && !tc::mbar_wait(&sm.full[st], (uint32_t)(taken / STAGES) & 1u)) {
+                    dead = true;
+                    if (w.lane == 0) atomicExch(&g_recurrence_status, 1);
+                }
+                ++taken;
+            }
+            __syncwarp();
+            float2 G = zero, H = zero;
+            const auto* row = &sm.slot[st].in[0][kRows - 1 - w.warp * TOK][2 * w.lane];
+            const float* dout = &sm.slot[st].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
+            auto gates = [&](int i) {
+                float2 y;
+                k.f[i] = grad_factors(smem_pair(row - i * kStrip),
+                                      smem_pair(row + (kRows - i) * kStrip),
+                                      smem_pair(row + (2 * kRows - i) * kStrip), prev[i], ch, y);
+                G = __fadd2_rn(G, y);
+                H = __fmul2_rn(k.f[i].lam, __fadd2_rn(smem_pair(dout - i * kStrip), H));
+            };
+            if (live == TOK) {
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) gates(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) {
+                    if (i < live) gates(i);
+                }
+            }
+            if (step + 1 < part.s1) load_prev(step + 1);
+            sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
+            sm.log_part[buf][w.warp][w.lane] = G;
+            __syncthreads();
+            // every warp is done with step - kHeld: its slot takes another tile
+            if (threadIdx.x == 0 && !dead && step - part.s0 >= kHeld) load_next();
+            k.j = publish<Cluster>(sm, turn++, w.warp, w.lane);
+        };
+        auto write_tile = [&](int step, const Held& k) {
+            float2 E = start_state<Cluster>(sm, k.j, w.lane, S, dead);
+            const long long last = last_of(step);
+            const int live = live_of(last);
+            const float* dout = &sm.slot[k.slot].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
+            if (w.in_c) {
+                Tin* dx = static_cast<Tin*>(r.grad_x) + last * r.ld_grad + w.c;
+                Tin* da = static_cast<Tin*>(r.grad_a) + last * r.ld_grad + w.c;
+                Tin* db = static_cast<Tin*>(r.grad_b) + last * r.ld_grad + w.c;
+                auto token = [&](int i) {
+                    const float2 D = __fadd2_rn(smem_pair(dout - i * kStrip), E);
+                    const long long o = i * r.ld_grad;
+                    store_grads(k.f[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
+                    E = __fmul2_rn(k.f[i].lam, D);
+                };
+                if (live == TOK) {
+#pragma unroll
+                    for (int i = 0; i < TOK; ++i) token(i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < TOK; ++i) {
+                        if (i < live) token(i);
+                    }
+                }
+                // the warp with the sequence's first token
+                if (live > 0 && last + 1 - live == w.t0 && r.grad_init)
+                    *reinterpret_cast<float2*>(r.grad_init + at) = E;
+            }
+            __syncwarp();
+        };
+        if constexpr (Smem::Pipe) {
+            // a step's exchange runs while the next step's tile is read
+            Held even, odd;
+            if (part.s0 < part.s1) read_tile(part.s0, even);
+            if (part.s0 > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
+            for (int step = part.s0; step < part.s1; step += 2) {
+                if (step + 1 < part.s1) read_tile(step + 1, odd);
+                write_tile(step, even);
+                if (step + 1 < part.s1) {
+                    if (step + 2 < part.s1) read_tile(step + 2, even);
+                    write_tile(step + 1, odd);
+                }
+            }
+        } else {
+            Held k;
+            for (int step = part.s0; step < part.s1; ++step) {
+                read_tile(step, k);
+                if (Cluster && step == part.s0 && step > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
+                write_tile(step, k);
             }
         }
-    } else {
-        Held k;
-        for (int step = 0; step < w.steps; ++step) {
-            read_tile(step, k);
-            write_tile(step, k);
-        }
-    }
-    if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && r.grad_init)
-        *reinterpret_cast<float2*>(r.grad_init + at) = S;
-    __syncthreads();
-    sm.part[0][w.warp][w.lane] = make_float4(acc_A.x, acc_A.y, acc_bias.x, acc_bias.y);
-    __syncthreads();
-    if (w.warp == 0 && w.in_c) {
-        float4 s = sm.part[0][0][w.lane];
+        if (Cluster && part.s1 < w.steps && w.rank == 0 && w.warp == 0)
+            hand_over(sched, parts.index, w.lane, S);
+        if (w.tiles == 0 && w.rank == 0 && w.warp == 0 && w.in_c && r.grad_init)
+            *reinterpret_cast<float2*>(r.grad_init + at) = S;
+        __syncthreads();
+        sm.part[0][w.warp][w.lane] = make_float4(acc_A.x, acc_A.y, acc_bias.x, acc_bias.y);
+        __syncthreads();
+        if (w.warp == 0 && w.in_c) {
+            float4 s = sm.part[0][0][w.lane];
 #pragma unroll
-        for (int k = 1; k < Smem::WARPS; ++k) {
-            const float4 v = sm.part[0][k][w.lane];
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            for (int k = 1; k < Smem::WARPS; ++k) {
+                const float4 v = sm.part[0][k][w.lane];
+                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            }
+            const float2 sum_A = __fmul2_rn(make_float2(s.x, s.y), bcast2(kLn2));
+            const float2 sum_bias = make_float2(s.z, s.w);
+            const size_t row = (size_t)w.seq * w.K + w.rank, later = (size_t)p.nseq * w.K;
+            auto put = [&](size_t row, float2 a, float2 b) {
+                float* o = partial + row * 2 * p.C + w.c;
+                *reinterpret_cast<float2*>(o) = a;
+                *reinterpret_cast<float2*>(o + p.C) = b;
+            };
+            put(part.s0 > 0 ? row + later : row, sum_A, sum_bias);
+            if (Cluster && sched.span && part.s0 == 0 && part.s1 == w.steps) put(row + later, zero, zero);
         }
-        float* o = part + ((size_t)w.seq * w.K + w.rank) * 2 * p.C + w.c;
-        *reinterpret_cast<float2*>(o) = __fmul2_rn(make_float2(s.x, s.y), bcast2(kLn2));
-        *reinterpret_cast<float2*>(o + p.C) = make_float2(s.z, s.w);
+        if (!Cluster) break;
     }
     if (dead && threadIdx.x == 0) wait_in_flight(sm.full, STAGES, issued);
     if constexpr (Cluster) cluster_barrier();
@@ -743,47 +872,69 @@ long long units_of(const RecurrenceParams& p) {
 // Sequences of up to a warp's tokens leave the tiled form's other warps idle.
 bool use_tiles(const RecurrenceParams& p) { return mean_length(p) > 16; }
 
-// CTAs per cluster for `units` (sequence, strip) pairs of `tiles` tiles.  A cluster's CTAs
-// take one SM each, so K of them for every unit pay only while the units leave SMs idle: the
-// largest K whose clusters the device still holds at once, at one CTA per SM.  (96 units of
-// 8192 tokens: 141 us forward with K = 1, 168 with K = 2, 178 with K = 3.)
+// Clusters of K CTAs of a kernel that the current device holds at once; the runtime is asked once
+// per kernel, K and device.
+struct Capacity {
+    std::atomic<int> fit[64][kMaxCluster + 1];
+};
 template <typename Kernel>
-cudaError_t cluster_of(Kernel kernel, int threads, size_t smem, long long units, int tiles, int* K) {
-    *K = 1;
-    const int most = (int)std::min<long long>({(long long)kMaxCluster, (long long)tiles,
-                                               device_sms() / units});
-    if (most < 2) return cudaSuccess;
-    // clusters of k CTAs that the current device holds at once; asked once per kernel and device
-    struct Held {
-        std::atomic<int> fit[kMaxCluster + 1];
-    };
-    static Held held[64];
+cudaError_t clusters_held(Capacity& held, Kernel kernel, int threads, size_t smem, int K, int* fit) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
     if (e != cudaSuccess) return e;
-    for (int k = most; k > 1; --k) {
-        int fit = held[dev].fit[k].load();
-        if (fit == 0) {
-            cudaLaunchAttribute attr = {};
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = (unsigned)k;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)k);
-            cfg.blockDim = dim3(threads);
-            cfg.dynamicSmemBytes = smem;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            e = allow_smem((const void*)kernel, smem);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
-            if (e != cudaSuccess) return e;
-            held[dev].fit[k].store(std::max(fit, 1));
-        }
-        if (fit >= units) {
-            *K = k;
-            break;
-        }
+    *fit = held.fit[dev][K].load();
+    if (*fit > 0) return cudaSuccess;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)K;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)K);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = allow_smem((const void*)kernel, smem);
+    if (e == cudaSuccess && K > 8)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(fit, kernel, &cfg);
+    if (e == cudaSuccess) held.fit[dev][K].store(*fit = std::max(*fit, 1));
+    return e;
+}
+
+// What a launch of the tiled kernels looks like: which form, K CTAs per cluster, and steps per
+// cluster under a split schedule (0: plain).
+struct Plan {
+    int form, K, span, clusters;
+    double time;
+};
+
+// Offers `slots` clusters of K CTAs that take `rows` tokens of a unit per step of `ns`, plain and
+// (cuttable: equal lengths) split.  The time is that of the busiest slot's steps.  A split
+// schedule spends some 8 us more: another node of the stream sets its counters to zero, and a
+// part's first tile is not copied ahead.
+void offer(Plan* plan, const RecurrenceParams& p, int form, int K, long long slots, long long rows,
+           double ns, bool cuttable) {
+    const long long units = units_of(p), steps = (mean_length(p) + rows - 1) / rows;
+    double t = (double)((units + slots - 1) / slots) * steps * ns;
+    if (!plan->K || t < 0.98 * plan->time) *plan = {form, K, 0, 0, t};
+    const long long total = units * steps, span = std::max(steps, (total + slots - 1) / slots);
+    if (!cuttable || p.cu_seqlens || total + span > (1 << 30)) return;
+    t = (double)(span + 1) * ns + 8000.0;
+    if (t < 0.95 * plan->time)
+        *plan = {form, K, (int)span, (int)((total + span - 1) / span), t};
+}
+template <typename Smem, typename Kernel>
+cudaError_t offer_clusters(Plan* plan, const RecurrenceParams& p, int form, Kernel kernel,
+                           Capacity& held, double ns, double ns_per_rank) {
+    for (int K = 2; K <= Smem::PEERS; ++K) {
+        // clusters are for units that leave SMs idle, and for at least a tile each
+        if (units_of(p) > 2LL * device_sms() || (long long)(K - 1) * Smem::kRows >= mean_length(p)) break;
+        int fit = 0;
+        const cudaError_t e = clusters_held(held, kernel, 32 * Smem::WARPS, sizeof(Smem), K, &fit);
+        if (e != cudaSuccess) return e;
+        offer(plan, p, form, K, fit, (long long)K * Smem::kRows, ns + K * ns_per_rank, true);
     }
     return cudaSuccess;
 }
@@ -816,86 +967,158 @@ bool make_maps(Maps& m, const RecurrenceParams& p, const float* dout, int box) {
            (!dout || make_map_pitched(&m.dout, dout, true, p.C, rows, p.C, kStrip, box));
 }
 
-// Warps, tokens per warp, slots, CTAs per SM of each kernel.  Registers set the tokens (two
-// values per token and channel forward, five backward, twice that in a cluster, where a
-// warp holds two steps), shared memory the slots.
-template <typename Tin, bool Cluster> struct Forms;
-template <> struct Forms<__nv_bfloat16, false> {
-    using Fwd = TileSmem<__nv_bfloat16, 8, 12, 2, false>;
-    using Bwd = TileSmem<__nv_bfloat16, 8, 8, 3, true>;
-    static constexpr int kFwdBlocks = 2;
+// The forms of each kernel: warps, tokens per warp, slots, CTAs per cluster at most.  One: no
+// cluster, for units that fill the SMs.  Wide: one CTA per SM, two steps in registers, for
+// few units.  Pair: two CTAs per SM, whose phases overlap each other's instead, for units in
+// between (a cluster's CTAs share SMs, so it needs enough clusters).  Registers set the
+// tokens (two values per token and channel forward, five backward), shared memory the slots.
+// Times of a step in ns as measured with every SM at work; One has a second where a CTA has
+// its SM for itself.
+template <typename Tin> struct Forms;
+template <> struct Forms<__nv_bfloat16> {
+    using T = __nv_bfloat16;
+    struct Fwd {
+        using One = TileSmem<T, 8, 12, 2, 1, false, false>;
+        using Wide = TileSmem<T, 8, 16, 2, 12, true, false>;
+        using Pair = TileSmem<T, 8, 12, 2, 4, false, false>;
+        static constexpr int kOneBlocks = 2;
+        static constexpr double kAlone = 1640, kOne = 3000, kWide = 2700, kPair = 3350;
+    };
+    struct Bwd {
+        using One = TileSmem<T, 8, 8, 3, 1, false, true>;
+        using Wide = TileSmem<T, 8, 8, 3, 12, true, true>;
+        using Pair = TileSmem<T, 8, 8, 2, 4, false, true>;
+        static constexpr int kOneBlocks = 1;
+        static constexpr double kAlone = 2100, kOne = 2500, kWide = 2950, kPair = 4750;
+    };
 };
-template <> struct Forms<__nv_bfloat16, true> {
-    using Fwd = TileSmem<__nv_bfloat16, 8, 16, 2, false>;
-    using Bwd = TileSmem<__nv_bfloat16, 8, 8, 3, true>;
-    static constexpr int kFwdBlocks = 1;
+template <> struct Forms<float> {
+    using T = float;
+    struct Fwd {
+        using One = TileSmem<T, 8, 8, 2, 1, false, false>;
+        using Wide = TileSmem<T, 8, 8, 3, 12, true, false>;
+        using Pair = TileSmem<T, 8, 6, 2, 4, false, false>;
+        static constexpr int kOneBlocks = 2;
+        static constexpr double kAlone = 1310, kOne = 2350, kWide = 1950, kPair = 2300;
+    };
+    struct Bwd {
+        using One = TileSmem<T, 8, 8, 3, 1, false, true>;
+        using Wide = TileSmem<T, 8, 8, 3, 8, true, true>;
+        using Pair = TileSmem<T, 8, 4, 2, 4, false, true>;
+        static constexpr int kOneBlocks = 1;
+        static constexpr double kAlone = 2430, kOne = 2550, kWide = 2950, kPair = 3000;
+    };
 };
-template <> struct Forms<float, false> {
-    using Fwd = TileSmem<float, 8, 8, 2, false>;
-    using Bwd = TileSmem<float, 8, 8, 3, true>;
-    static constexpr int kFwdBlocks = 2;
-};
-template <> struct Forms<float, true> {
-    using Fwd = TileSmem<float, 8, 8, 3, false>;
-    using Bwd = TileSmem<float, 8, 8, 3, true>;
-    static constexpr int kFwdBlocks = 1;
-};
+constexpr double kPerRank = 30;
 
-template <typename Tin, bool Cluster>
-cudaError_t forward_tiles(const RecurrenceParams& p, int K, cudaStream_t stream) {
-    using F = Forms<Tin, Cluster>;
-    using Smem = typename F::Fwd;
-    const int strips = (p.C + kStrip - 1) / kStrip;
-    const long long grid = (long long)p.nseq * strips * K;
-    Maps m;
-    if (grid > 0x7fffffffLL || !make_maps(m, p, nullptr, Smem::kRows)) return cudaErrorNotSupported;
-    return launch_tiles(recurrence_tile_kernel<Smem, F::kFwdBlocks, Cluster>, grid,
-                        32 * Smem::WARPS, K, sizeof(Smem), stream, m, p, strips);
+enum { kOneForm, kWideForm, kPairForm };
+
+template <typename F>
+void offer_one(Plan* plan, const RecurrenceParams& p) {
+    const bool alone = units_of(p) <= device_sms();
+    offer(plan, p, kOneForm, 1, alone ? device_sms() : (long long)F::kOneBlocks * device_sms(),
+          F::One::kRows, alone ? F::kAlone : F::kOne, false);
 }
 
-template <typename Tin, bool Cluster>
-cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, int K,
-                           cudaStream_t stream) {
-    using Smem = typename Forms<Tin, Cluster>::Bwd;
+// A split schedule's counters and states in `ws`, the counters set to zero.
+size_t schedule_bytes(const Plan& plan) {
+    return plan.span ? sizeof(float) * plan.clusters * (size_t)kStrip + sizeof(int) * (plan.clusters + 1) : 0;
+}
+cudaError_t set_schedule(Schedule* s, const Plan& plan, long long units, int steps, void* ws,
+                         cudaStream_t stream) {
+    *s = {};
+    if (!plan.span) return cudaSuccess;
+    s->span = plan.span;
+    s->steps = steps;
+    s->total = (int)(units * steps);
+    s->states = static_cast<float*>(ws);
+    s->ready = reinterpret_cast<uint32_t*>(s->states + (size_t)plan.clusters * kStrip);
+    s->ticket = reinterpret_cast<int*>(s->ready + plan.clusters);
+    return cudaMemsetAsync(s->ready, 0, sizeof(int) * (plan.clusters + 1), stream);
+}
+
+template <typename Smem, int Blocks>
+cudaError_t forward_tiles(const RecurrenceParams& p, const Plan& plan, cudaStream_t stream) {
     const int strips = (p.C + kStrip - 1) / kStrip;
-    const long long grid = (long long)p.nseq * strips * K, rows = (long long)p.nseq * K;
+    const long long units = units_of(p);
+    const long long grid = (plan.span ? plan.clusters : units) * plan.K;
+    const long long rows = (long long)Smem::kRows * plan.K;
     Maps m;
-    if (grid > 0x7fffffffLL || !make_maps(m, p, r.grad_out, Smem::kRows))
-        return cudaErrorNotSupported;
-    float* part = nullptr;
-    cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);
+    if (grid > 0x7fffffffLL || !make_maps(m, p, nullptr, Smem::kRows)) return cudaErrorNotSupported;
+    void* ws = nullptr;
+    cudaError_t e = plan.span ? workspace_alloc(&ws, schedule_bytes(plan), stream) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    e = launch_tiles(recurrence_tile_backward_kernel<Smem, 1, Cluster>, grid,
-                     32 * Smem::WARPS, K, sizeof(Smem), stream, m, p, r, part, strips);
+    Schedule s;
+    e = set_schedule(&s, plan, units, (int)((p.T + rows - 1) / rows), ws, stream);
     if (e == cudaSuccess)
-        e = launch_column_sum(part, rows, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
+        e = launch_tiles(recurrence_tile_kernel<Smem, Blocks>, grid, 32 * Smem::WARPS, plan.K,
+                         sizeof(Smem), stream, m, p, strips, s);
+    const cudaError_t f = ws ? cudaFreeAsync(ws, stream) : cudaSuccess;
+    return e != cudaSuccess ? e : f;
+}
+
+template <typename Smem, int Blocks>
+cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, const Plan& plan,
+                           cudaStream_t stream) {
+    const int strips = (p.C + kStrip - 1) / kStrip;
+    const long long units = units_of(p);
+    const long long grid = (plan.span ? plan.clusters : units) * plan.K;
+    const long long rows = (long long)Smem::kRows * plan.K;
+    // rows of partial sums: one per (sequence, rank), and one for a cut unit's later part
+    const long long sums = (long long)p.nseq * plan.K * (plan.span ? 2 : 1);
+    Maps m;
+    if (grid > 0x7fffffffLL || !make_maps(m, p, r.grad_out, Smem::kRows)) return cudaErrorNotSupported;
+    const size_t sum_bytes = sizeof(float) * sums * 2 * p.C;
+    float* part = nullptr;
+    cudaError_t e = workspace_alloc((void**)&part, sum_bytes + schedule_bytes(plan), stream);
+    if (e != cudaSuccess) return e;
+    Schedule s;
+    e = set_schedule(&s, plan, units, (int)((p.T + rows - 1) / rows),
+                     reinterpret_cast<char*>(part) + sum_bytes, stream);
+    if (e == cudaSuccess)
+        e = launch_tiles(recurrence_tile_backward_kernel<Smem, Blocks>, grid, 32 * Smem::WARPS,
+                         plan.K, sizeof(Smem), stream, m, p, r, part, strips, s);
+    if (e == cudaSuccess)
+        e = launch_column_sum(part, sums, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
     const cudaError_t f = cudaFreeAsync(part, stream);
     return e != cudaSuccess ? e : f;
 }
 
 template <typename Tin>
 cudaError_t forward_tiles(const RecurrenceParams& p, cudaStream_t stream) {
-    using F = Forms<Tin, true>;
-    using Smem = typename F::Fwd;
-    int K = 1;
-    const cudaError_t e =
-        cluster_of(recurrence_tile_kernel<Smem, F::kFwdBlocks, true>, 32 * Smem::WARPS, sizeof(Smem),
-                   units_of(p), (mean_length(p) + Smem::kRows - 1) / Smem::kRows, &K);
+    using F = typename Forms<Tin>::Fwd;
+    static Capacity wide, pair;
+    Plan plan = {};
+    offer_one<F>(&plan, p);
+    cudaError_t e = offer_clusters<typename F::Wide>(
+        &plan, p, kWideForm, recurrence_tile_kernel<typename F::Wide, 1>, wide, F::kWide, kPerRank);
+    if (e == cudaSuccess)
+        e = offer_clusters<typename F::Pair>(
+            &plan, p, kPairForm, recurrence_tile_kernel<typename F::Pair, 2>, pair, F::kPair, kPerRank);
     if (e != cudaSuccess) return e;
-    return K > 1 ? forward_tiles<Tin, true>(p, K, stream) : forward_tiles<Tin, false>(p, 1, stream);
+    return plan.form == kOneForm    ? forward_tiles<typename F::One, F::kOneBlocks>(p, plan, stream)
+           : plan.form == kWideForm ? forward_tiles<typename F::Wide, 1>(p, plan, stream)
+                                    : forward_tiles<typename F::Pair, 2>(p, plan, stream);
 }
 
 template <typename Tin>
 cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r,
                            cudaStream_t stream) {
-    using Smem = typename Forms<Tin, true>::Bwd;
-    int K = 1;
-    const cudaError_t e =
-        cluster_of(recurrence_tile_backward_kernel<Smem, 1, true>, 32 * Smem::WARPS, sizeof(Smem),
-                   units_of(p), (mean_length(p) + Smem::kRows - 1) / Smem::kRows, &K);
+    using F = typename Forms<Tin>::Bwd;
+    static Capacity wide, pair;
+    Plan plan = {};
+    offer_one<F>(&plan, p);
+    cudaError_t e = offer_clusters<typename F::Wide>(
+        &plan, p, kWideForm, recurrence_tile_backward_kernel<typename F::Wide, 1>, wide, F::kWide,
+        kPerRank);
+    if (e == cudaSuccess)
+        e = offer_clusters<typename F::Pair>(
+            &plan, p, kPairForm, recurrence_tile_backward_kernel<typename F::Pair, 2>, pair,
+            F::kPair, kPerRank);
     if (e != cudaSuccess) return e;
-    return K > 1 ? backward_tiles<Tin, true>(p, r, K, stream)
-                 : backward_tiles<Tin, false>(p, r, 1, stream);
+    return plan.form == kOneForm    ? backward_tiles<typename F::One, F::kOneBlocks>(p, r, plan, stream)
+           : plan.form == kWideForm ? backward_tiles<typename F::Wide, 1>(p, r, plan, stream)
+                                    : backward_tiles<typename F::Pair, 2>(p, r, plan, stream);
 }
 
 }  // namespace
