@@ -856,8 +856,11 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
     if constexpr (Cluster) cluster_barrier();
 }
 
-// Rows of CTAs of the sequential form: the partial sums have one row each.
-int seq_rows(int nseq) { return std::min(nseq, 64); }
+// Rows of CTAs of the sequential form backward, one row of partial sums each: enough threads to
+// fill the SMs.
+int seq_rows(const RecurrenceParams& p) {
+    return std::min(p.nseq, std::max(64, (300000 + p.C - 1) / p.C));
+}
 
 // The tokens of a call's mean sequence; the host does not know packed sequences' lengths.
 int mean_length(const RecurrenceParams& p) {
@@ -868,9 +871,6 @@ int mean_length(const RecurrenceParams& p) {
 long long units_of(const RecurrenceParams& p) {
     return (long long)p.nseq * ((p.C + kStrip - 1) / kStrip);
 }
-
-// Sequences of up to a warp's tokens leave the tiled form's other warps idle.
-bool use_tiles(const RecurrenceParams& p) { return mean_length(p) > 16; }
 
 // Clusters of K CTAs of a kernel that the current device holds at once; the runtime is asked once
 // per kernel, K and device.
@@ -911,30 +911,31 @@ struct Plan {
 };
 
 // Offers `slots` clusters of K CTAs that take `rows` tokens of a unit per step of `ns`, plain and
-// (cuttable: equal lengths) split.  The time is that of the busiest slot's steps.  A split
+// (cuttable: equal lengths) split.  The time is that of the busiest slot's steps, and of what
+// a CTA does before its first (`start_ns`, less where another CTA of its SM works on).  A split
 // schedule spends some 8 us more: another node of the stream sets its counters to zero, and a
 // part's first tile is not copied ahead.
 void offer(Plan* plan, const RecurrenceParams& p, int form, int K, long long slots, long long rows,
-           double ns, bool cuttable) {
+           double ns, double start_ns, bool cuttable) {
     const long long units = units_of(p), steps = (mean_length(p) + rows - 1) / rows;
-    double t = (double)((units + slots - 1) / slots) * steps * ns;
+    double t = (double)((units + slots - 1) / slots) * (steps * ns + start_ns);
     if (!plan->K || t < 0.98 * plan->time) *plan = {form, K, 0, 0, t};
     const long long total = units * steps, span = std::max(steps, (total + slots - 1) / slots);
     if (!cuttable || p.cu_seqlens || total + span > (1 << 30)) return;
-    t = (double)(span + 1) * ns + 8000.0;
+    t = (double)(span + 1) * ns + start_ns + 8000.0;
     if (t < 0.95 * plan->time)
         *plan = {form, K, (int)span, (int)((total + span - 1) / span), t};
 }
 template <typename Smem, typename Kernel>
 cudaError_t offer_clusters(Plan* plan, const RecurrenceParams& p, int form, Kernel kernel,
-                           Capacity& held, double ns, double ns_per_rank) {
+                           Capacity& held, double ns, double ns_per_rank, double start_ns) {
     for (int K = 2; K <= Smem::PEERS; ++K) {
         // clusters are for units that leave SMs idle, and for at least a tile each
         if (units_of(p) > 2LL * device_sms() || (long long)(K - 1) * Smem::kRows >= mean_length(p)) break;
         int fit = 0;
         const cudaError_t e = clusters_held(held, kernel, 32 * Smem::WARPS, sizeof(Smem), K, &fit);
         if (e != cudaSuccess) return e;
-        offer(plan, p, form, K, fit, (long long)K * Smem::kRows, ns + K * ns_per_rank, true);
+        offer(plan, p, form, K, fit, (long long)K * Smem::kRows, ns + K * ns_per_rank, start_ns, true);
     }
     return cudaSuccess;
 }
@@ -968,56 +969,70 @@ bool make_maps(Maps& m, const RecurrenceParams& p, const float* dout, int box) {
 }
 
 // The forms of each kernel: warps, tokens per warp, slots, CTAs per cluster at most.  One: no
-// cluster, for units that fill the SMs.  Wide: one CTA per SM, two steps in registers, for
-// few units.  Pair: two CTAs per SM, whose phases overlap each other's instead, for units in
-// between (a cluster's CTAs share SMs, so it needs enough clusters).  Registers set the
-// tokens (two values per token and channel forward, five backward), shared memory the slots.
-// Times of a step in ns as measured with every SM at work; One has a second where a CTA has
-// its SM for itself.
+// cluster, a CTA per SM.  Many: no cluster, two CTAs per SM, whose phases and starts overlap.
+// Wide: clusters with one CTA per SM and two steps in registers, for few units.  Pair:
+// clusters with two CTAs per SM, for units in between (a cluster's CTAs share SMs, so it
+// needs enough clusters).  Registers set the tokens (two values per token and channel
+// forward, five backward), shared memory the slots.  Times in ns as measured with every SM at
+// work (One: with the SM to itself): a step, and a CTA's start.
 template <typename Tin> struct Forms;
 template <> struct Forms<__nv_bfloat16> {
     using T = __nv_bfloat16;
     struct Fwd {
         using One = TileSmem<T, 8, 12, 2, 1, false, false>;
+        using Many = One;
         using Wide = TileSmem<T, 8, 16, 2, 12, true, false>;
         using Pair = TileSmem<T, 8, 12, 2, 4, false, false>;
-        static constexpr int kOneBlocks = 2;
-        static constexpr double kAlone = 1640, kOne = 3000, kWide = 2700, kPair = 3350;
+        static constexpr double kOne = 1710, kMany = 3140, kWide = 2800, kPair = 3500;
+        static constexpr double kStart = 1500, kSharedStart = 300;
     };
     struct Bwd {
         using One = TileSmem<T, 8, 8, 3, 1, false, true>;
+        using Many = TileSmem<T, 8, 6, 2, 1, false, true>;
         using Wide = TileSmem<T, 8, 8, 3, 12, true, true>;
-        using Pair = TileSmem<T, 8, 8, 2, 4, false, true>;
-        static constexpr int kOneBlocks = 1;
-        static constexpr double kAlone = 2100, kOne = 2500, kWide = 2950, kPair = 4750;
+        using Pair = TileSmem<T, 8, 6, 2, 4, false, true>;
+        static constexpr double kOne = 2070, kMany = 3300, kWide = 2900, kPair = 3450;
+        static constexpr double kStart = 3400, kSharedStart = 1500;
     };
 };
 template <> struct Forms<float> {
     using T = float;
     struct Fwd {
         using One = TileSmem<T, 8, 8, 2, 1, false, false>;
+        using Many = One;
         using Wide = TileSmem<T, 8, 8, 3, 12, true, false>;
         using Pair = TileSmem<T, 8, 6, 2, 4, false, false>;
-        static constexpr int kOneBlocks = 2;
-        static constexpr double kAlone = 1310, kOne = 2350, kWide = 1950, kPair = 2300;
+        static constexpr double kOne = 1290, kMany = 2350, kWide = 1750, kPair = 2250;
+        static constexpr double kStart = 1500, kSharedStart = 300;
     };
     struct Bwd {
         using One = TileSmem<T, 8, 8, 3, 1, false, true>;
+        using Many = TileSmem<T, 8, 4, 2, 1, false, true>;
         using Wide = TileSmem<T, 8, 8, 3, 8, true, true>;
         using Pair = TileSmem<T, 8, 4, 2, 4, false, true>;
-        static constexpr int kOneBlocks = 1;
-        static constexpr double kAlone = 2430, kOne = 2550, kWide = 2950, kPair = 3000;
+        static constexpr double kOne = 2380, kMany = 2700, kWide = 3600, kPair = 2850;
+        static constexpr double kStart = 3400, kSharedStart = 1500;
     };
 };
-constexpr double kPerRank = 30;
+constexpr double kWideRank = 10, kPairRank = 50;  // a step's further ns for each CTA of the cluster
 
-enum { kOneForm, kWideForm, kPairForm };
+enum Form { kOneForm, kManyForm, kWideForm, kPairForm };
 
 template <typename F>
-void offer_one(Plan* plan, const RecurrenceParams& p) {
-    const bool alone = units_of(p) <= device_sms();
-    offer(plan, p, kOneForm, 1, alone ? device_sms() : (long long)F::kOneBlocks * device_sms(),
-          F::One::kRows, alone ? F::kAlone : F::kOne, false);
+void offer_single(Plan* plan, const RecurrenceParams& p) {
+    const int sms = device_sms();
+    if (units_of(p) <= sms)
+        offer(plan, p, kOneForm, 1, sms, F::One::kRows, F::kOne, F::kStart, false);
+    else
+        offer(plan, p, kManyForm, 1, 2LL * sms, F::Many::kRows, F::kMany, F::kSharedStart, false);
+}
+
+// The sequential form's time: a chain of tokens, each at least a memory latency and at least its
+// bytes' time.  Against a plan's, which it beats for short sequences (64 sequences of 6144
+// channels, forward: 31 against 82 us at 32 tokens, 117 against 134 at 128; one sequence: 16
+// against 8 at 16).
+double seq_time(const RecurrenceParams& p, double latency_ns, double channel_ns) {
+    return mean_length(p) * std::max(latency_ns, channel_ns * p.nseq * p.C);
 }
 
 // A split schedule's counters and states in `ws`, the counters set to zero.
@@ -1085,76 +1100,78 @@ cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, 
 }
 
 template <typename Tin>
-cudaError_t forward_tiles(const RecurrenceParams& p, cudaStream_t stream) {
+cudaError_t forward(const RecurrenceParams& p, cudaStream_t stream) {
     using F = typename Forms<Tin>::Fwd;
     static Capacity wide, pair;
     Plan plan = {};
-    offer_one<F>(&plan, p);
+    offer_single<F>(&plan, p);
+    if (seq_time(p, 620, 0.0023) < plan.time) {
+        const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads),
+                        (unsigned)std::min(p.nseq, 65535));
+        recurrence_seq_kernel<Tin><<<grid, kSeqThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     cudaError_t e = offer_clusters<typename F::Wide>(
-        &plan, p, kWideForm, recurrence_tile_kernel<typename F::Wide, 1>, wide, F::kWide, kPerRank);
+        &plan, p, kWideForm, recurrence_tile_kernel<typename F::Wide, 1>, wide, F::kWide, kWideRank,
+        F::kStart);
     if (e == cudaSuccess)
         e = offer_clusters<typename F::Pair>(
-            &plan, p, kPairForm, recurrence_tile_kernel<typename F::Pair, 2>, pair, F::kPair, kPerRank);
+            &plan, p, kPairForm, recurrence_tile_kernel<typename F::Pair, 2>, pair, F::kPair,
+            kPairRank, F::kSharedStart);
     if (e != cudaSuccess) return e;
-    return plan.form == kOneForm    ? forward_tiles<typename F::One, F::kOneBlocks>(p, plan, stream)
-           : plan.form == kWideForm ? forward_tiles<typename F::Wide, 1>(p, plan, stream)
-                                    : forward_tiles<typename F::Pair, 2>(p, plan, stream);
+    switch (plan.form) {
+        case kOneForm: return forward_tiles<typename F::One, 2>(p, plan, stream);
+        case kManyForm: return forward_tiles<typename F::Many, 2>(p, plan, stream);
+        case kWideForm: return forward_tiles<typename F::Wide, 1>(p, plan, stream);
+        default: return forward_tiles<typename F::Pair, 2>(p, plan, stream);
+    }
 }
 
 template <typename Tin>
-cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r,
-                           cudaStream_t stream) {
+cudaError_t backward(const RecurrenceParams& p, const RecurrenceGrads& r, cudaStream_t stream) {
     using F = typename Forms<Tin>::Bwd;
     static Capacity wide, pair;
     Plan plan = {};
-    offer_one<F>(&plan, p);
+    offer_single<F>(&plan, p);
+    if (seq_time(p, 750, 0.0038) < plan.time) {
+        const int rows = seq_rows(p);
+        float* part = nullptr;
+        cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);
+        if (e != cudaSuccess) return e;
+        const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads), (unsigned)rows);
+        recurrence_seq_backward_kernel<Tin><<<grid, kSeqThreads, 0, stream>>>(p, r, part);
+        e = cudaGetLastError();
+        if (e == cudaSuccess)
+            e = launch_column_sum(part, rows, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
+        const cudaError_t f = cudaFreeAsync(part, stream);
+        return e != cudaSuccess ? e : f;
+    }
     cudaError_t e = offer_clusters<typename F::Wide>(
         &plan, p, kWideForm, recurrence_tile_backward_kernel<typename F::Wide, 1>, wide, F::kWide,
-        kPerRank);
+        kWideRank, F::kStart);
     if (e == cudaSuccess)
         e = offer_clusters<typename F::Pair>(
             &plan, p, kPairForm, recurrence_tile_backward_kernel<typename F::Pair, 2>, pair,
-            F::kPair, kPerRank);
+            F::kPair, kPairRank, F::kSharedStart);
     if (e != cudaSuccess) return e;
-    return plan.form == kOneForm    ? backward_tiles<typename F::One, F::kOneBlocks>(p, r, plan, stream)
-           : plan.form == kWideForm ? backward_tiles<typename F::Wide, 1>(p, r, plan, stream)
-                                    : backward_tiles<typename F::Pair, 2>(p, r, plan, stream);
+    switch (plan.form) {
+        case kOneForm: return backward_tiles<typename F::One, 1>(p, r, plan, stream);
+        case kManyForm: return backward_tiles<typename F::Many, 2>(p, r, plan, stream);
+        case kWideForm: return backward_tiles<typename F::Wide, 1>(p, r, plan, stream);
+        default: return backward_tiles<typename F::Pair, 2>(p, r, plan, stream);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_recurrence(const RecurrenceParams& p, cudaStream_t stream) {
-    if (use_tiles(p))
-        return p.in == InType::BF16 ? forward_tiles<__nv_bfloat16>(p, stream)
-                                    : forward_tiles<float>(p, stream);
-    const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads),
-                    (unsigned)std::min(p.nseq, 65535));
-    if (p.in == InType::BF16)
-        recurrence_seq_kernel<__nv_bfloat16><<<grid, kSeqThreads, 0, stream>>>(p);
-    else
-        recurrence_seq_kernel<float><<<grid, kSeqThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return p.in == InType::BF16 ? forward<__nv_bfloat16>(p, stream) : forward<float>(p, stream);
 }
 
 cudaError_t launch_recurrence_backward(const RecurrenceParams& p, const RecurrenceGrads& r,
                                        cudaStream_t stream) {
-    if (use_tiles(p))
-        return p.in == InType::BF16 ? backward_tiles<__nv_bfloat16>(p, r, stream)
-                                    : backward_tiles<float>(p, r, stream);
-    const int rows = seq_rows(p.nseq);
-    float* part = nullptr;
-    cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads), (unsigned)rows);
-    if (p.in == InType::BF16)
-        recurrence_seq_backward_kernel<__nv_bfloat16><<<grid, kSeqThreads, 0, stream>>>(p, r, part);
-    else
-        recurrence_seq_backward_kernel<float><<<grid, kSeqThreads, 0, stream>>>(p, r, part);
-    e = cudaGetLastError();
-    if (e == cudaSuccess)
-        e = launch_column_sum(part, rows, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
-    const cudaError_t f = cudaFreeAsync(part, stream);
-    return e != cudaSuccess ? e : f;
+    return p.in == InType::BF16 ? backward<__nv_bfloat16>(p, r, stream)
+                                : backward<float>(p, r, stream);
 }
 
 int read_and_clear_recurrence_status() {

@@ -159,13 +159,14 @@ def test_rows_outside_the_sequences_stay_and_are_not_read(lens, lead):
     got = gdr.linear_recurrence_backward(*args, kept, dev(big["go"]), dev(m["gf"]),
                                          dev(m["init"]), cu, *grads)
     torch.cuda.synchronize()
-    _, want = on_gpu(m)
-    for v, w in zip((out,) + got[:3], (want[0],) + want[2:5]):
+    inner = slice(lead, lead + sum(lens))
+    for v in (out,) + tuple(got[:3]):
         assert (v[:, :lead] == 5).all() and (v[:, lead + sum(lens):] == 5).all()
-        assert torch.equal(v[:, lead:lead + sum(lens)], w)
-    assert torch.equal(final, want[1])
-    for v, w in zip(got[3:], want[5:]):
-        assert torch.equal(v, w)
+    # (not bit by bit against a call without the outer rows: the number of tokens chooses
+    # among forms that add in another order)
+    ref, mag = expected(m)
+    check(m, (out[:, inner], final) + tuple(g[:, inner] for g in got[:3]) + tuple(got[3:]), ref,
+          mag, max(lens))
 
 
 @gpu
