@@ -116,6 +116,83 @@ def test_packed(lens, dtype):
     check(m, on_gpu(m)[1], ref, mag, max(lens))
 
 
+def some_channels(m, got, every):
+    """the case and its results at every `every`-th channel: channels do not mix"""
+    cut = dict(m)
+    for k in ("x", "a", "b", "go", "A_log", "dt_bias", "init", "gf"):
+        if m[k] is not None:
+            cut[k] = m[k][..., ::every]
+    return cut, tuple(g[..., ::every] for g in got)
+
+
+# calls large enough for clusters of CTAs and for sequences cut between them: few strips and long,
+# some strips, a strip count that no cluster count divides, many strips; ragged lengths; the
+# last one's sequences differ in nothing but their place
+LARGE = [(1, 30000, 192, "bf16"), (1, 20011, 1024, "bf16"), (1, 5000, 6144, "bf16"),
+         (2, 4099, 2048, "bf16"), (3, 1500, 4104, "bf16"), (1, 6000, 328, "f32"),
+         (2, 3000, 2048, "f32"), (1, 9001, 5000, "f32"), (5, 700, 4096, "f32")]
+
+
+@gpu
+@pytest.mark.parametrize("B,T,C,dtype", LARGE)
+def test_large(B, T, C, dtype):
+    m = make(B, T, C, dtype, seed=C)
+    got = on_gpu(m)[1]
+    again = on_gpu(m)[1]
+    for name, p, q in zip(NAMES, got, again):
+        assert torch.equal(p, q), name
+    m, got = some_channels(m, got, max(1, B * T * C // 3_000_000))
+    ref, mag = expected(m)
+    check(m, got, ref, mag, T)
+
+
+@gpu
+def test_large_calls_on_two_streams_and_from_a_graph():
+    """calls whose clusters hand states to one another, two at a time"""
+    ms = [make(1, 5000, 6144, seed=3), make(1, 20011, 1024, seed=4)]
+    want = [on_gpu(m)[1] for m in ms]
+    ready = [([dev(m[k], torch.bfloat16) for k in ("x", "a", "b")] +
+              [dev(m["A_log"]), dev(m["dt_bias"])], dev(m["init"]), dev(m["go"]), dev(m["gf"]))
+             for m in ms]
+    streams = [torch.cuda.Stream() for _ in ms]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def both():
+        for i, s in enumerate(streams):
+            args, init, go, gf = ready[i]
+            with torch.cuda.stream(s):
+                out, final = gdr.linear_recurrence(*args, init)
+                got[i] = (out, final) + gdr.linear_recurrence_backward(*args, out, go, gf, init)
+
+    for _ in range(4):
+        both()
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for name, p, q in zip(NAMES, w, g):
+            assert torch.equal(p, q), name
+    graph, cap = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=cap):
+        for s in streams:
+            s.wait_stream(cap)
+        both()
+        for s in streams:
+            cap.wait_stream(s)
+    torch.cuda.current_stream().wait_stream(cap)
+    for _ in range(3):
+        for g in got:
+            for t in g:
+                t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            for name, p, q in zip(NAMES, w, g):
+                assert torch.equal(p, q), name
+    assert gdr.gdr_device_status() == gdr.GDR_OK
+    del graph
+
+
 @gpu
 @pytest.mark.parametrize("B,T,C", [(1, 1, 64), (2, 300, 72), (3, 20, 136)])
 def test_slices_of_one_projection(B, T, C):
