@@ -481,7 +481,7 @@ struct Ring {
 // ------------------------------------------------------------------------------ backward
 // part [gridDim.x][2 d]: each block's sums over its rows, dweight, then dbias.
 template <typename Tin, int NV, int Threads>
-__global__ void __launch_bounds__(Threads)
+__global__ void __launch_bounds__(Threads, Threads == 384 ? 2 : 1)
 layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ weight,
                            const float* __restrict__ mean, const float* __restrict__ rstd,
                            const Tin* dy, Tin* dx, float* __restrict__ part, long long rows, int d,
@@ -537,7 +537,8 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
 #pragma unroll
         for (int r = 0; r < kRingRows; ++r) {
             if (r < n_rows) {
-                const float2 r2 = bcast2(rs[r]), shift = bcast2(mu[r]);
+                // xh = x rstd - mean rstd: its rounding is of the size of the mean's own
+                const float2 r2 = bcast2(rs[r]), shift = bcast2(mu[r] * rs[r]);
                 float2 m1 = bcast2(0.f), m2 = m1;
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
@@ -551,7 +552,7 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
                         b.get(g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 xh = __fmul2_rn(__fadd2_rn(xv[e], shift), r2);
+                            const float2 xh = __ffma2_rn(xv[e], r2, shift);
                             dw[n][e] = __ffma2_rn(g[e], xh, dw[n][e]);
                             db[n][e] = __fadd2_rn(db[n][e], g[e]);
                             const float2 q = __fmul2_rn(g[e], w[n][e]);
@@ -571,10 +572,12 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
         Tin* dxp = dx + ring.row0(k) * d;
 #pragma unroll
         for (int r = 0; r < kRingRows; ++r) {
+            // dx = rstd (q - m1 - xh m2) as g (w rstd) + x k1 + k0
             const float n1 = __shfl_sync(0xffffffffu, t, 2 * r);
             const float n2 = __shfl_sync(0xffffffffu, t, 2 * r + 1);
             if (r < n_rows) {
-                const float2 r2 = bcast2(rs[r]), shift = bcast2(mu[r]);
+                const float2 r2 = bcast2(rs[r]), k1 = bcast2(n2 * rs[r] * rs[r]);
+                const float2 k0 = bcast2(rs[r] * fmaf(mu[r] * rs[r], n2, n1));
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     const int c = kVec * (tid + n * (int)blockDim.x);
@@ -586,11 +589,8 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
                         a.get(xv);
                         b.get(g);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 xh = __fmul2_rn(__fadd2_rn(xv[e], shift), r2);
-                            const float2 q = __ffma2_rn(g[e], w[n][e], bcast2(n1));
-                            g[e] = __fmul2_rn(__ffma2_rn(xh, bcast2(n2), q), r2);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            g[e] = __ffma2_rn(g[e], __fmul2_rn(w[n][e], r2), __ffma2_rn(xv[e], k1, k0));
                         store_vec(dxp + (long long)r * d + c, g);
                     }
                 }
@@ -776,7 +776,7 @@ layer_norm_backward_wide_kernel(const Tin* __restrict__ x, const float* __restri
 }
 
 // Shared memory for rings, per SM; beside it each block needs its sums and barriers.
-constexpr size_t kRoom = 216 * 1024;
+constexpr size_t kRoom = 212 * 1024;
 
 // Rows per group and slots of a ring whose rows take `row` bytes per slot, for `blocks` blocks per
 // SM: the most rows per group that leave `want` slots (a group's phases and one to fill).
@@ -859,19 +859,21 @@ struct BackwardPlan {
             grid = (unsigned)std::min<long long>(p.rows, std::max<long long>(1, 2 * device_sms() / across));
             return;
         }
-        // threads of 8 columns up to 768 of them, then 512 of up to 32; two slots of the most rows
-        // that fit
+        // 8 columns per thread up to 768 threads, several blocks per SM up to 384 and one above
+        // (6144 columns: 80 us in one block of 768 threads and four rows per group, 84 in two of
+        // 384 and two rows), then up to 32 columns in 512; fewer blocks where they would leave
+        // each a single row per group
         nv = vecs <= 768 ? 1 : vecs <= 1024 ? 2 : 4;
         threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
         const size_t row = 2 * sizeof(Tin) * p.d;  // x and dy
-        const RingShape ring(row, 1, 2);
+        int blocks = nv > 1 ? 1 : std::max(1, std::min(8, 768 / threads));
+        while (blocks > 1 && RingShape(row, blocks, 2).group_rows < 2) --blocks;
+        const RingShape ring(row, blocks, 2);
         group_rows = ring.group_rows;
         stages = ring.stages;
         smem = (size_t)stages * group_rows * row;
         const long long groups = (p.rows + group_rows - 1) / group_rows;
-        const long long blocks = std::max<long long>(
-            1, std::min<long long>((long long)(kRoom / (smem + 2048)), 1024 / threads));
-        grid = (unsigned)std::min<long long>(groups, blocks * device_sms());
+        grid = (unsigned)std::min<long long>(groups, (long long)blocks * device_sms());
     }
 };
 
@@ -903,10 +905,10 @@ cudaError_t backward(const LayerNormGrads& p, const BackwardPlan<Tin>& plan, flo
                                                                   p.rows, p.d);
         return cudaGetLastError();
     }
-    auto kernel = plan.nv == 2   ? layer_norm_backward_kernel<Tin, 2, 512>
-                  : plan.nv == 4 ? layer_norm_backward_kernel<Tin, 4, 512>
-                  : plan.threads <= 512 ? layer_norm_backward_kernel<Tin, 1, 512>
-                                        : layer_norm_backward_kernel<Tin, 1, 768>;
+    auto kernel = plan.nv == 4           ? layer_norm_backward_kernel<Tin, 4, 512>
+                  : plan.nv == 2         ? layer_norm_backward_kernel<Tin, 2, 512>
+                  : plan.threads <= 384 ? layer_norm_backward_kernel<Tin, 1, 384>
+                                         : layer_norm_backward_kernel<Tin, 1, 768>;
     const cudaError_t e = allow_smem((const void*)kernel, plan.smem);
     if (e != cudaSuccess) return e;
     kernel<<<plan.grid, plan.threads, plan.smem, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx, part,

@@ -69,7 +69,7 @@ def check(x, dy, w, b, dtype, eps=1e-5):
 @pytest.mark.parametrize("rows,d", [
     (1, 8), (5, 16), (33, 24), (300, 64), (17, 136), (1000, 256), (3, 264), (64, 512),
     (700, 1024), (1001, 1160), (31, 4096), (200, 6144), (3, 8192), (5, 8200), (2, 16384),
-    (3, 16392), (2, 32768)])
+    (3, 16392), (2, 32768), (601, 2056), (703, 4104), (1501, 6144), (640, 9216), (1201, 8200)])
 def test_against_oracle(rows, d, dtype):
     check(*make(rows, d, dtype, rows * 31 + d), dtype)
 
