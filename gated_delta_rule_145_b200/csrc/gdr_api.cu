@@ -646,7 +646,7 @@ const char* gdr_status_string(int status) {
         case GDR_ERR_SHAPE: return "GDR_ERR_SHAPE: inconsistent sizes";
         case GDR_ERR_UNSUPPORTED: return "GDR_ERR_UNSUPPORTED: head or chunk size not built";
         case GDR_ERR_ALIGN: return "GDR_ERR_ALIGN: misaligned pointer";
-        case GDR_ERR_OOM: return "GDR_ERR_OOM: the prefill workspace could not be allocated";
+        case GDR_ERR_OOM: return "GDR_ERR_OOM: the call's workspace could not be allocated";
         case GDR_ERR_CUDA: return "GDR_ERR_CUDA: kernel launch failed";
         case GDR_ERR_TIMEOUT: return "GDR_ERR_TIMEOUT: a kernel abandoned a bounded wait";
         case GDR_ERR_TOO_LARGE:

@@ -178,6 +178,19 @@ int device_sms();
 // once per kernel, device and size above the last one.
 cudaError_t allow_smem(const void* kernel, size_t bytes);
 
+// While it lives, this thread may make calls that a stream capture elsewhere would otherwise
+// forbid (creating the pool, asking for occupancy): they enqueue nothing, so a first call may
+// be captured.
+class CaptureRelaxed {
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+
+  public:
+    CaptureRelaxed() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    ~CaptureRelaxed() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    CaptureRelaxed(const CaptureRelaxed&) = delete;
+    CaptureRelaxed& operator=(const CaptureRelaxed&) = delete;
+};
+
 // The library's stream-ordered workspace pool (workspace.cu).
 cudaError_t workspace_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 

@@ -115,7 +115,8 @@ __device__ __forceinline__ float lane_sum(float v) {
 // registers as loaded (bf16 in pairs): no barrier, and a whole row of loads in flight per
 // warp; U rows at a time where rows are short.  (One block per row, eight values per thread and
 // two barriers, ran [8192, 6144] bf16 at 0.25 of HBM.)  Statistics, then y, re-expand the
-// registers.
+// registers.  [65536, 768] bf16 45 us (0.68 of a copy's rate), [393216, 128] 51 us (0.60):
+// bound by the shuffles and the scalar work of a row beside its few values.
 template <typename Tin, int NV>
 constexpr int kRawRegs = NV * (sizeof(Tin) == 2 ? 4 : 8);
 template <typename Tin, int NV>
@@ -209,8 +210,10 @@ layer_norm_kernel(const Tin* x, const float* __restrict__ weight, const float* _
 
 // Wide rows: a team of one to six warps (the block) per U rows, NV vectors per thread and row, so
 // that a thread's share stays small enough for many teams per SM and each load of the
-// parameters serves U rows.  (A warp per row: 64 us at [8192, 6144] bf16, with 12 warps per SM
-// and the parameters' loads twice the row's; its next row staged in shared memory: 72.)
+// parameters serves U rows.  [8192, 6144] bf16 takes 39 us (5.2 TB/s, 0.79 of a copy's rate;
+// two thirds of the issue slots are used), [8192, 4096] fp32 51 us (0.80).  (A warp per row:
+// 64 us at [8192, 6144] bf16, with 12 warps per SM and the parameters' loads twice the row's;
+// its next row staged in shared memory: 72.)
 template <typename Tin>
 constexpr int kTeamRows = sizeof(Tin) == 2 ? 2 : 1;
 
@@ -397,14 +400,15 @@ layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
     }
 }
 
-// Wide rows, forward and backward: thread -> kVec columns (NV times) of all its block's rows, so
-// that the parameters, and backward the columns' sums, stay in registers.  The block takes
-// groups of up to kRingRows rows from a ring in shared memory (bulk copies: rows are
-// contiguous), so the bytes in flight depend neither on registers nor on barriers.  A group
-// passes through its phases in consecutive iterations (sum, centred sum, output; backward:
-// both sums, output), so one barrier per iteration serves them all, and a phase's sums are
-// there when the next one starts.  (A warp per row re-read the parameters for every row: at
-// [8192, 6144] bf16 their four times larger L1 traffic held it at 0.46 of HBM.)
+// Backward, wide rows: thread -> kVec columns (NV times) of all its block's rows, so that the
+// weight and the columns' sums stay in registers.  The block takes groups of up to kRingRows
+// rows from a ring in shared memory (bulk copies: rows are contiguous), so the bytes in flight
+// depend neither on registers nor on barriers; the values are expanded again after the
+// barrier behind the two sums of each row instead of being held.  [8192, 6144] bf16 takes
+// 71 us (0.65 of a copy's rate), [8192, 4096] fp32 87 us (0.71): the two barriers of a group
+// and the sums between them, which one block per SM cannot overlap.  (Both phases of two
+// groups per barrier: 98 us; a column's sums over a warp's rows by shared-memory atomics
+// would add in no fixed order.)
 constexpr int kRingRows = 4;
 
 // Adds v[0 .. 7] over the warp: lane l ends with the sum of v[l % 8].  Each exchange halves
@@ -618,6 +622,7 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
 }
 
 // Narrow rows (d <= 256): L adjacent lanes per row, one vector each, U rows of loads in flight.
+// [393216, 128] bf16 64 us (0.72 of a copy's rate).
 constexpr int kNarrowThreads = 256, kNarrowRows = 4;
 
 template <typename Tin, int L>

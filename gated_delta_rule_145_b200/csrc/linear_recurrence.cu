@@ -154,7 +154,8 @@ __device__ __forceinline__ void store_grads(const GradFactors& f, float2 D, Tin*
 // ------------------------------------------------------------- sequential form
 // Thread -> two channels of the sequences s = blockIdx.y, + gridDim.y, ...; one token after
 // the other, the state in registers.  For single tokens and short sequences, where there is
-// nothing to split.
+// nothing to split.  One token of 64 sequences x 6144 channels takes 4 us, bound by the
+// latency of three dependent loads; 32 tokens 31 us (0.62 of a copy's rate).
 constexpr int kSeqThreads = 128;
 
 template <typename Tin>
@@ -232,7 +233,14 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
 // each warp forms (P, H) of its tokens from zero, the CTA composes its warps' pairs through
 // shared memory, the cluster its CTAs' through distributed shared memory, and every warp
 // then runs its tokens once more from its true start state and stores them.  Nothing is
-// read twice and no CTA waits for one outside its cluster.
+// read twice.
+//
+// What bounds it (B200, bf16): with every SM at work the steady state reads and writes at
+// 5.9 TB/s (0.9 of a copy), where the special-function unit is 46 % busy (eight operations
+// per token and channel pair) and half the issue slots are used; a call loses the rest to
+// its last wave, to CTA starts and to the exchanges.  Forward [8, 1024, 6144] 100 us (0.77
+// of a copy's rate), [1, 8192, 6144] 120 us (0.64), [1, 65536, 1024] 177 us (0.58);
+// backward 207 us (0.74), 223 us (0.69), 358 us (0.57).
 //
 // Decays are composed as sums of log-decays.  From tile to tile a factor P near 1 acts
 // through W = P - 1, formed as expm1 of its tile's sum: a slow channel's state lasts over
@@ -392,6 +400,7 @@ __device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int lan
         }
         __syncwarp();
         const uint32_t K = cluster_size(), rank = cluster_rank();
+#pragma unroll 4
         for (uint32_t k = 0; k < K; ++k) {
             if (k == rank) in = S;
             const float4 v = sm.peer[step & 3][k][lane];
@@ -895,6 +904,7 @@ cudaError_t clusters_held(Capacity& held, Kernel kernel, int threads, size_t sme
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    CaptureRelaxed relaxed;
     e = allow_smem((const void*)kernel, smem);
     if (e == cudaSuccess && K > 8)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1027,12 +1037,14 @@ void offer_single(Plan* plan, const RecurrenceParams& p) {
         offer(plan, p, kManyForm, 1, 2LL * sms, F::Many::kRows, F::kMany, F::kSharedStart, false);
 }
 
-// The sequential form's time: a chain of tokens, each at least a memory latency and at least its
-// bytes' time.  Against a plan's, which it beats for short sequences (64 sequences of 6144
-// channels, forward: 31 against 82 us at 32 tokens, 117 against 134 at 128; one sequence: 16
-// against 8 at 16).
-double seq_time(const RecurrenceParams& p, double latency_ns, double channel_ns) {
-    return mean_length(p) * std::max(latency_ns, channel_ns * p.nseq * p.C);
+// Whether the sequential form is the faster one: a chain of tokens, each at least a memory latency
+// and at least its bytes' time, against a plan.  It is for short sequences (64 sequences of
+// 6144 channels, forward: 31 against 82 us at 32 tokens, 117 against 134 at 128; one
+// sequence: 16 against 8 at 16).  Of packed sequences only the mean length is known here; one
+// that holds most of the tokens may cost the sequential form at most 20 times a plan.
+bool sequential(const RecurrenceParams& p, const Plan& plan, double latency_ns, double channel_ns) {
+    if (p.cu_seqlens && p.T * latency_ns > 20 * plan.time) return false;
+    return mean_length(p) * std::max(latency_ns, channel_ns * p.nseq * p.C) < plan.time;
 }
 
 // A split schedule's counters and states in `ws`, the counters set to zero.
@@ -1105,7 +1117,7 @@ cudaError_t forward(const RecurrenceParams& p, cudaStream_t stream) {
     static Capacity wide, pair;
     Plan plan = {};
     offer_single<F>(&plan, p);
-    if (seq_time(p, 620, 0.0023) < plan.time) {
+    if (sequential(p, plan, 620, 0.0023)) {
         const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads),
                         (unsigned)std::min(p.nseq, 65535));
         recurrence_seq_kernel<Tin><<<grid, kSeqThreads, 0, stream>>>(p);
@@ -1133,7 +1145,7 @@ cudaError_t backward(const RecurrenceParams& p, const RecurrenceGrads& r, cudaSt
     static Capacity wide, pair;
     Plan plan = {};
     offer_single<F>(&plan, p);
-    if (seq_time(p, 750, 0.0038) < plan.time) {
+    if (sequential(p, plan, 750, 0.0038)) {
         const int rows = seq_rows(p);
         float* part = nullptr;
         cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);

@@ -128,19 +128,22 @@ union ConvBackwardSmem {
     float sums[kGWarps][5][kGCh];
 };
 
-// CTA -> (channel tile, group of 8 segments of the B * nseg segments); warp -> segment of
+// CTA -> (channel tile, group of 8 segments of the B * nseg segments); warp -> segments of
 // `seg` tokens, lane -> four channels, one token after the other, its loads two batches
 // ahead (held in registers, one batch at a time, the loads' latency showed: 0.6 of HBM).
+// [1, 8192, 18432] takes 193 us (0.72 of a copy's rate, 4.7 TB/s), [8, 2048, 4096] 97 us (0.64):
+// 102 instructions per token and four channels use 57 % of the issue slots, the paired fp32
+// pipe more, and the segments' ends and one wave's uneven SMs take the rest.
 // part [groups][5 C]: the taps' sums as [C][4], then the bias's.
+template <bool Loop>
 __global__ void __launch_bounds__(32 * kGWarps, 2)
-conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, float* part) {
+conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float* part) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     ConvBackwardSmem& smem = *reinterpret_cast<ConvBackwardSmem*>(smem_raw);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int ct = blockIdx.x % nct, group = blockIdx.x / nct;
     const int c = ct * kGCh + 4 * lane;
-    const long long sid = (long long)group * kGWarps + warp;
-    const bool live = c < p.C && sid < (long long)p.B * nseg;
+    const long long segments = c < p.C ? (long long)p.B * nseg : 0;
     const float2 zero = splat(0.f);
     ConvLane a[2];
 #pragma unroll
@@ -149,7 +152,9 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, float* part) {
 #pragma unroll
         for (int i = 0; i < kW; ++i) a[k].sum_w[i] = zero;
     }
-    if (live) {
+    // this warp's segments: one, unless (Loop) there are more than the grid's groups take
+    for (long long sid = (long long)group * kGWarps + warp; sid < segments;
+         sid = Loop ? sid + (long long)groups * kGWarps : segments) {
         const int b = (int)(sid / nseg), T = p.T, C = p.C;
         const int t0 = (int)(sid % nseg) * seg, t1 = min(T, t0 + seg);
         const size_t base = (size_t)b * T * C + c;
@@ -165,6 +170,7 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, float* part) {
             a[k].w[1] = make_float2(u.y, v.y);
             a[k].w[2] = make_float2(u.z, v.z);
             a[k].w[3] = make_float2(u.w, v.w);
+            a[k].d0 = a[k].d1 = a[k].d2 = zero;
             a[k].bias = p.bias ? make_float2(p.bias[c + 2 * k], p.bias[c + 2 * k + 1]) : zero;
         }
         // the three inputs before the segment: x, or the state (oldest first)
@@ -307,7 +313,8 @@ __device__ __forceinline__ void store_z4(__nv_bfloat16* p, const float (&z)[4]) 
 }
 
 // L = d / 4 adjacent lanes share a row, four values each; a warp takes 32 / L rows at a
-// time, grid-stride.  part [gridDim.x][d].
+// time, grid-stride.  part [gridDim.x][d].  [393216, 128] with a bf16 gate takes 140 us with its
+// column sums (0.88 of a copy's rate), the kernel alone 0.94: memory bounds it.
 template <typename Tz, int D>
 __global__ void __launch_bounds__(kNThreads)
 gated_rmsnorm_backward_kernel(NormGrads p, float* part) {
@@ -410,15 +417,18 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
         const long long cost = (ctas + slots - 1) / slots * (std::min<long long>(len, p.T) + 24);
         if (!seg || cost < best) seg = (int)len, nseg = (int)n, best = cost;
     }
-    const long long groups = ((long long)p.B * nseg + kGWarps - 1) / kGWarps;
+    // at most eight waves of CTAs, which bounds the partial sums too
+    const long long all = ((long long)p.B * nseg + kGWarps - 1) / kGWarps;
+    const long long groups = std::min(all, std::max<long long>(1, 8 * slots / nct));
     if (groups * nct > 0x7fffffffLL) return cudaErrorNotSupported;
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * groups * 5 * p.C, stream);
     if (e != cudaSuccess) return e;
-    e = allow_smem((const void*)conv_backward_kernel, sizeof(ConvBackwardSmem));
+    auto kernel = groups < all ? conv_backward_kernel<true> : conv_backward_kernel<false>;
+    e = allow_smem((const void*)kernel, sizeof(ConvBackwardSmem));
     if (e == cudaSuccess) {
-        conv_backward_kernel<<<(unsigned)(groups * nct), 32 * kGWarps, sizeof(ConvBackwardSmem),
-                               stream>>>(p, nct, nseg, seg, part);
+        kernel<<<(unsigned)(groups * nct), 32 * kGWarps, sizeof(ConvBackwardSmem), stream>>>(
+            p, nct, nseg, seg, (int)groups, part);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess)

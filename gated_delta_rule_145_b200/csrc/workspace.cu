@@ -63,6 +63,7 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
     for (int i = 0; i < used && !at; ++i)
         if (table[i].kernel == kernel && table[i].dev == dev) at = &table[i];
     if (at && at->bytes >= bytes) return cudaSuccess;
+    CaptureRelaxed relaxed;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     if (!at && used < kEntries) at = &table[used++];
@@ -78,6 +79,7 @@ cudaError_t workspace_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
     PoolSet& ps = pools();
     std::lock_guard<std::mutex> lock(ps.mu);
     if (!ps.made[dev]) {
+        CaptureRelaxed relaxed;
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;

@@ -77,7 +77,7 @@ typedef void* gdr_stream_t; /* cudaStream_t */
 #define GDR_ERR_SHAPE (-2)       /* B, T, Hk, Hv inconsistent (e.g. Hv % Hk != 0) */
 #define GDR_ERR_UNSUPPORTED (-3) /* head size or chunk size not built */
 #define GDR_ERR_ALIGN (-4)       /* a pointer is not aligned as stated above */
-#define GDR_ERR_OOM (-5)         /* the prefill workspace could not be allocated */
+#define GDR_ERR_OOM (-5)         /* the call's workspace could not be allocated */
 #define GDR_ERR_CUDA (-6)        /* a kernel launch failed */
 #define GDR_ERR_TIMEOUT (-7)     /* a kernel gave up a bounded on-chip wait (see below) */
 #define GDR_ERR_TOO_LARGE (-8)   /* more workspace than gdr_prefill_chunked_noalloc's scratch */
@@ -476,7 +476,8 @@ GDR_API int gdr_linear_recurrence_backward_f32(
 /*
  * Device-side status of the kernels enqueued so far.  Synchronises `stream`, then returns
  * GDR_ERR_TIMEOUT if any tensor-core prefill kernel (or the TMA-fed convolution that
- * gdr_short_conv_silu runs for T >= 256) abandoned one of its bounded waits
+ * gdr_short_conv_silu runs for T >= 256, a tiled kernel of gdr_linear_recurrence or its backward
+ * call, or gdr_layer_norm_backward on rows above 256) abandoned one of its bounded waits
  * (each wait on an mbarrier gives up after 2 s, records the event and lets the kernel
  * exit instead of hanging), GDR_ERR_CUDA if the stream reports an error, else GDR_OK.
  * The timeout record is cleared by the call.

@@ -66,7 +66,8 @@ def conv_check(m, got):
 
 # lengths below the taps, around a warp's segment and a CTA's rows; channel tails of 8
 CONV = [(1, 1, 8), (2, 2, 16), (3, 3, 64), (2, 4, 128), (1, 61, 136), (2, 64, 96), (1, 65, 1160),
-        (2, 67, 8), (3, 200, 64), (1, 511, 128), (2, 777, 1160), (1, 2100, 72), (70, 5, 64)]
+        (2, 67, 8), (3, 200, 64), (1, 511, 128), (2, 777, 1160), (1, 2100, 72), (70, 5, 64),
+        (20001, 3, 8)]  # more segments than a grid takes at once
 
 
 @gpu
