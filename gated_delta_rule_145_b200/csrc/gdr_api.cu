@@ -404,7 +404,7 @@ int gdr_short_conv_silu_backward(const void* x, const float* weight, const float
                                  float* grad_conv_state_in, int B, int T, int C, int width,
                                  gdr_stream_t stream) {
     if (!weight || (T > 0 && (!x || !grad_y || !grad_x))) return GDR_ERR_NULL;
-    if (B < 1 || T < 0 || C < 8 || C % 8 != 0) return GDR_ERR_SHAPE;
+    if (B < 1 || T < 0 || T > 0x7fffff00 || C < 8 || C % 8 != 0) return GDR_ERR_SHAPE;
     if (width != 4) return GDR_ERR_UNSUPPORTED;
     if ((long long)B * C * ((long long)T + 64) > 0x3fffffffffffLL || 5LL * C > 0x7fffffffLL ||
         (long long)B * (((long long)T + 63) / 64) > 0x7fffffLL)

@@ -354,7 +354,7 @@ GDR_API int gdr_gated_rmsnorm_f32(const float* o, const float* z, const float* w
  *                                                      [B, C, 3] fp32, NULL to skip
  * grad_conv_state_out [B, C, 3] fp32 (NULL = zeros) is the gradient of the state after the
  * call; it is added to the inputs that this state holds.  Sizes and alignment as for
- * gdr_short_conv_silu; B * ceil(T / 64) below 2^23.  grad_x must not overlap any input, nor
+ * gdr_short_conv_silu; T below 2^31 - 256, B * ceil(T / 64) below 2^23.  grad_x must not overlap any input, nor
  * grad_conv_state_in grad_conv_state_out.
  */
 GDR_API int gdr_short_conv_silu_backward(const void* x, const float* weight, const float* bias,

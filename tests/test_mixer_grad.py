@@ -193,7 +193,8 @@ def test_conv_refusals():
 
     for p in ("x", "weight", "grad_y", "grad_x"):
         assert call(**{p: None}) == gdr.GDR_ERR_NULL, p
-    for kw in (dict(B=0), dict(T=-1), dict(C=0), dict(C=60), dict(B=1 << 24, T=64)):
+    for kw in (dict(B=0), dict(T=-1), dict(C=0), dict(C=60), dict(B=1 << 24, T=64),
+               dict(T=2 ** 31 - 1, C=8)):
         assert call(**kw) == gdr.GDR_ERR_SHAPE, kw
     assert call(width=3) == gdr.GDR_ERR_UNSUPPORTED
     for p in ("x", "grad_y", "grad_x", "weight"):
