@@ -565,6 +565,10 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
         if (Cluster) __syncthreads();  // the part before is done with its tiles
         if (threadIdx.x == 0 && !dead)
             for (int i = 0; i < STAGES; ++i) load_next();
+        // The state has arrived in every lane before any barrier or exchange that lets another warp
+        // write the final one, which may be the same memory.
+        S.x = __shfl_sync(0xffffffffu, S.x, w.lane);
+        S.y = __shfl_sync(0xffffffffu, S.y, w.lane);
         // the run from zero, up to the exchange
         auto read_tile = [&](int step, Held& k) {
             const int st = taken % STAGES, buf = turn & 1, live = live_of(first_of(step));
@@ -724,6 +728,10 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
         if (Cluster) __syncthreads();  // the part before is done with its tiles
         if (threadIdx.x == 0 && !dead)
             for (int i = 0; i < STAGES; ++i) load_next();
+        // The state has arrived in every lane before any barrier or exchange that lets another warp
+        // write the final one, which may be the same memory.
+        S.x = __shfl_sync(0xffffffffu, S.x, w.lane);
+        S.y = __shfl_sync(0xffffffffu, S.y, w.lane);
         // the states before a step's tokens of this warp: last, last - 1, ...
         float2 prev[TOK];
         auto load_prev = [&](int step) {

@@ -299,6 +299,31 @@ def test_steps_continue_a_prompt_in_place(T0):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,T,C", [(70, 3, 136), (300, 150, 64), (2, 5000, 64), (3, 3000, 2048)])
+def test_a_state_in_place_has_the_bits_of_one_apart(B, T, C, dtype):
+    """final_state may be init_state and grad_init_state grad_final_state: one CTA, clusters,
+    and units cut between clusters"""
+    g = torch.Generator(device="cuda").manual_seed(B + T)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    x, a, b = (r(B, T, C).to(dtype) for _ in range(3))
+    A, dt, init, gf, go = r(C), r(C), r(B, C), r(B, C), r(B, T, C)
+    out, final = gdr.linear_recurrence(x, a, b, A, dt, init)
+    apart = gdr.linear_recurrence_backward(x, a, b, A, dt, out, go, gf, init)
+    state, grad = init.clone(), gf.clone()
+    again, _ = gdr.linear_recurrence(x, a, b, A, dt, state, final_state=state)
+    call = gdr.gdr_linear_recurrence_backward if dtype is torch.bfloat16 else \
+        gdr.gdr_linear_recurrence_backward_f32
+    dx, da, db = (torch.empty_like(x) for _ in range(3))
+    dA, ddt = torch.empty_like(A), torch.empty_like(dt)
+    call(x, a, b, A, dt, init, out, go, grad, dx, da, db, dA, ddt, grad, None, B, T, C, C, C)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out) and torch.equal(state, final)
+    for name, p, q in zip(NAMES[2:], (dx, da, db, dA, ddt, grad), apart):
+        assert torch.equal(p, q), name
+
+
+@gpu
 def test_no_tokens():
     C = 64
     e = torch.empty((2, 0, C), device="cuda", dtype=torch.bfloat16)
