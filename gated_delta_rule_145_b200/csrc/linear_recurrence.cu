@@ -881,7 +881,7 @@ int seq_rows(const RecurrenceParams& p) {
 
 // The tokens of a call's mean sequence; the host does not know packed sequences' lengths.
 int mean_length(const RecurrenceParams& p) {
-    return p.cu_seqlens ? (p.T + p.nseq - 1) / p.nseq : p.T;
+    return p.cu_seqlens ? (int)(((long long)p.T + p.nseq - 1) / p.nseq) : p.T;
 }
 
 // (sequence, strip of channels) pairs, each one chain of tiles.
@@ -900,8 +900,8 @@ cudaError_t clusters_held(Capacity& held, Kernel kernel, int threads, size_t sme
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
     if (e != cudaSuccess) return e;
-    *fit = held.fit[dev][K].load();
-    if (*fit > 0) return cudaSuccess;
+    *fit = held.fit[dev][K].load();  // 0: not asked yet, -1: none
+    if (*fit != 0) return cudaSuccess;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)K;
@@ -917,7 +917,12 @@ cudaError_t clusters_held(Capacity& held, Kernel kernel, int threads, size_t sme
     if (e == cudaSuccess && K > 8)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(fit, kernel, &cfg);
-    if (e == cudaSuccess) held.fit[dev][K].store(*fit = std::max(*fit, 1));
+    if (e != cudaSuccess && K > 8) {  // a device without clusters of this size
+        cudaGetLastError();
+        e = cudaSuccess;
+        *fit = 0;
+    }
+    if (e == cudaSuccess) held.fit[dev][K].store(*fit = *fit > 0 ? *fit : -1);
     return e;
 }
 
@@ -953,6 +958,7 @@ cudaError_t offer_clusters(Plan* plan, const RecurrenceParams& p, int form, Kern
         int fit = 0;
         const cudaError_t e = clusters_held(held, kernel, 32 * Smem::WARPS, sizeof(Smem), K, &fit);
         if (e != cudaSuccess) return e;
+        if (fit < 1) break;
         offer(plan, p, form, K, fit, (long long)K * Smem::kRows, ns + K * ns_per_rank, start_ns, true);
     }
     return cudaSuccess;
