@@ -30,10 +30,10 @@ __device__ __forceinline__ float rcpg(float x) {
     return y;
 }
 
-// The larger value; NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The smaller value; NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 
@@ -66,28 +66,35 @@ __device__ __forceinline__ float2 bf2(uint32_t u) {
 }
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 // Two adjacent channels walking along time: the taps, the three inputs and the three ds before
-// the current token, and the sums of the parameters' gradients.
+// the current token, and the sums of the parameters' gradients.  Taps and bias are held times
+// -log2 e, so that they give the exponent m = -s log2 e of the sigmoid; ds times -ln 2, so
+// that dx, of products of a tap and a ds, needs no scale, and the sums one at the end.
 struct ConvLane {
     float2 w[kW], bias;
     float2 h0, h1, h2;  // x at t - 3, t - 2, t - 1
     float2 d0, d1, d2;  // ds likewise
     float2 sum_w[kW], sum_b;
 
-    // ds of the token with input v and output gradient g
+    // ds of the token with input v and output gradient g, times -ln 2
     __device__ __forceinline__ float2 slope(float2 v, float2 g) const {
-        float2 s = __ffma2_rn(w[0], h0, bias);
-        s = __ffma2_rn(w[1], h1, s);
-        s = __ffma2_rn(w[2], h2, s);
-        s = __ffma2_rn(w[3], v, s);
-        // SiLU'(s) = r (1 + s (1 - r)), r = sigmoid(s) = 1 / den.  Below -41 it is under 2^-53 in
-        // magnitude; there s is taken as -41, so that the two channels' den stay finite when
-        // multiplied: one reciprocal, the pass's scarcest instruction, serves both.  NaN stays.
-        s = make_float2(max_nan(s.x, -41.f), max_nan(s.y, -41.f));
-        const float2 m = __fmul2_rn(s, splat(-1.4426950408889634f));
-        const float2 den = __fadd2_rn(make_float2(ex2g(m.x), ex2g(m.y)), splat(1.f));
+        float2 m = __ffma2_rn(w[0], h0, bias);
+        m = __ffma2_rn(w[1], h1, m);
+        m = __ffma2_rn(w[2], h2, m);
+        m = __ffma2_rn(w[3], v, m);
+        // SiLU'(s) = r (1 + s (1 - r)), r = sigmoid(s) = 1 / den, den = 1 + 2^m.  Below s = -41 it
+        // is under 2^-53 in magnitude; there s is taken as -41 (m as 59.15), so that the two
+        // channels' den stay finite when multiplied: one reciprocal, the pass's scarcest
+        // instruction, serves both.  A NaN stays in its channel: the first minimum keeps it, the
+        // second drops it for den.
+        m = make_float2(min_nan(m.x, 59.15f), min_nan(m.y, 59.15f));
+        const float2 den = __fadd2_rn(make_float2(ex2g(fminf(m.x, 59.15f)), ex2g(fminf(m.y, 59.15f))),
+                                      splat(1.f));
         const float2 r = __fmul2_rn(splat(rcpg(den.x * den.y)), make_float2(den.y, den.x));
-        const float2 q = __ffma2_rn(s, __ffma2_rn(r, splat(-1.f), splat(1.f)), splat(1.f));
+        const float2 q = __ffma2_rn(m, __ffma2_rn(r, splat(-kLn2 * kLn2), splat(kLn2 * kLn2)),
+                                    splat(-kLn2));
         return __fmul2_rn(g, __fmul2_rn(r, q));
     }
     __device__ __forceinline__ void add(float2 v, float2 d) {
@@ -166,12 +173,14 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float*
         for (int k = 0; k < 2; ++k) {
             const float4 u = *reinterpret_cast<const float4*>(p.weight + (size_t)(c + 2 * k) * kW);
             const float4 v = *reinterpret_cast<const float4*>(p.weight + (size_t)(c + 2 * k + 1) * kW);
-            a[k].w[0] = make_float2(u.x, v.x);
-            a[k].w[1] = make_float2(u.y, v.y);
-            a[k].w[2] = make_float2(u.z, v.z);
-            a[k].w[3] = make_float2(u.w, v.w);
+            a[k].w[0] = __fmul2_rn(make_float2(u.x, v.x), splat(-kLog2e));
+            a[k].w[1] = __fmul2_rn(make_float2(u.y, v.y), splat(-kLog2e));
+            a[k].w[2] = __fmul2_rn(make_float2(u.z, v.z), splat(-kLog2e));
+            a[k].w[3] = __fmul2_rn(make_float2(u.w, v.w), splat(-kLog2e));
             a[k].d0 = a[k].d1 = a[k].d2 = zero;
-            a[k].bias = p.bias ? make_float2(p.bias[c + 2 * k], p.bias[c + 2 * k + 1]) : zero;
+            a[k].bias = p.bias ? __fmul2_rn(make_float2(p.bias[c + 2 * k], p.bias[c + 2 * k + 1]),
+                                            splat(-kLog2e))
+                               : zero;
         }
         // the three inputs before the segment: x, or the state (oldest first)
         float2 h[3][2];
@@ -290,7 +299,7 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float*
         float s = 0.f;
 #pragma unroll
         for (int wi = 0; wi < kGWarps; ++wi) s += sm[wi][i][ch];
-        row[i < kW ? (size_t)cc * kW + i : (size_t)kW * p.C + cc] = s;
+        row[i < kW ? (size_t)cc * kW + i : (size_t)kW * p.C + cc] = s * -kLog2e;
     }
 }
 

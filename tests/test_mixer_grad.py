@@ -102,6 +102,27 @@ def test_conv_chained_through_the_state_is_one_call(T0):
 
 
 @gpu
+@pytest.mark.parametrize("T", [9, 300])
+def test_conv_nan_and_infinity_stay_in_their_channels(T):
+    """two channels share a reciprocal: its rounding (within the tolerances) depends on both, but
+    a NaN or an infinite sum of one is not the other's"""
+    m = conv_case(2, T, 72, True, True, seed=4)
+    m["x"][0, 4, 3] = np.nan
+    m["x"][1, 5, 8] = np.inf
+    m["dy"][0, 6, 20] = np.nan
+    m["bias"][31] = -np.inf
+    m["bias"][40] = np.nan
+    got = conv_gpu(m)
+    torch.cuda.synchronize()
+    keep = np.array([c for c in range(72) if c not in (3, 8, 20, 31, 40)])
+    at = torch.from_numpy(keep).cuda()
+    axis = dict(x=2, w=0, dy=2, bias=0, state=1, ds=1)
+    conv_check({k: v.take(keep, axis[k]) for k, v in m.items()},
+               [v.index_select(d, at) for v, d in zip(got, (2, 0, 0, 1))])
+    assert torch.isnan(got[0][0, 4, 3]) and torch.isnan(got[2][[3, 20, 40]]).all()
+
+
+@gpu
 def test_conv_of_no_tokens_and_skipped_outputs():
     e = torch.empty(2, 0, 16, device="cuda", dtype=torch.bfloat16)
     w, ds = torch.ones(16, 4, device="cuda"), torch.randn(2, 16, 3, device="cuda")
