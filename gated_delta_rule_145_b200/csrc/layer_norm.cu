@@ -576,12 +576,12 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
         Tin* dxp = dx + ring.row0(k) * d;
 #pragma unroll
         for (int r = 0; r < kRingRows; ++r) {
-            // dx = rstd (q - m1 - xh m2) as g (w rstd) + x k1 + k0
+            // dx = rstd (q - m1 - xh m2) as rstd (g w + x k1 + k0); rstd^2 could overflow
             const float n1 = __shfl_sync(0xffffffffu, t, 2 * r);
             const float n2 = __shfl_sync(0xffffffffu, t, 2 * r + 1);
             if (r < n_rows) {
-                const float2 r2 = bcast2(rs[r]), k1 = bcast2(n2 * rs[r] * rs[r]);
-                const float2 k0 = bcast2(rs[r] * fmaf(mu[r] * rs[r], n2, n1));
+                const float2 r2 = bcast2(rs[r]), k1 = bcast2(n2 * rs[r]);
+                const float2 k0 = bcast2(fmaf(mu[r] * rs[r], n2, n1));
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     const int c = kVec * (tid + n * (int)blockDim.x);
@@ -594,7 +594,7 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
                         b.get(g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            g[e] = __ffma2_rn(g[e], __fmul2_rn(w[n][e], r2), __ffma2_rn(xv[e], k1, k0));
+                            g[e] = __fmul2_rn(__ffma2_rn(g[e], w[n][e], __ffma2_rn(xv[e], k1, k0)), r2);
                         store_vec(dxp + (long long)r * d + c, g);
                     }
                 }

@@ -95,6 +95,31 @@ def test_without_bias_far_mean_constant_rows_and_large_values():
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 1160, 6144, 20480])
+def test_a_variance_whose_inverse_no_float_holds(d):
+    """no eps and values of 1e-18: rstd times a gradient of 1e6 is a float, rstd^2 times it none"""
+    x, dy, w, b = make(21, d, "f32", 8, scale=1e-18)
+    check(x, dy * np.float32(1e6), w, b, "f32", 0.0)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 1160, 20480])
+def test_a_gradient_of_nan_stays_in_its_row(d):
+    x, dy, w, b = make(40, d, "f32", 9)
+    xd, wd = dev(x), dev(w)
+    _, mean, rstd = gdr.layer_norm(xd, wd)
+    clean = gdr.layer_norm_backward(xd, wd, mean, rstd, dev(dy))
+    dy[6, 5] = np.nan
+    dy[13, 2] = np.inf
+    got = gdr.layer_norm_backward(xd, wd, mean, rstd, dev(dy))
+    rows = [i for i in range(40) if i not in (6, 13)]
+    cols = [i for i in range(d) if i not in (5, 2)]
+    assert torch.equal(clean[0][rows], got[0][rows])
+    assert torch.isnan(got[0][6]).all() and torch.isnan(got[1][5]) and torch.isnan(got[2][5])
+    assert torch.equal(clean[1][cols], got[1][cols]) and torch.equal(clean[2][cols], got[2][cols])
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 1160])
 def test_a_row_of_nan_stays_alone(d):
     x, dy, w, b = make(40, d, "f32", 6)
