@@ -143,10 +143,16 @@ def _stream(s):
     return s if isinstance(s, int) else s.cuda_stream
 
 
+_INT_MAX = 0x7fffffff
+
+
 def _call(name, ptrs, ints, stream, check):
     fn = getattr(_lib or library(), name)
-    status = fn(*[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs],
-                *map(int, ints), _stream(stream))
+    if max(ints) > _INT_MAX or min(ints) < -_INT_MAX:  # ctypes would drop the upper bits
+        status = GDR_ERR_SHAPE
+    else:
+        status = fn(*[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs],
+                    *map(int, ints), _stream(stream))
     if check and status != GDR_OK:
         raise GdrError(name, status)
     return status
@@ -279,9 +285,12 @@ def gdr_short_conv_silu(x, weight, bias, conv_state_in, conv_state_out, y, B, T,
 
 def _rows_call(name, ptrs, rows, d, rest, stream, check):
     """A row-wise call: pointers, then rows, d and what follows them (eps)."""
-    status = getattr(_lib or library(), name)(
-        *[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs], int(rows), int(d),
-        *rest, _stream(stream))
+    fn = getattr(_lib or library(), name)
+    if not -_INT_MAX <= d <= _INT_MAX or not -1 << 62 < rows < 1 << 62:  # as in _call
+        status = GDR_ERR_SHAPE
+    else:
+        status = fn(*[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs],
+                    int(rows), int(d), *rest, _stream(stream))
     if check and status != GDR_OK:
         raise GdrError(name, status)
     return status

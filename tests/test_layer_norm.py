@@ -204,6 +204,8 @@ def test_refusals(suffix):
         assert call(d=32776) == gdr.GDR_ERR_UNSUPPORTED
         for p in ("x", "weight"):
             assert call(**{p: A + 8}) == gdr.GDR_ERR_ALIGN, p
+    # sizes that would wrap to others
+    assert fwd(d=2 ** 32 + 64) == gdr.GDR_ERR_SHAPE == bwd(rows=2 ** 64 + 4)
     assert fwd(eps=-1.0) == gdr.GDR_ERR_SHAPE and fwd(eps=float("nan")) == gdr.GDR_ERR_SHAPE
     assert fwd(bias=A + 4) == gdr.GDR_ERR_ALIGN and fwd(y=A + 4) == gdr.GDR_ERR_ALIGN
     assert bwd(grad_y=A + 8) == gdr.GDR_ERR_ALIGN and bwd(grad_x=A + 8) == gdr.GDR_ERR_ALIGN

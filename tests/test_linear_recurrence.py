@@ -443,6 +443,12 @@ def test_refusals(call, suffix):
         assert call(name, ld_grad=68) == gdr.GDR_ERR_SHAPE
 
 
+@pytest.mark.parametrize("kw", [dict(T=2 ** 32 + 16), dict(C=2 ** 32 + 64), dict(B=2 ** 32 + 1),
+                                dict(T=-2 ** 32 + 16)])
+def test_sizes_that_would_wrap_to_others_are_refused(kw):
+    assert _fwd(**kw) == gdr.GDR_ERR_SHAPE and _bwd(**kw) == gdr.GDR_ERR_SHAPE
+
+
 def test_binding_refuses_cpu_tensors():
     x, p = torch.zeros(1, 4, 8), torch.zeros(8)
     with pytest.raises(ValueError, match="CUDA"):
