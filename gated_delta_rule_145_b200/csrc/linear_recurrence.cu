@@ -113,41 +113,39 @@ __device__ __forceinline__ void seq_bounds(const int32_t* cu, int s, int T, long
     }
 }
 
-// One token's backward step on two channels: its decay (and its base-2 logarithm y), and the
-// factors of D, the gradient of its h, in dx, db, da and (times log2 e) dA_log, from the
-// inputs and the state before the token.  sigmoid(v) is r = 1 / (1 + t) for v >= 0 and t r
-// below, t = e^{-|v|}, so that small values keep their relative accuracy; sigmoid(v) (1 -
-// sigmoid(v)) is t r^2 for both signs.  Both forms of the backward pass use it, so they agree
-// bit for bit where they add in the same order.
-struct GradFactors {
-    float2 lam, x, b, a, A;
-};
-__device__ __forceinline__ GradFactors grad_factors(float2 x, float2 a, float2 b, float2 prev,
-                                                    const Channels& ch, float2& y) {
+// One token's backward step on two channels.  The factors of D, the gradient of its h, in da and
+// (times log2 e) dA_log, from the token's decay lam and the state before it; returns the decay's
+// base-2 logarithm.  sigmoid(v) is r = 1 / (1 + t) for v >= 0 and t r below, t = e^{-|v|}, so that
+// small values keep their relative accuracy; sigmoid(v) (1 - sigmoid(v)) is t r^2 for both signs.
+// Both forms of the backward pass use these, so they agree bit for bit where they add in the
+// same order.
+__device__ __forceinline__ float2 decay_factors(float2 a, float2 prev, const Channels& ch, float2& lam,
+                                                float2& fa, float2& fA) {
     const Gate g = decay_gate(a, ch);
-    y = g.y;
-    GradFactors f;
-    f.lam = ex2f2(g.y);
+    lam = ex2f2(g.y);
     const float2 rz = rcpf2(__fadd2_rn(g.t, bcast2(1.f))), tz = __fmul2_rn(g.t, rz);
     const float2 slope = make_float2(g.zl.x >= 0.f ? rz.x : tz.x, g.zl.y >= 0.f ? rz.y : tz.y);
+    const float2 lp = __fmul2_rn(lam, prev);
+    fa = __fmul2_rn(__fmul2_rn(lp, ch.A), slope);
+    fA = __fmul2_rn(lp, g.y);
+    return g.y;
+}
+// Those in dx and db.
+__device__ __forceinline__ void input_factors(float2 x, float2 b, float2& fx, float2& fb) {
     const float2 bl = __fmul2_rn(b, bcast2(kLog2e));
     const float2 tb = ex2f2(make_float2(-fabsf(bl.x), -fabsf(bl.y)));
     const float2 rb = rcpf2(__fadd2_rn(tb, bcast2(1.f))), tr = __fmul2_rn(tb, rb);
-    f.x = make_float2(bl.x >= 0.f ? rb.x : tr.x, bl.y >= 0.f ? rb.y : tr.y);
-    f.b = __fmul2_rn(x, __fmul2_rn(rb, tr));
-    const float2 lp = __fmul2_rn(f.lam, prev);
-    f.a = __fmul2_rn(__fmul2_rn(lp, ch.A), slope);
-    f.A = __fmul2_rn(lp, g.y);
-    return f;
+    fx = make_float2(bl.x >= 0.f ? rb.x : tr.x, bl.y >= 0.f ? rb.y : tr.y);
+    fb = __fmul2_rn(x, __fmul2_rn(rb, tr));
 }
 template <typename Tin>
-__device__ __forceinline__ void store_grads(const GradFactors& f, float2 D, Tin* dx, Tin* da,
-                                            Tin* db, float2& acc_A, float2& acc_bias) {
-    const float2 va = __fmul2_rn(f.a, D);
-    store_pair(dx, __fmul2_rn(f.x, D));
+__device__ __forceinline__ void store_grads(float2 fx, float2 fb, float2 fa, float2 fA, float2 D, Tin* dx,
+                                            Tin* da, Tin* db, float2& acc_A, float2& acc_bias) {
+    const float2 va = __fmul2_rn(fa, D);
+    store_pair(dx, __fmul2_rn(fx, D));
     store_pair(da, va);
-    store_pair(db, __fmul2_rn(f.b, D));
-    acc_A = __ffma2_rn(f.A, D, acc_A);
+    store_pair(db, __fmul2_rn(fb, D));
+    acc_A = __ffma2_rn(fA, D, acc_A);
     acc_bias = __fadd2_rn(acc_bias, va);
 }
 
@@ -211,12 +209,12 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
         for (long long t = t1 - 1; t >= t0; --t) {
             const float2 prev = t > t0 ? load_pair(p.out + (t - 1) * p.C + c) : init;
             D = __fadd2_rn(load_pair(r.grad_out + t * p.C + c), D);
-            float2 y;
-            const GradFactors f = grad_factors(load_pair(x + t * p.ld), load_pair(a + t * p.ld),
-                                               load_pair(b + t * p.ld), prev, ch, y);
-            store_grads(f, D, dx + t * r.ld_grad, da + t * r.ld_grad, db + t * r.ld_grad, acc_A,
-                        acc_bias);
-            D = __fmul2_rn(f.lam, D);
+            float2 lam, fa, fA, fx, fb;
+            decay_factors(load_pair(a + t * p.ld), prev, ch, lam, fa, fA);
+            input_factors(load_pair(x + t * p.ld), load_pair(b + t * p.ld), fx, fb);
+            store_grads(fx, fb, fa, fA, D, dx + t * r.ld_grad, da + t * r.ld_grad, db + t * r.ld_grad,
+                        acc_A, acc_bias);
+            D = __fmul2_rn(lam, D);
         }
         if (r.grad_init) *reinterpret_cast<float2*>(r.grad_init + at) = D;
     }
@@ -235,12 +233,12 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
 // then runs its tokens once more from its true start state and stores them.  Nothing is
 // read twice.
 //
-// What bounds it (B200, bf16): with every SM at work the steady state reads and writes at
-// 5.9 TB/s (0.9 of a copy), where the special-function unit is 46 % busy (eight operations
-// per token and channel pair) and half the issue slots are used; a call loses the rest to
-// its last wave, to CTA starts and to the exchanges.  Forward [8, 1024, 6144] 100 us (0.77
-// of a copy's rate), [1, 8192, 6144] 120 us (0.64), [1, 65536, 1024] 177 us (0.58);
-// backward 207 us (0.74), 223 us (0.69), 358 us (0.57).
+// What bounds it (B200, bf16): with as many units as SMs the backward pass runs at a copy's rate
+// ([1, 8192, 9472] 236 us) and the forward pass at 0.86 of it (137 us), where the
+// special-function unit does eight operations per token and channel pair; other calls lose to
+// their last wave, to CTA starts and to the exchanges.  Forward [8, 1024, 6144] 98 us (0.78 of a
+// copy's rate), [1, 8192, 6144] 110 us (0.70), [1, 65536, 1024] 155 us (0.66); backward 179 us
+// (0.86), 195 us (0.79), 270 us (0.76).
 //
 // Decays are composed as sums of log-decays.  From tile to tile a factor P near 1 acts
 // through W = P - 1, formed as expm1 of its tile's sum: a slow channel's state lasts over
@@ -249,16 +247,16 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
 // large forgotten state would leave its rounding error in a small new one.
 constexpr int kStrip = 64;
 constexpr int kMaxCluster = 12;  // above 8 where the device allows it
+constexpr size_t kSmemPerSm = 228 * 1024;  // 1 KB of it per CTA is the system's
 
 // Shared memory of a CTA: per slot the x, a, b tiles, and for the backward pass dout's.
-// PEERS: CTAs per cluster at most (1: none); Pipe: a step's exchange overlaps the next step's
-// tile, at the price of both steps' tokens in registers.
-template <typename Tin_, int WARPS_, int TOK_, int STAGES_, int PEERS_, bool Pipe_, bool Grad>
+// PEERS: CTAs per cluster at most (1: none).
+template <typename Tin_, int WARPS_, int TOK_, int STAGES_, int PEERS_, bool Grad>
 struct alignas(128) TileSmem {
     using Tin = Tin_;
     static constexpr int WARPS = WARPS_, TOK = TOK_, STAGES = STAGES_, kRows = WARPS * TOK;
     static constexpr int PEERS = PEERS_;
-    static constexpr bool Cluster = PEERS > 1, Pipe = Pipe_;
+    static constexpr bool Cluster = PEERS > 1;
     struct alignas(128) Slot {
         Tin in[3][kRows][kStrip];
         float dout[Grad ? kRows : 1][Grad ? kStrip : 4];
@@ -266,11 +264,11 @@ struct alignas(128) TileSmem {
     Slot slot[STAGES];
     float4 part[2][WARPS][32];       // per warp and lane: P pair, H pair; by step parity
     float2 log_part[2][WARPS][32];   // log2 of P
-    // The cluster's tiles: coded factor pair, H pair; by step modulo 4.  A CTA publishes step
-    // s + 4 only once it has every peer's step s + 2, which a peer publishes after all its
+    // The cluster's tiles: coded factor pair, H pair; by step parity.  A CTA publishes step
+    // s + 2 only once it has every peer's step s + 1, which a peer publishes after all its
     // warps are done with step s: nothing still unread is overwritten.
-    float4 peer[4][PEERS][32];
-    uint64_t full[STAGES], peers_in[4];
+    float4 peer[2][PEERS][32];
+    uint64_t full[STAGES], peers_in[2];
     int ticket;
 };
 
@@ -378,11 +376,11 @@ __device__ __forceinline__ Joined publish(Smem& sm, int step, int warp, int lane
     j.H = Hp;
     j.all = make_float4(code_factor(G.x), code_factor(G.y), H.x, H.y);
     if constexpr (Cluster) {
-        uint64_t* bar = &sm.peers_in[step & 3];
+        uint64_t* bar = &sm.peers_in[step & 1];
         const uint32_t K = cluster_size();
         if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(bar, K * (uint32_t)sizeof(sm.peer[0][0]));
         for (uint32_t k = warp; k < K; k += Smem::WARPS)
-            store_peer(&sm.peer[step & 3][cluster_rank()][lane], bar, k, j.all);
+            store_peer(&sm.peer[step & 1][cluster_rank()][lane], bar, k, j.all);
     }
     return j;
 }
@@ -394,7 +392,7 @@ __device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int lan
     const int step = j.step;
     float2 in = S;
     if constexpr (Cluster) {
-        if (!dead && !tc::mbar_wait(&sm.peers_in[step & 3], (uint32_t)(step >> 2) & 1u)) {
+        if (!dead && !tc::mbar_wait(&sm.peers_in[step & 1], (uint32_t)(step >> 1) & 1u)) {
             dead = true;
             if (lane == 0) atomicExch(&g_recurrence_status, 1);
         }
@@ -403,7 +401,7 @@ __device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int lan
 #pragma unroll 4
         for (uint32_t k = 0; k < K; ++k) {
             if (k == rank) in = S;
-            const float4 v = sm.peer[step & 3][k][lane];
+            const float4 v = sm.peer[step & 1][k][lane];
             S = make_float2(carry(S.x, v.x, v.z), carry(S.y, v.y, v.w));
         }
     } else {
@@ -515,7 +513,7 @@ __device__ __forceinline__ Place place_of(const RecurrenceParams& p, int unit, i
 template <typename Smem>
 __device__ __forceinline__ void init_cta(Smem& sm, const Schedule& s, int rank) {
     for (int i = 0; i < Smem::STAGES; ++i) tc::mbar_init(&sm.full[i], 1);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&sm.peers_in[i], 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.peers_in[i], 1);
     tc::mbar_init_fence();
     if (Smem::Cluster && s.span && rank == 0) sm.ticket = atomicAdd(s.ticket, 1);
 }
@@ -524,6 +522,7 @@ template <typename Smem, int Blocks>
 __global__ void __launch_bounds__(32 * Smem::WARPS, Blocks)
 recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, int strips,
                        Schedule sched) {
+    static_assert(sizeof(Smem) <= kSmemPerSm / Blocks - 1024, "the SM's CTAs have to fit");
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
     constexpr bool Cluster = Smem::Cluster;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -639,26 +638,11 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
             }
             __syncwarp();
         };
-        if constexpr (Smem::Pipe) {
-            // a step's exchange runs while the next step's tile is read
-            Held even, odd;
-            if (part.s0 < part.s1) read_tile(part.s0, even);
-            if (part.s0 > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
-            for (int step = part.s0; step < part.s1; step += 2) {
-                if (step + 1 < part.s1) read_tile(step + 1, odd);
-                write_tile(step, even);
-                if (step + 1 < part.s1) {
-                    if (step + 2 < part.s1) read_tile(step + 2, even);
-                    write_tile(step + 1, odd);
-                }
-            }
-        } else {
-            Held k;
-            for (int step = part.s0; step < part.s1; ++step) {
-                read_tile(step, k);
-                if (Cluster && step == part.s0 && step > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
-                write_tile(step, k);
-            }
+        Held k;
+        for (int step = part.s0; step < part.s1; ++step) {
+            read_tile(step, k);
+            if (Cluster && step == part.s0 && step > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
+            write_tile(step, k);
         }
         if (Cluster && part.s1 < w.steps && w.rank == 0 && w.warp == 0)
             hand_over(sched, parts.index, w.lane, S);
@@ -673,9 +657,10 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
 
 // The same pass against time: with E the gradient that reaches h_t from later tokens,
 // D_t = dout_t + E and E <- exp(g_t) D_t, so tokens are taken from the last one back and a
-// warp's pair is (P, H) of E.  Tiles are counted from the sequence's end.  Everything that
-// multiplies D is formed while the tile is read, so that the second run over a warp's tokens,
-// after the join, is short.  h comes by plain loads, one step ahead.
+// warp's pair is (P, H) of E.  Tiles are counted from the sequence's end.  What D is multiplied
+// with for da and dA_log is formed while the tile is read, for dx and db (sigmoid(b)) in the
+// second run, from the slot: three values per token and channel to hold, not five.  h comes by
+// plain loads, one step ahead.
 // partial [rows][2 C]: each CTA's sums for A_log and dt_bias, one row per (sequence, rank), and
 // under a split schedule as many rows again for the units' later parts.
 template <typename Smem, int Blocks>
@@ -685,9 +670,8 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
     constexpr bool Cluster = Smem::Cluster;
     using Tin = typename Smem::Tin;
-    // steps after which a tile's dout is no longer needed: the exchange takes one of two
-    constexpr int kHeld = Smem::Pipe ? 2 : 1;
-    static_assert(STAGES > kHeld, "a slot has to be free for the next tile");
+    static_assert(STAGES > 1, "a slot has to be free for the next tile");
+    static_assert(sizeof(Smem) <= kSmemPerSm / Blocks - 1024, "the SM's CTAs have to fit");
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     if (threadIdx.x == 0) init_cta(sm, sched, Cluster ? (int)cluster_rank() : 0);
@@ -695,7 +679,7 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
     const Parts parts = parts_of<Cluster>(sm, sched);
     const float2 zero = make_float2(0.f, 0.f);
     struct Held {
-        GradFactors f[TOK];
+        float2 lam[TOK], a[TOK], A[TOK];
         Joined j;
         int slot;
     };
@@ -764,15 +748,12 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
             }
             __syncwarp();
             float2 G = zero, H = zero;
-            const auto* row = &sm.slot[st].in[0][kRows - 1 - w.warp * TOK][2 * w.lane];
+            const auto* a = &sm.slot[st].in[1][kRows - 1 - w.warp * TOK][2 * w.lane];
             const float* dout = &sm.slot[st].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
             auto gates = [&](int i) {
-                float2 y;
-                k.f[i] = grad_factors(smem_pair(row - i * kStrip),
-                                      smem_pair(row + (kRows - i) * kStrip),
-                                      smem_pair(row + (2 * kRows - i) * kStrip), prev[i], ch, y);
+                const float2 y = decay_factors(smem_pair(a - i * kStrip), prev[i], ch, k.lam[i], k.a[i], k.A[i]);
                 G = __fadd2_rn(G, y);
-                H = __fmul2_rn(k.f[i].lam, __fadd2_rn(smem_pair(dout - i * kStrip), H));
+                H = __fmul2_rn(k.lam[i], __fadd2_rn(smem_pair(dout - i * kStrip), H));
             };
             if (live == TOK) {
 #pragma unroll
@@ -787,14 +768,15 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
             sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
             sm.log_part[buf][w.warp][w.lane] = G;
             __syncthreads();
-            // every warp is done with step - kHeld: its slot takes another tile
-            if (threadIdx.x == 0 && !dead && step - part.s0 >= kHeld) load_next();
+            // every warp is done with the step before: its slot takes another tile
+            if (threadIdx.x == 0 && !dead && step > part.s0) load_next();
             k.j = publish<Cluster>(sm, turn++, w.warp, w.lane);
         };
         auto write_tile = [&](int step, const Held& k) {
             float2 E = start_state<Cluster>(sm, k.j, w.lane, S, dead);
             const long long last = last_of(step);
             const int live = live_of(last);
+            const auto* x = &sm.slot[k.slot].in[0][kRows - 1 - w.warp * TOK][2 * w.lane];
             const float* dout = &sm.slot[k.slot].dout[kRows - 1 - w.warp * TOK][2 * w.lane];
             if (w.in_c) {
                 Tin* dx = static_cast<Tin*>(r.grad_x) + last * r.ld_grad + w.c;
@@ -803,8 +785,10 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
                 auto token = [&](int i) {
                     const float2 D = __fadd2_rn(smem_pair(dout - i * kStrip), E);
                     const long long o = i * r.ld_grad;
-                    store_grads(k.f[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
-                    E = __fmul2_rn(k.f[i].lam, D);
+                    float2 fx, fb;
+                    input_factors(smem_pair(x - i * kStrip), smem_pair(x + (2 * kRows - i) * kStrip), fx, fb);
+                    store_grads(fx, fb, k.a[i], k.A[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
+                    E = __fmul2_rn(k.lam[i], D);
                 };
                 if (live == TOK) {
 #pragma unroll
@@ -821,26 +805,11 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
             }
             __syncwarp();
         };
-        if constexpr (Smem::Pipe) {
-            // a step's exchange runs while the next step's tile is read
-            Held even, odd;
-            if (part.s0 < part.s1) read_tile(part.s0, even);
-            if (part.s0 > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
-            for (int step = part.s0; step < part.s1; step += 2) {
-                if (step + 1 < part.s1) read_tile(step + 1, odd);
-                write_tile(step, even);
-                if (step + 1 < part.s1) {
-                    if (step + 2 < part.s1) read_tile(step + 2, even);
-                    write_tile(step + 1, odd);
-                }
-            }
-        } else {
-            Held k;
-            for (int step = part.s0; step < part.s1; ++step) {
-                read_tile(step, k);
-                if (Cluster && step == part.s0 && step > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
-                write_tile(step, k);
-            }
+        Held k;
+        for (int step = part.s0; step < part.s1; ++step) {
+            read_tile(step, k);
+            if (Cluster && step == part.s0 && step > 0) S = take_over(sched, parts.index - 1, w.lane, dead);
+            write_tile(step, k);
         }
         if (Cluster && part.s1 < w.steps && w.rank == 0 && w.warp == 0)
             hand_over(sched, parts.index, w.lane, S);
@@ -994,48 +963,49 @@ bool make_maps(Maps& m, const RecurrenceParams& p, const float* dout, int box) {
 
 // The forms of each kernel: warps, tokens per warp, slots, CTAs per cluster at most.  One: no
 // cluster, a CTA per SM.  Many: no cluster, two CTAs per SM, whose phases and starts overlap.
-// Wide: clusters with one CTA per SM and two steps in registers, for few units.  Pair:
-// clusters with two CTAs per SM, for units in between (a cluster's CTAs share SMs, so it
-// needs enough clusters).  Registers set the tokens (two values per token and channel
-// forward, five backward), shared memory the slots.  Times in ns as measured with every SM at
-// work (One: with the SM to itself): a step, and a CTA's start.
+// Wide: clusters with one CTA per SM, for few units; its tiles are the largest that the slots
+// hold, since a step's exchange costs the same 0.6 us for any.  Pair: clusters with two CTAs
+// per SM, for units in between (a cluster's CTAs share SMs, so it needs enough clusters).
+// Registers set the tokens of two CTAs per SM (two values per token and channel forward, three
+// backward, where a slot is held through its step, too).  Times in ns as measured: a step, and
+// a CTA's start.
 template <typename Tin> struct Forms;
 template <> struct Forms<__nv_bfloat16> {
     using T = __nv_bfloat16;
     struct Fwd {
-        using One = TileSmem<T, 8, 12, 2, 1, false, false>;
-        using Many = One;
-        using Wide = TileSmem<T, 8, 16, 2, 12, true, false>;
-        using Pair = TileSmem<T, 8, 12, 2, 4, false, false>;
-        static constexpr double kOne = 1710, kMany = 3140, kWide = 2800, kPair = 3500;
-        static constexpr double kStart = 1500, kSharedStart = 300;
+        using One = TileSmem<T, 8, 20, 2, 1, false>;
+        using Many = TileSmem<T, 8, 12, 2, 1, false>;
+        using Wide = TileSmem<T, 8, 32, 2, 12, false>;
+        using Pair = TileSmem<T, 8, 12, 2, 4, false>;
+        static constexpr double kOne = 2600, kMany = 3140, kWide = 4450, kPair = 3500;
+        static constexpr double kStart = 1500, kManyStart = 300, kWideStart = 4500, kPairStart = 300;
     };
     struct Bwd {
-        using One = TileSmem<T, 8, 8, 3, 1, false, true>;
-        using Many = TileSmem<T, 8, 6, 2, 1, false, true>;
-        using Wide = TileSmem<T, 8, 8, 3, 12, true, true>;
-        using Pair = TileSmem<T, 8, 6, 2, 4, false, true>;
-        static constexpr double kOne = 2070, kMany = 3300, kWide = 2900, kPair = 3450;
-        static constexpr double kStart = 3400, kSharedStart = 1500;
+        using One = TileSmem<T, 8, 10, 3, 1, true>;
+        using Many = TileSmem<T, 8, 8, 2, 1, true>;
+        using Wide = TileSmem<T, 8, 14, 2, 12, true>;
+        using Pair = TileSmem<T, 8, 7, 2, 4, true>;
+        static constexpr double kOne = 2200, kMany = 3370, kWide = 3550, kPair = 3600;
+        static constexpr double kStart = 3400, kManyStart = 6000, kWideStart = 6000, kPairStart = 1500;
     };
 };
 template <> struct Forms<float> {
     using T = float;
     struct Fwd {
-        using One = TileSmem<T, 8, 8, 2, 1, false, false>;
-        using Many = One;
-        using Wide = TileSmem<T, 8, 8, 3, 12, true, false>;
-        using Pair = TileSmem<T, 8, 6, 2, 4, false, false>;
-        static constexpr double kOne = 1290, kMany = 2350, kWide = 1750, kPair = 2250;
-        static constexpr double kStart = 1500, kSharedStart = 300;
+        using One = TileSmem<T, 8, 12, 2, 1, false>;
+        using Many = TileSmem<T, 8, 8, 2, 1, false>;
+        using Wide = TileSmem<T, 8, 16, 2, 12, false>;
+        using Pair = TileSmem<T, 8, 6, 2, 4, false>;
+        static constexpr double kOne = 2110, kMany = 2350, kWide = 2850, kPair = 2250;
+        static constexpr double kStart = 1500, kManyStart = 300, kWideStart = 4500, kPairStart = 300;
     };
     struct Bwd {
-        using One = TileSmem<T, 8, 8, 3, 1, false, true>;
-        using Many = TileSmem<T, 8, 4, 2, 1, false, true>;
-        using Wide = TileSmem<T, 8, 8, 3, 8, true, true>;
-        using Pair = TileSmem<T, 8, 4, 2, 4, false, true>;
-        static constexpr double kOne = 2380, kMany = 2700, kWide = 3600, kPair = 2850;
-        static constexpr double kStart = 3400, kSharedStart = 1500;
+        using One = TileSmem<T, 8, 6, 3, 1, true>;
+        using Many = TileSmem<T, 8, 6, 2, 1, true>;
+        using Wide = TileSmem<T, 8, 12, 2, 12, true>;
+        using Pair = TileSmem<T, 8, 5, 2, 4, true>;
+        static constexpr double kOne = 2230, kMany = 3490, kWide = 4100, kPair = 3000;
+        static constexpr double kStart = 3400, kManyStart = 6000, kWideStart = 6000, kPairStart = 1500;
     };
 };
 constexpr double kWideRank = 10, kPairRank = 50;  // a step's further ns for each CTA of the cluster
@@ -1048,7 +1018,7 @@ void offer_single(Plan* plan, const RecurrenceParams& p) {
     if (units_of(p) <= sms)
         offer(plan, p, kOneForm, 1, sms, F::One::kRows, F::kOne, F::kStart, false);
     else
-        offer(plan, p, kManyForm, 1, 2LL * sms, F::Many::kRows, F::kMany, F::kSharedStart, false);
+        offer(plan, p, kManyForm, 1, 2LL * sms, F::Many::kRows, F::kMany, F::kManyStart, false);
 }
 
 // Whether the sequential form is the faster one: a chain of tokens, each at least a memory latency
@@ -1139,14 +1109,14 @@ cudaError_t forward(const RecurrenceParams& p, cudaStream_t stream) {
     }
     cudaError_t e = offer_clusters<typename F::Wide>(
         &plan, p, kWideForm, recurrence_tile_kernel<typename F::Wide, 1>, wide, F::kWide, kWideRank,
-        F::kStart);
+        F::kWideStart);
     if (e == cudaSuccess)
         e = offer_clusters<typename F::Pair>(
             &plan, p, kPairForm, recurrence_tile_kernel<typename F::Pair, 2>, pair, F::kPair,
-            kPairRank, F::kSharedStart);
+            kPairRank, F::kPairStart);
     if (e != cudaSuccess) return e;
     switch (plan.form) {
-        case kOneForm: return forward_tiles<typename F::One, 2>(p, plan, stream);
+        case kOneForm: return forward_tiles<typename F::One, 1>(p, plan, stream);
         case kManyForm: return forward_tiles<typename F::Many, 2>(p, plan, stream);
         case kWideForm: return forward_tiles<typename F::Wide, 1>(p, plan, stream);
         default: return forward_tiles<typename F::Pair, 2>(p, plan, stream);
@@ -1174,11 +1144,11 @@ cudaError_t backward(const RecurrenceParams& p, const RecurrenceGrads& r, cudaSt
     }
     cudaError_t e = offer_clusters<typename F::Wide>(
         &plan, p, kWideForm, recurrence_tile_backward_kernel<typename F::Wide, 1>, wide, F::kWide,
-        kWideRank, F::kStart);
+        kWideRank, F::kWideStart);
     if (e == cudaSuccess)
         e = offer_clusters<typename F::Pair>(
             &plan, p, kPairForm, recurrence_tile_backward_kernel<typename F::Pair, 2>, pair,
-            F::kPair, kPairRank, F::kSharedStart);
+            F::kPair, kPairRank, F::kPairStart);
     if (e != cudaSuccess) return e;
     switch (plan.form) {
         case kOneForm: return backward_tiles<typename F::One, 1>(p, r, plan, stream);

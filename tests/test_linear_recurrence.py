@@ -103,6 +103,23 @@ def test_dense(B, T, C, dtype):
     check(m, on_gpu(m)[1], ref, mag, T)
 
 
+# around the tiles of the forms with one CTA per SM (48 to 256 tokens), their clusters' steps, and
+# those of the forms with two, which take many sequences
+EDGES = [(1, t, 64) for t in (39, 41, 48, 56, 79, 81, 95, 97, 111, 113, 159, 161, 225, 256, 449, 511,
+                              513, 1281, 3000)] + [(160, t, 136) for t in (129, 191, 193, 256)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C", EDGES)
+def test_tile_edges(B, T, C, dtype):
+    m = make(B, T, C, dtype, seed=T + C, init=T % 2 == 0)
+    got = on_gpu(m)[1]
+    m, got = some_channels(m, got, 1 + B // 40)
+    ref, mag = expected(m)
+    check(m, got, ref, mag, T)
+
+
 PACKED = [[1], [0, 5, 0], [1, 1, 1, 1], [17, 0, 64, 1, 130], [300, 3, 128, 129, 0, 1, 255],
           [0, 1500, 2], [64, 64, 64], [2000]]
 
