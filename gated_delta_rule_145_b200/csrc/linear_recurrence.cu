@@ -905,17 +905,17 @@ struct Plan {
 // Offers `slots` clusters of K CTAs that take `rows` tokens of a unit per step of `ns`, plain and
 // (cuttable: equal lengths) split.  The time is that of the busiest slot's steps, and of what
 // a CTA does before its first (`start_ns`, less where another CTA of its SM works on).  A split
-// schedule spends some 8 us more: another node of the stream sets its counters to zero, and a
-// part's first tile is not copied ahead.
+// schedule spends a start per unit and some 8 us more: another node of the stream sets its
+// counters to zero, and a part's first tile is not copied ahead.
 void offer(Plan* plan, const RecurrenceParams& p, int form, int K, long long slots, long long rows,
            double ns, double start_ns, bool cuttable) {
     const long long units = units_of(p), steps = (mean_length(p) + rows - 1) / rows;
     double t = (double)((units + slots - 1) / slots) * (steps * ns + start_ns);
-    if (!plan->K || t < 0.98 * plan->time) *plan = {form, K, 0, 0, t};
+    if (!plan->K || t < 0.97 * plan->time) *plan = {form, K, 0, 0, t};
     const long long total = units * steps, span = std::max(steps, (total + slots - 1) / slots);
     if (!cuttable || p.cu_seqlens || total + span > (1 << 30)) return;
-    t = (double)(span + 1) * ns + start_ns + 8000.0;
-    if (t < 0.95 * plan->time)
+    t = (double)(span + 1) * ns + (double)span / steps * start_ns + 8000.0;
+    if (t < 0.97 * plan->time)
         *plan = {form, K, (int)span, (int)((total + span - 1) / span), t};
 }
 template <typename Smem, typename Kernel>
@@ -977,7 +977,7 @@ template <> struct Forms<__nv_bfloat16> {
         using Many = TileSmem<T, 8, 12, 2, 1, false>;
         using Wide = TileSmem<T, 8, 32, 2, 12, false>;
         using Pair = TileSmem<T, 8, 12, 2, 4, false>;
-        static constexpr double kOne = 2600, kMany = 3140, kWide = 4450, kPair = 3500;
+        static constexpr double kOne = 2600, kMany = 3140, kWide = 4450, kPair = 3350;
         static constexpr double kStart = 1500, kManyStart = 300, kWideStart = 4500, kPairStart = 300;
     };
     struct Bwd {
@@ -1055,6 +1055,8 @@ cudaError_t forward_tiles(const RecurrenceParams& p, const Plan& plan, cudaStrea
     const long long grid = (plan.span ? plan.clusters : units) * plan.K;
     const long long rows = (long long)Smem::kRows * plan.K;
     Maps m;
+    // a cluster's exchange needs a launch in clusters
+    if (Smem::Cluster != (plan.K > 1)) return cudaErrorInvalidValue;
     if (grid > 0x7fffffffLL || !make_maps(m, p, nullptr, Smem::kRows)) return cudaErrorNotSupported;
     void* ws = nullptr;
     cudaError_t e = plan.span ? workspace_alloc(&ws, schedule_bytes(plan), stream) : cudaSuccess;
@@ -1078,6 +1080,8 @@ cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, 
     // rows of partial sums: one per (sequence, rank), and one for a cut unit's later part
     const long long sums = (long long)p.nseq * plan.K * (plan.span ? 2 : 1);
     Maps m;
+    // a cluster's exchange needs a launch in clusters
+    if (Smem::Cluster != (plan.K > 1)) return cudaErrorInvalidValue;
     if (grid > 0x7fffffffLL || !make_maps(m, p, r.grad_out, Smem::kRows)) return cudaErrorNotSupported;
     const size_t sum_bytes = sizeof(float) * sums * 2 * p.C;
     float* part = nullptr;
