@@ -163,6 +163,23 @@ def test_large(B, T, C, dtype):
     check(m, got, ref, mag, T)
 
 
+# more strips than the SMs take at once
+MANY = [(5, 1300, 4104, "bf16"), (8, 520, 6144, "bf16"), (3, 1999, 5000, "f32"), (6, 640, 4160, "f32")]
+
+
+@gpu
+@pytest.mark.parametrize("B,T,C,dtype", MANY)
+def test_more_strips_than_sms(B, T, C, dtype):
+    m = make(B, T, C, dtype, seed=T)
+    got = on_gpu(m)[1]
+    again = on_gpu(m)[1]
+    for name, p, q in zip(NAMES, got, again):
+        assert torch.equal(p, q), name
+    m, got = some_channels(m, got, max(1, B * T * C // 3_000_000))
+    ref, mag = expected(m)
+    check(m, got, ref, mag, T)
+
+
 @gpu
 def test_large_calls_on_two_streams_and_from_a_graph():
     """calls whose clusters hand states to one another, two at a time"""
