@@ -151,6 +151,8 @@ struct NormGrads {
 };
 cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t stream);
 cudaError_t launch_gated_rmsnorm_backward(const NormGrads& p, cudaStream_t stream);
+// Reads and clears the convolution backward's timeout record (nonzero if set, -1 on error).
+int read_and_clear_mixer_grad_status();
 
 // out0 [n0] and out1 [N - n0] = the column sums of part [P, N], rows added in a fixed order
 // (either output may be nullptr; P = 0 gives zeros); N a multiple of 4, part 16-byte aligned;
@@ -200,7 +202,7 @@ size_t noalloc_scratch_bytes();
 cudaError_t noalloc_scratch(void** ptr);
 
 // Reads and clears the tensor-core kernels', the tiled convolution's and recurrence's, the
-// layer norm's and the self-test's
+// layer norm's, the convolution backward's and the self-test's
 // timeout records (nonzero if set, 0 if not, -1 on a CUDA error); workspace.cu.
 int read_and_clear_tc_status();
 

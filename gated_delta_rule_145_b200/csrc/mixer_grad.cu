@@ -14,6 +14,8 @@
 
 #include "gdr_common.cuh"
 #include "gdr_internal.h"
+#include "tcgen05.cuh"
+#include "tma_map.h"
 
 namespace gdr {
 
@@ -27,13 +29,6 @@ __device__ __forceinline__ float ex2g(float x) {
 __device__ __forceinline__ float rcpg(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// The smaller value; NaN if either is.
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 
@@ -84,15 +79,9 @@ struct ConvLane {
         m = __ffma2_rn(w[1], h1, m);
         m = __ffma2_rn(w[2], h2, m);
         m = __ffma2_rn(w[3], v, m);
-        // SiLU'(s) = r (1 + s (1 - r)), r = sigmoid(s) = 1 / den, den = 1 + 2^m.  Below s = -41 it
-        // is under 2^-53 in magnitude; there s is taken as -41 (m as 59.15), so that the two
-        // channels' den stay finite when multiplied: one reciprocal, the pass's scarcest
-        // instruction, serves both.  A NaN stays in its channel: the first minimum keeps it, the
-        // second drops it for den.
-        m = make_float2(min_nan(m.x, 59.15f), min_nan(m.y, 59.15f));
-        const float2 den = __fadd2_rn(make_float2(ex2g(fminf(m.x, 59.15f)), ex2g(fminf(m.y, 59.15f))),
-                                      splat(1.f));
-        const float2 r = __fmul2_rn(splat(rcpg(den.x * den.y)), make_float2(den.y, den.x));
+        // SiLU'(s) = r (1 + s (1 - r)), r = sigmoid(s) = 1 / (1 + 2^m)
+        const float2 den = __fadd2_rn(make_float2(ex2g(m.x), ex2g(m.y)), splat(1.f));
+        const float2 r = make_float2(rcpg(den.x), rcpg(den.y));
         const float2 q = __ffma2_rn(m, __ffma2_rn(r, splat(-kLn2 * kLn2), splat(kLn2 * kLn2)),
                                     splat(-kLn2));
         return __fmul2_rn(g, __fmul2_rn(r, q));
@@ -117,18 +106,15 @@ struct ConvLane {
     }
 };
 
-// Eight bytes global -> shared, zeros if not `in` (the source is not read then).
-__device__ __forceinline__ void copy8(uint2* dst, const void* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                 "l"(src), "r"(in ? 8 : 0)
-                 : "memory");
-}
+// Set by a kernel that gave up a bounded wait; gdr_device_status reads it.
+__device__ int g_mixer_grad_status;
 
-// x and dy of kGBatch tokens, one lane's eight bytes each: a lane reads only what it copied
-// itself, so the ring needs no barrier.
-struct ConvBatch {
+// x and dy of kGBatch tokens of a warp's 128 channels, each by one TMA copy.
+struct alignas(128) ConvBatch {
     uint2 x[kGBatch][32], g[kGBatch][32];
+};
+struct ConvMaps {
+    CUtensorMap x, g;
 };
 union ConvBackwardSmem {
     ConvBatch ring[kGWarps][kGRing];
@@ -144,13 +130,25 @@ union ConvBackwardSmem {
 // part [groups][5 C]: the taps' sums as [C][4], then the bias's.
 template <bool Loop>
 __global__ void __launch_bounds__(32 * kGWarps, 2)
-conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float* part) {
+conv_backward_kernel(const __grid_constant__ ConvMaps maps, ConvGrads p, int nct, int nseg, int seg,
+                     int groups, float* part) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ uint64_t bars[kGWarps][kGRing];
     ConvBackwardSmem& smem = *reinterpret_cast<ConvBackwardSmem*>(smem_raw);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint64_t* full = bars[warp];  // a warp's own: its ring needs no barrier of the block
+    if (lane == 0) {
+        for (int i = 0; i < kGRing; ++i) tc::mbar_init(&full[i], 1);
+        tc::mbar_init_fence();
+    }
+    __syncwarp();
+    bool dead = false;
+    int issued = 0, taken = 0;  // batches copied (lane 0's), batches waited for
     const int ct = blockIdx.x % nct, group = blockIdx.x / nct;
-    const int c = ct * kGCh + 4 * lane;
-    const long long segments = c < p.C ? (long long)p.B * nseg : 0;
+    // lanes behind the last channel go along on the tile's first ones and store nothing
+    const bool in_c = ct * kGCh + 4 * lane < p.C;
+    const int c = ct * kGCh + (in_c ? 4 * lane : 0);
+    const long long segments = (long long)p.B * nseg;
     const float2 zero = splat(0.f);
     ConvLane a[2];
 #pragma unroll
@@ -166,7 +164,6 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float*
         const int t0 = (int)(sid % nseg) * seg, t1 = min(T, t0 + seg);
         const size_t base = (size_t)b * T * C + c;
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + base;
-        const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(p.grad_y) + base;
         __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(p.grad_x) + base;
         const size_t st = ((size_t)b * C + c) * 3;
 #pragma unroll
@@ -217,36 +214,40 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float*
         };
         ConvBatch* ring = smem.ring[warp];
         const int end = min(T, t1 + 3);  // tokens read: three past the segment
-        auto fetch = [&](int t, int slot) {
-            const __nv_bfloat16* xp = x + (size_t)t * C;
-            const __nv_bfloat16* gp = dy + (size_t)t * C;
-            if (t < end) {
-#pragma unroll
-                for (int i = 0; i < kGBatch; ++i) {
-                    const bool in = t + i < end;
-                    copy8(&ring[slot].x[i][lane], in ? xp + (size_t)i * C : x, in);
-                    copy8(&ring[slot].g[i][lane], in ? gp + (size_t)i * C : dy, in);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+        auto fetch = [&](int t) {  // lane 0; rows behind `end` come too, and are not used
+            if (t >= end || dead) return;
+            ConvBatch& to = ring[issued % kGRing];
+            uint64_t* bar = &full[issued % kGRing];
+            tc::mbar_arrive_expect_tx(bar, (uint32_t)sizeof(ConvBatch));
+            tc::tma_load_2d(&to.x[0][0], &maps.x, ct * kGCh, b * T + t, bar);
+            tc::tma_load_2d(&to.g[0][0], &maps.g, ct * kGCh, b * T + t, bar);
+            ++issued;
         };
+        if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < kGRing - 1; ++k) fetch(t0 + k * kGBatch, k);
-        int slot = 0;
+            for (int k = 0; k < kGRing - 1; ++k) fetch(t0 + k * kGBatch);
+        }
 #pragma unroll 1
         for (int t = t0; t < t1 + 3; t += kGBatch) {
-            // the slot used last takes the batch two ahead; all but the newest two have landed
-            fetch(t + (kGRing - 1) * kGBatch, slot == 0 ? kGRing - 1 : slot - 1);
-            asm volatile("cp.async.wait_group %0;" ::"n"(kGRing - 1) : "memory");
+            __syncwarp();  // every lane has read the batch before: its slot takes the one two ahead
+            if (lane == 0) fetch(t + (kGRing - 1) * kGBatch);
+            const int slot = taken % kGRing;
+            if (t < end) {
+                if (!dead && !tc::mbar_wait(&full[slot], (uint32_t)(taken / kGRing) & 1u)) {
+                    dead = true;
+                    if (lane == 0) atomicExch(&g_mixer_grad_status, 1);
+                }
+                ++taken;
+            }
+            __syncwarp();
             const ConvBatch& now = ring[slot];
-            slot = slot + 1 == kGRing ? 0 : slot + 1;
             __nv_bfloat16* op = dx + ((ptrdiff_t)t - 3) * C;
             if (t > t0 && t + kGBatch <= t1) {
 #pragma unroll
                 for (int i = 0; i < kGBatch; ++i) {
                     const float4 o = token(now.x[i][lane], now.g[i][lane], true);
                     const float f[4] = {o.x, o.y, o.z, o.w};
-                    __stcs(reinterpret_cast<uint2*>(op + (size_t)i * C), pack4(f));
+                    if (in_c) __stcs(reinterpret_cast<uint2*>(op + (size_t)i * C), pack4(f));
                 }
                 continue;
             }
@@ -261,7 +262,7 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float*
                     ug = now.g[i][lane];
                 }
                 const float4 o = token(ux, ug, t + i < t1);
-                if (u < t0 && t0 > 0) continue;  // another segment's
+                if ((u < t0 && t0 > 0) || !in_c) continue;  // another segment's, or nobody's
                 float f[4] = {o.x, o.y, o.z, o.w};
                 // the state after the call holds the inputs T - 3 .. T - 1
                 if (p.grad_state_out && u >= T - 3) {
@@ -276,8 +277,10 @@ conv_backward_kernel(ConvGrads p, int nct, int nseg, int seg, int groups, float*
                 }
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    if (dead && lane == 0)  // copies may still be in flight: the CTA stays for them
+        for (int k = max(0, issued - kGRing); k < issued; ++k)
+            tc::mbar_wait(&full[k % kGRing], (uint32_t)(k / kGRing) & 1u);
     __syncthreads();  // the ring is done with: its memory takes the sums
     float(*sm)[5][kGCh] = smem.sums;
 #pragma unroll
@@ -430,6 +433,11 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
     const long long all = ((long long)p.B * nseg + kGWarps - 1) / kGWarps;
     const long long groups = std::min(all, std::max<long long>(1, 8 * slots / nct));
     if (groups * nct > 0x7fffffffLL) return cudaErrorNotSupported;
+    ConvMaps maps;
+    const uint64_t rows = (uint64_t)p.B * p.T;
+    if (!make_map_pitched(&maps.x, p.x, false, p.C, rows, p.C, kGCh, kGBatch) ||
+        !make_map_pitched(&maps.g, p.grad_y, false, p.C, rows, p.C, kGCh, kGBatch))
+        return cudaErrorNotSupported;
     float* part = nullptr;
     cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * groups * 5 * p.C, stream);
     if (e != cudaSuccess) return e;
@@ -437,7 +445,7 @@ cudaError_t launch_short_conv_silu_backward(const ConvGrads& p, cudaStream_t str
     e = allow_smem((const void*)kernel, sizeof(ConvBackwardSmem));
     if (e == cudaSuccess) {
         kernel<<<(unsigned)(groups * nct), 32 * kGWarps, sizeof(ConvBackwardSmem), stream>>>(
-            p, nct, nseg, seg, (int)groups, part);
+            maps, p, nct, nseg, seg, (int)groups, part);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess)
@@ -459,6 +467,16 @@ cudaError_t launch_gated_rmsnorm_backward(const NormGrads& p, cudaStream_t strea
         e = launch_column_sum(part, grid, p.d, p.grad_weight, p.d, nullptr, stream);
     const cudaError_t f = cudaFreeAsync(part, stream);
     return e != cudaSuccess ? e : f;
+}
+
+int read_and_clear_mixer_grad_status() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_mixer_grad_status, sizeof(int)) != cudaSuccess) return -1;
+    if (v != 0) {
+        const int zero = 0;
+        cudaMemcpyToSymbol(g_mixer_grad_status, &zero, sizeof(int));
+    }
+    return v;
 }
 
 }  // namespace gdr

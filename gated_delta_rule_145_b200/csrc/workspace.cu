@@ -123,8 +123,9 @@ int read_and_clear_tc_status() {
     const int vcv = read_and_clear_conv_status();
     const int vrc = read_and_clear_recurrence_status();
     const int vln = read_and_clear_layer_norm_status();
-    if (v64 < 0 || vst < 0 || vcv < 0 || vrc < 0 || vln < 0) return -1;
-    return v64 != 0 ? v64 : vst != 0 ? vst : vcv != 0 ? vcv : vrc != 0 ? vrc : vln;
+    const int vmg = read_and_clear_mixer_grad_status();
+    if (v64 < 0 || vst < 0 || vcv < 0 || vrc < 0 || vln < 0 || vmg < 0) return -1;
+    return v64 != 0 ? v64 : vst != 0 ? vst : vcv != 0 ? vcv : vrc != 0 ? vrc : vln != 0 ? vln : vmg;
 }
 
 }  // namespace gdr

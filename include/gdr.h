@@ -477,7 +477,8 @@ GDR_API int gdr_linear_recurrence_backward_f32(
  * Device-side status of the kernels enqueued so far.  Synchronises `stream`, then returns
  * GDR_ERR_TIMEOUT if any tensor-core prefill kernel (or the TMA-fed convolution that
  * gdr_short_conv_silu runs for T >= 256, a tiled kernel of gdr_linear_recurrence or its backward
- * call, or gdr_layer_norm_backward on rows above 256) abandoned one of its bounded waits
+ * call, gdr_layer_norm_backward on rows above 256, or gdr_short_conv_silu_backward) abandoned one
+ * of its bounded waits
  * (each wait on an mbarrier gives up after 2 s, records the event and lets the kernel
  * exit instead of hanging), GDR_ERR_CUDA if the stream reports an error, else GDR_OK.
  * The timeout record is cleared by the call.

@@ -104,8 +104,7 @@ def test_conv_chained_through_the_state_is_one_call(T0):
 @gpu
 @pytest.mark.parametrize("T", [9, 300])
 def test_conv_nan_and_infinity_stay_in_their_channels(T):
-    """two channels share a reciprocal: its rounding (within the tolerances) depends on both, but
-    a NaN or an infinite sum of one is not the other's"""
+    """a lane holds four channels: a NaN or an infinite sum of one is not another's"""
     m = conv_case(2, T, 72, True, True, seed=4)
     m["x"][0, 4, 3] = np.nan
     m["x"][1, 5, 8] = np.inf
