@@ -5,10 +5,10 @@
 // The rows are added in a fixed order (thread row y takes rows y, y + Y, ...; then a tree
 // over y), so a call's result does not depend on which CTA finished first, as it would with
 // atomic adds.  With P = 0 the sums are zero.  A thread takes four columns; few blocks of
-// many rows (a norm's 128 columns) need all their loads in flight at once, many blocks of
-// few rows (a convolution's taps) need small blocks: Y = 128 above 128 rows, else 16.  Of 1184
-// rows of 128 columns it takes 6 us, of 148 of 12288 8 us (one thread per column and 32 rows of
-// threads: 10 and 11).
+// many rows (a norm's 128 columns) need all their loads in flight at once, many blocks of few rows
+// (a convolution's taps) need small blocks: Y = 16 up to 128 rows, above 128, or 32 where 256
+// blocks and more share the SMs.  Of 1184 rows of 128 columns it takes 6 us, of 148 of 12288 7 us
+// (9 with Y = 128; one thread per column and 32 rows of threads: 10 and 11).
 #include "gdr_internal.h"
 #include "tcgen05.cuh"
 
@@ -66,12 +66,15 @@ cudaError_t launch_column_sum(const float* part, long long P, int N, float* out0
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((N + 4 * kSumX - 1) / (4 * kSumX)));
-    cfg.blockDim = dim3(kSumX * (P > 128 ? 128 : 16));
+    const int Y = P <= 128 ? 16 : cfg.gridDim.x < 256 ? 128 : 32;
+    cfg.blockDim = dim3(kSumX * Y);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, P > 128 ? column_sum_kernel<128> : column_sum_kernel<16>, part,
-                              P, N, out0, n0, out1);
+    return cudaLaunchKernelEx(&cfg, Y == 128  ? column_sum_kernel<128>
+                                    : Y == 32 ? column_sum_kernel<32>
+                                              : column_sum_kernel<16>,
+                              part, P, N, out0, n0, out1);
 }
 
 }  // namespace gdr

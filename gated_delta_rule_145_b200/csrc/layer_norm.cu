@@ -864,11 +864,12 @@ struct BackwardPlan {
             grid = (unsigned)std::min<long long>(p.rows, std::max<long long>(1, 2 * device_sms() / across));
             return;
         }
-        // 8 columns per thread up to 768 threads, several blocks per SM up to 384 and one above
-        // (6144 columns: 80 us in one block of 768 threads and four rows per group, 84 in two of
-        // 384 and two rows), then up to 32 columns in 512; fewer blocks where they would leave
-        // each a single row per group
-        nv = vecs <= 768 ? 1 : vecs <= 1024 ? 2 : 4;
+        // 8 columns per thread up to 384 threads, several blocks per SM; above, one block with 16
+        // columns, then up to 32 in 512 threads: a thread's work per row (the shuffles, the scalars)
+        // is shared by its columns (6144 columns: 66 us; 71 in 768 threads of 8 columns with the
+        // same four rows per group, 75 in two blocks and two rows per group).  Fewer blocks where
+        // they would leave each a single row per group.
+        nv = vecs <= 384 ? 1 : vecs <= 1024 ? 2 : 4;
         threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
         const size_t row = 2 * sizeof(Tin) * p.d;  // x and dy
         int blocks = nv > 1 ? 1 : std::max(1, std::min(8, 768 / threads));
@@ -910,10 +911,9 @@ cudaError_t backward(const LayerNormGrads& p, const BackwardPlan<Tin>& plan, flo
                                                                   p.rows, p.d);
         return cudaGetLastError();
     }
-    auto kernel = plan.nv == 4           ? layer_norm_backward_kernel<Tin, 4, 512>
-                  : plan.nv == 2         ? layer_norm_backward_kernel<Tin, 2, 512>
-                  : plan.threads <= 384 ? layer_norm_backward_kernel<Tin, 1, 384>
-                                         : layer_norm_backward_kernel<Tin, 1, 768>;
+    auto kernel = plan.nv == 4   ? layer_norm_backward_kernel<Tin, 4, 512>
+                  : plan.nv == 2 ? layer_norm_backward_kernel<Tin, 2, 512>
+                                 : layer_norm_backward_kernel<Tin, 1, 384>;
     const cudaError_t e = allow_smem((const void*)kernel, plan.smem);
     if (e != cudaSuccess) return e;
     kernel<<<plan.grid, plan.threads, plan.smem, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx, part,
