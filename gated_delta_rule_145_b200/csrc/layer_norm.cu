@@ -405,10 +405,10 @@ layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
 // rows from a ring in shared memory (bulk copies: rows are contiguous), so the bytes in flight
 // depend neither on registers nor on barriers; the values are expanded again after the
 // barrier behind the two sums of each row instead of being held.  [8192, 6144] bf16 takes
-// 71 us (0.65 of a copy's rate), [8192, 4096] fp32 87 us (0.71): the two barriers of a group
+// 66 us (0.70 of a copy's rate), [8192, 4096] fp32 80 us (0.77): the two barriers of a group
 // and the sums between them, which one block per SM cannot overlap.  (Both phases of two
-// groups per barrier: 98 us; a column's sums over a warp's rows by shared-memory atomics
-// would add in no fixed order.)
+// groups per barrier: 98 us; one barrier per group, a slot refilled behind the next one: 74;
+// a column's sums over a warp's rows by shared-memory atomics would add in no fixed order.)
 constexpr int kRingRows = 4;
 
 // Adds v[0 .. 7] over the warp: lane l ends with the sum of v[l % 8].  Each exchange halves
@@ -485,7 +485,7 @@ struct Ring {
 // ------------------------------------------------------------------------------ backward
 // part [gridDim.x][2 d]: each block's sums over its rows, dweight, then dbias.
 template <typename Tin, int NV, int Threads>
-__global__ void __launch_bounds__(Threads, Threads == 384 ? 2 : 1)
+__global__ void __launch_bounds__(Threads, Threads == 512 ? 1 : 2)
 layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ weight,
                            const float* __restrict__ mean, const float* __restrict__ rstd,
                            const Tin* dy, Tin* dx, float* __restrict__ part, long long rows, int d,
@@ -864,15 +864,16 @@ struct BackwardPlan {
             grid = (unsigned)std::min<long long>(p.rows, std::max<long long>(1, 2 * device_sms() / across));
             return;
         }
-        // 8 columns per thread up to 384 threads, several blocks per SM; above, one block with 16
-        // columns, then up to 32 in 512 threads: a thread's work per row (the shuffles, the scalars)
-        // is shared by its columns (6144 columns: 66 us; 71 in 768 threads of 8 columns with the
-        // same four rows per group, 75 in two blocks and two rows per group).  Fewer blocks where
-        // they would leave each a single row per group.
+        // 8 columns per thread up to 384 threads, several blocks per SM; above, 16 columns, two
+        // blocks up to 256 threads and one above; then up to 32 columns in 512 threads.  A thread's
+        // work per row (the shuffles, the scalars) is shared by its columns (6144 columns: 66 us;
+        // 71 in 768 threads of 8 columns, 75 in two blocks and two rows per group; 4096 columns: 56
+        // in two blocks, 62 in one).  Fewer blocks where they would leave each a single row per
+        // group.
         nv = vecs <= 384 ? 1 : vecs <= 1024 ? 2 : 4;
         threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
         const size_t row = 2 * sizeof(Tin) * p.d;  // x and dy
-        int blocks = nv > 1 ? 1 : std::max(1, std::min(8, 768 / threads));
+        int blocks = nv == 1 ? std::max(1, std::min(8, 768 / threads)) : threads <= 256 ? 2 : 1;
         while (blocks > 1 && RingShape(row, blocks, 2).group_rows < 2) --blocks;
         const RingShape ring(row, blocks, 2);
         group_rows = ring.group_rows;
@@ -911,9 +912,10 @@ cudaError_t backward(const LayerNormGrads& p, const BackwardPlan<Tin>& plan, flo
                                                                   p.rows, p.d);
         return cudaGetLastError();
     }
-    auto kernel = plan.nv == 4   ? layer_norm_backward_kernel<Tin, 4, 512>
-                  : plan.nv == 2 ? layer_norm_backward_kernel<Tin, 2, 512>
-                                 : layer_norm_backward_kernel<Tin, 1, 384>;
+    auto kernel = plan.nv == 4          ? layer_norm_backward_kernel<Tin, 4, 512>
+                  : plan.nv == 1        ? layer_norm_backward_kernel<Tin, 1, 384>
+                  : plan.threads <= 256 ? layer_norm_backward_kernel<Tin, 2, 256>
+                                        : layer_norm_backward_kernel<Tin, 2, 512>;
     const cudaError_t e = allow_smem((const void*)kernel, plan.smem);
     if (e != cudaSuccess) return e;
     kernel<<<plan.grid, plan.threads, plan.smem, stream>>>(x, p.weight, p.mean, p.rstd, dy, dx, part,

@@ -95,6 +95,15 @@ def test_without_bias_far_mean_constant_rows_and_large_values():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", [(3, 3080), (700, 3600), (301, 4096), (5, 4104), (450, 6152), (77, 8192),
+                                    (9, 8200)])
+def test_columns_per_thread_edges(rows, d, dtype):
+    """widths around those where a thread takes twice the columns, or an SM half the blocks"""
+    check(*make(rows, d, dtype, rows + d), dtype)
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 1160, 6144, 20480])
 def test_a_variance_whose_inverse_no_float_holds(d):
     """no eps and values of 1e-18: rstd times a gradient of 1e6 is a float, rstd^2 times it none"""
