@@ -123,10 +123,13 @@ union ConvBackwardSmem {
 
 // CTA -> (channel tile, group of 8 segments of the B * nseg segments); warp -> segments of
 // `seg` tokens, lane -> four channels, one token after the other, its loads two batches
-// ahead (held in registers, one batch at a time, the loads' latency showed: 0.6 of HBM).
-// [1, 8192, 18432] takes 193 us (0.72 of a copy's rate, 4.7 TB/s), [8, 2048, 4096] 97 us (0.64):
-// 102 instructions per token and four channels use 57 % of the issue slots, the paired fp32
-// pipe more, and the segments' ends and one wave's uneven SMs take the rest.
+// ahead (held in registers, one batch at a time, the loads' latency showed: 0.6 of HBM; by
+// asynchronous copies of eight bytes per lane they cost a tenth of the instructions).
+// [1, 8192, 18432] takes 178 us (0.78 of a copy's rate, 5.1 TB/s), [8, 2048, 4096] 89 us (0.69):
+// 89 instructions per token and four channels use 54 % of the issue slots, the paired fp32
+// pipe more, and the segments' ends and one wave's uneven SMs take the rest.  (Two channels per
+// lane and twice the warps: 228 us; one reciprocal for two channels, with the minima that keep
+// the product finite: 189.)
 // part [groups][5 C]: the taps' sums as [C][4], then the bias's.
 template <bool Loop>
 __global__ void __launch_bounds__(32 * kGWarps, 2)
