@@ -463,12 +463,13 @@ def decode_step(q, k, v, a, b, A_log, dt_bias, state, out=None, stream=None, era
     return out
 
 
-def _check(device, *specs):
-    """Every (name, tensor, dtype, shape, dense) of `specs` is a CUDA tensor on `device` of this
-    type and shape, contiguous if `dense`; None passes."""
+def _check(first, *specs):
+    """Every (name, tensor, dtype, shape, dense) of `specs` is a CUDA tensor on `first`'s device of
+    this type and shape, contiguous if `dense`; None passes."""
+    index = first.get_device()  # -1: none; an integer, compared in half of a device's time
     for name, t, dtype, shape, dense in specs:
-        if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and
-                         t.is_cuda and (not dense or t.is_contiguous())):
+        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and
+                         (not dense or t.is_contiguous())):
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
@@ -476,8 +477,8 @@ def _check(device, *specs):
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -486,6 +487,8 @@ def _token_stride(tensors, B, T, C):
     or slices of the last dimension of a wider dense tensor."""
     if B * T * C == 0:
         return max(C, 1)
+    if all([t.is_contiguous() for t in tensors]):
+        return C
     first = tensors[0].stride()
     ld = first[1] if T > 1 else first[0] if B > 1 else C
     for t in tensors:
@@ -544,7 +547,7 @@ def _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens):
         if B != 1:
             raise ValueError("packed sequences need B == 1")
         nseq = cu_seqlens.numel() - 1
-    _check(x.device, ("x", x, dtype, shape, False), ("a", a, dtype, shape, False),
+    _check(x, ("x", x, dtype, shape, False), ("a", a, dtype, shape, False),
            ("b", b, dtype, shape, False), ("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), True),
            ("A_log", A_log, f32, (C,), True), ("dt_bias", dt_bias, f32, (C,), True),
            ("init_state", init_state, f32, (nseq, C), True))
@@ -563,12 +566,12 @@ def linear_recurrence(x, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None,
 
     dtype, nseq, T, C, ld = _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens)
     f32 = torch.float32
+    _check(x, ("out", out, f32, x.shape, True),
+           ("final_state", final_state, f32, (nseq, C), True))
     if out is None:
         out, = _empty(x, stream, (x.shape, f32))
     if final_state is None:
         final_state, = _empty(x, stream, ((nseq, C), f32))
-    _check(x.device, ("out", out, f32, x.shape, True),
-           ("final_state", final_state, f32, (nseq, C), True))
     fn = gdr_linear_recurrence_f32 if dtype == f32 else gdr_linear_recurrence
     _on_device(x, stream, fn, x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens,
                nseq, T, C, ld)
@@ -588,14 +591,16 @@ def linear_recurrence_backward(x, a, b, A_log, dt_bias, out, grad_out, grad_fina
     dtype, nseq, T, C, ld = _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens)
     f32 = torch.float32
     grads = (grad_x, grad_a, grad_b)
+    _check(x, ("out", out, f32, x.shape, True), ("grad_out", grad_out, f32, x.shape, True),
+           ("grad_final_state", grad_final_state, f32, (nseq, C), True))
     if grad_x is None or grad_a is None or grad_b is None:
         if any(g is not None for g in grads):
             raise ValueError("give grad_x, grad_a and grad_b together, or none of them")
-        grads = _empty(x, stream, *[(x.shape, dtype)] * 3)
-    _check(x.device, ("out", out, f32, x.shape, True), ("grad_out", grad_out, f32, x.shape, True),
-           ("grad_final_state", grad_final_state, f32, (nseq, C), True),
-           *[(n, g, dtype, x.shape, False) for n, g in zip(("grad_x", "grad_a", "grad_b"), grads)])
-    ld_grad = _token_stride(grads, x.shape[0], T, C)
+        grads, ld_grad = _empty(x, stream, *[(x.shape, dtype)] * 3), max(C, 1)
+    else:
+        _check(x, *[(n, g, dtype, x.shape, False)
+                    for n, g in zip(("grad_x", "grad_a", "grad_b"), grads)])
+        ld_grad = _token_stride(grads, x.shape[0], T, C)
     grad_A_log, grad_dt_bias, grad_init = _empty(x, stream, ((C,), f32), ((C,), f32),
                                                  ((nseq, C), f32))
     fn = (gdr_linear_recurrence_backward_f32 if dtype == f32 else
@@ -620,7 +625,7 @@ def layer_norm(x, weight, bias=None, eps=1e-5, y=None, stream=None):
 
     dtype, f32 = _input_type(x, "x"), torch.float32
     rows, d = _row_args(x)
-    _check(x.device, ("x", x, dtype, x.shape, True), ("weight", weight, f32, (d,), True),
+    _check(x, ("x", x, dtype, x.shape, True), ("weight", weight, f32, (d,), True),
            ("bias", bias, f32, (d,), True), ("y", y, dtype, x.shape, True))
     mean, rstd = _empty(x, stream, (x.shape[:-1], f32), (x.shape[:-1], f32))
     if y is None:
@@ -637,7 +642,7 @@ def layer_norm_backward(x, weight, mean, rstd, grad_y, grad_x=None, stream=None)
 
     dtype, f32 = _input_type(x, "x"), torch.float32
     rows, d = _row_args(x)
-    _check(x.device, ("x", x, dtype, x.shape, True), ("weight", weight, f32, (d,), True),
+    _check(x, ("x", x, dtype, x.shape, True), ("weight", weight, f32, (d,), True),
            ("mean", mean, f32, x.shape[:-1], True), ("rstd", rstd, f32, x.shape[:-1], True),
            ("grad_y", grad_y, dtype, x.shape, True), ("grad_x", grad_x, dtype, x.shape, True))
     if grad_x is None:
@@ -660,7 +665,7 @@ def short_conv_silu_backward(x, weight, grad_y, bias=None, conv_state_in=None,
     if x.dim() != 3:
         raise ValueError(f"x must be [B, T, C], got shape {tuple(x.shape)}")
     B, T, C = x.shape
-    _check(x.device, ("x", x, bf16, x.shape, True), ("weight", weight, f32, (C, 4), True),
+    _check(x, ("x", x, bf16, x.shape, True), ("weight", weight, f32, (C, 4), True),
            ("grad_y", grad_y, bf16, x.shape, True), ("bias", bias, f32, (C,), True),
            ("conv_state_in", conv_state_in, f32, (B, C, 3), True),
            ("grad_conv_state_out", grad_conv_state_out, f32, (B, C, 3), True))
@@ -679,7 +684,7 @@ def gated_rmsnorm_backward(o, z, weight, grad_y, eps=1e-6, stream=None):
     f32 = torch.float32
     dtype = _input_type(z, "z")
     rows, d = _row_args(o)
-    _check(o.device, ("o", o, f32, o.shape, True), ("z", z, dtype, o.shape, True),
+    _check(o, ("o", o, f32, o.shape, True), ("z", z, dtype, o.shape, True),
            ("weight", weight, f32, (d,), True), ("grad_y", grad_y, f32, o.shape, True))
     grad_o, grad_z, grad_weight = _empty(o, stream, (o.shape, f32), (z.shape, dtype), ((d,), f32))
     fn = gdr_gated_rmsnorm_backward_f32 if dtype == f32 else gdr_gated_rmsnorm_backward
