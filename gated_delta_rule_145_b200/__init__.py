@@ -507,15 +507,19 @@ def _input_type(x, name):
     return x.dtype
 
 
-def _on_device(t, stream, fn, *args):
-    """fn(*args) on `stream` (None: the current one) of t's device, that device current."""
+def _launch(name, t, stream, tensors, sizes, *rest):
+    """The C call `name` on `stream` (None: the current one) of t's device, that device current:
+    pointers of `tensors` (or None), sizes, `rest`.  As the mirrors above, in less host time."""
     import torch
 
     index = t.get_device()
-    if index == torch.cuda.current_device():
-        return fn(*args, stream=stream)
-    with torch.cuda.device(index):
-        return fn(*args, stream=stream)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch(name, t, stream, tensors, sizes, *rest)
+    status = getattr(_lib or library(), name)(
+        *[None if v is None else v.data_ptr() for v in tensors], *sizes, *rest, _stream(stream))
+    if status != GDR_OK:
+        raise GdrError(name, status)
 
 
 def _empty(t, stream, *specs):
@@ -541,12 +545,14 @@ def _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens):
     if x.dim() != 3:
         raise ValueError(f"x must be [B, T, C], got shape {tuple(x.shape)}")
     B, T, C = shape = x.shape
+    _int_sizes(shape)
     f32 = torch.float32
     nseq = B
     if cu_seqlens is not None:
         if B != 1:
             raise ValueError("packed sequences need B == 1")
         nseq = cu_seqlens.numel() - 1
+        _int_sizes((nseq,))
     _check(x, ("x", x, dtype, shape, False), ("a", a, dtype, shape, False),
            ("b", b, dtype, shape, False), ("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), True),
            ("A_log", A_log, f32, (C,), True), ("dt_bias", dt_bias, f32, (C,), True),
@@ -572,9 +578,8 @@ def linear_recurrence(x, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None,
         out, = _empty(x, stream, (x.shape, f32))
     if final_state is None:
         final_state, = _empty(x, stream, ((nseq, C), f32))
-    fn = gdr_linear_recurrence_f32 if dtype == f32 else gdr_linear_recurrence
-    _on_device(x, stream, fn, x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens,
-               nseq, T, C, ld)
+    _launch("gdr_linear_recurrence_f32" if dtype is f32 else "gdr_linear_recurrence", x, stream,
+            (x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens), (nseq, T, C, ld))
     return out, final_state
 
 
@@ -603,17 +608,22 @@ def linear_recurrence_backward(x, a, b, A_log, dt_bias, out, grad_out, grad_fina
         ld_grad = _token_stride(grads, x.shape[0], T, C)
     grad_A_log, grad_dt_bias, grad_init = _empty(x, stream, ((C,), f32), ((C,), f32),
                                                  ((nseq, C), f32))
-    fn = (gdr_linear_recurrence_backward_f32 if dtype == f32 else
-          gdr_linear_recurrence_backward)
-    _on_device(x, stream, fn, x, a, b, A_log, dt_bias, init_state, out, grad_out,
-               grad_final_state, *grads, grad_A_log, grad_dt_bias, grad_init, cu_seqlens, nseq, T,
-               C, ld, ld_grad)
+    _launch("gdr_linear_recurrence_backward_f32" if dtype is f32 else
+            "gdr_linear_recurrence_backward", x, stream,
+            (x, a, b, A_log, dt_bias, init_state, out, grad_out, grad_final_state, *grads,
+             grad_A_log, grad_dt_bias, grad_init, cu_seqlens), (nseq, T, C, ld, ld_grad))
     return (*grads, grad_A_log, grad_dt_bias, grad_init)
+
+
+def _int_sizes(shape):
+    if max(shape) > _INT_MAX:  # ctypes would drop the upper bits
+        raise ValueError(f"sizes have to be below 2^31, got {tuple(shape)}")
 
 
 def _row_args(x):
     """(rows, d) of x [..., d]."""
     d = x.shape[-1] if x.dim() else 0
+    _int_sizes((d,))
     return (x.numel() // d if d else 0), d
 
 
@@ -630,8 +640,8 @@ def layer_norm(x, weight, bias=None, eps=1e-5, y=None, stream=None):
     mean, rstd = _empty(x, stream, (x.shape[:-1], f32), (x.shape[:-1], f32))
     if y is None:
         y, = _empty(x, stream, (x.shape, dtype))
-    fn = gdr_layer_norm_f32 if dtype == f32 else gdr_layer_norm
-    _on_device(x, stream, fn, x, weight, bias, y, mean, rstd, rows, d, eps)
+    _launch("gdr_layer_norm_f32" if dtype is f32 else "gdr_layer_norm", x, stream,
+            (x, weight, bias, y, mean, rstd), (rows, d), float(eps))
     return y, mean, rstd
 
 
@@ -648,9 +658,8 @@ def layer_norm_backward(x, weight, mean, rstd, grad_y, grad_x=None, stream=None)
     if grad_x is None:
         grad_x, = _empty(x, stream, (x.shape, dtype))
     grad_weight, grad_bias = _empty(x, stream, ((d,), f32), ((d,), f32))
-    fn = gdr_layer_norm_backward_f32 if dtype == f32 else gdr_layer_norm_backward
-    _on_device(x, stream, fn, x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias, rows,
-               d)
+    _launch("gdr_layer_norm_backward_f32" if dtype is f32 else "gdr_layer_norm_backward", x, stream,
+            (x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias), (rows, d))
     return grad_x, grad_weight, grad_bias
 
 
@@ -665,14 +674,16 @@ def short_conv_silu_backward(x, weight, grad_y, bias=None, conv_state_in=None,
     if x.dim() != 3:
         raise ValueError(f"x must be [B, T, C], got shape {tuple(x.shape)}")
     B, T, C = x.shape
+    _int_sizes(x.shape)
     _check(x, ("x", x, bf16, x.shape, True), ("weight", weight, f32, (C, 4), True),
            ("grad_y", grad_y, bf16, x.shape, True), ("bias", bias, f32, (C,), True),
            ("conv_state_in", conv_state_in, f32, (B, C, 3), True),
            ("grad_conv_state_out", grad_conv_state_out, f32, (B, C, 3), True))
     grad_x, grad_weight, grad_bias, grad_state = _empty(
         x, stream, (x.shape, bf16), ((C, 4), f32), ((C,), f32), ((B, C, 3), f32))
-    _on_device(x, stream, gdr_short_conv_silu_backward, x, weight, bias, conv_state_in, grad_y,
-               grad_conv_state_out, grad_x, grad_weight, grad_bias, grad_state, B, T, C)
+    _launch("gdr_short_conv_silu_backward", x, stream,
+            (x, weight, bias, conv_state_in, grad_y, grad_conv_state_out, grad_x, grad_weight,
+             grad_bias, grad_state), (B, T, C, 4))
     return grad_x, grad_weight, grad_bias, grad_state
 
 
@@ -687,6 +698,6 @@ def gated_rmsnorm_backward(o, z, weight, grad_y, eps=1e-6, stream=None):
     _check(o, ("o", o, f32, o.shape, True), ("z", z, dtype, o.shape, True),
            ("weight", weight, f32, (d,), True), ("grad_y", grad_y, f32, o.shape, True))
     grad_o, grad_z, grad_weight = _empty(o, stream, (o.shape, f32), (z.shape, dtype), ((d,), f32))
-    fn = gdr_gated_rmsnorm_backward_f32 if dtype == f32 else gdr_gated_rmsnorm_backward
-    _on_device(o, stream, fn, o, z, weight, grad_y, grad_o, grad_z, grad_weight, rows, d, eps)
+    _launch("gdr_gated_rmsnorm_backward_f32" if dtype is f32 else "gdr_gated_rmsnorm_backward", o,
+            stream, (o, z, weight, grad_y, grad_o, grad_z, grad_weight), (rows, d), float(eps))
     return grad_o, grad_z, grad_weight

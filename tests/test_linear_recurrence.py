@@ -483,6 +483,18 @@ def test_sizes_that_would_wrap_to_others_are_refused(kw):
     assert _fwd(**kw) == gdr.GDR_ERR_SHAPE and _bwd(**kw) == gdr.GDR_ERR_SHAPE
 
 
+def test_binding_refuses_sizes_that_would_wrap():
+    p = torch.zeros(8)
+    long = torch.zeros(1, 1, 8).expand(1, 2 ** 32 + 4, 8)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gdr.linear_recurrence(long, long, long, p, p)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gdr.short_conv_silu_backward(long, p, long)
+    wide = torch.zeros(1, 1).expand(1, 2 ** 32 + 8)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gdr.layer_norm(wide, p)
+
+
 def test_binding_refuses_cpu_tensors():
     x, p = torch.zeros(1, 4, 8), torch.zeros(8)
     with pytest.raises(ValueError, match="CUDA"):
