@@ -236,9 +236,9 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
 // What bounds it (B200, bf16): with as many units as SMs the backward pass runs at a copy's rate
 // ([1, 8192, 9472] 236 us) and the forward pass at 0.86 of it (137 us), where the
 // special-function unit does eight operations per token and channel pair; other calls lose to
-// their last wave, to CTA starts and to the exchanges.  Forward [8, 1024, 6144] 98 us (0.78 of a
-// copy's rate), [1, 8192, 6144] 110 us (0.70), [1, 65536, 1024] 155 us (0.66); backward 179 us
-// (0.86), 195 us (0.79), 270 us (0.76).
+// their last wave, to CTA starts and to the exchanges.  Forward [8, 1024, 6144] 88 us (0.87 of a
+// copy's rate), [1, 8192, 6144] 110 us (0.70), [1, 65536, 1024] 155 us (0.66); backward 170 us
+// (0.90), 195 us (0.79), 270 us (0.76).
 //
 // Decays are composed as sums of log-decays.  From tile to tile a factor P near 1 acts
 // through W = P - 1, formed as expm1 of its tile's sum: a slow channel's state lasts over
@@ -963,6 +963,9 @@ bool make_maps(Maps& m, const RecurrenceParams& p, const float* dout, int box) {
 
 // The forms of each kernel: warps, tokens per warp, slots, CTAs per cluster at most.  One: no
 // cluster, a CTA per SM.  Many: no cluster, two CTAs per SM, whose phases and starts overlap.
+// Crowd: no cluster, three small ones per SM, for dense calls of more units than Many takes at
+// once: their starts and their last wave cost less ([8, 1024, 6144] forward 88 against 98 us,
+// [64, 200, 6144] 140 against the sequential form's 182).
 // Wide: clusters with one CTA per SM, for few units; its tiles are the largest that the slots
 // hold, since a step's exchange costs the same 0.6 us for any.  Pair: clusters with two CTAs
 // per SM, for units in between (a cluster's CTAs share SMs, so it needs enough clusters).
@@ -975,18 +978,22 @@ template <> struct Forms<__nv_bfloat16> {
     struct Fwd {
         using One = TileSmem<T, 8, 20, 2, 1, false>;
         using Many = TileSmem<T, 8, 12, 2, 1, false>;
+        using Crowd = TileSmem<T, 4, 16, 2, 1, false>;
         using Wide = TileSmem<T, 8, 32, 2, 12, false>;
         using Pair = TileSmem<T, 8, 12, 2, 4, false>;
-        static constexpr double kOne = 2600, kMany = 3140, kWide = 4450, kPair = 3350;
-        static constexpr double kStart = 1500, kManyStart = 300, kWideStart = 4500, kPairStart = 300;
+        static constexpr double kOne = 2600, kMany = 3140, kCrowd = 2500, kWide = 4450, kPair = 3350;
+        static constexpr double kStart = 1500, kManyStart = 300, kCrowdStart = 1800,
+                                kWideStart = 4500, kPairStart = 300;
     };
     struct Bwd {
         using One = TileSmem<T, 8, 10, 3, 1, true>;
         using Many = TileSmem<T, 8, 8, 2, 1, true>;
+        using Crowd = TileSmem<T, 4, 11, 2, 1, true>;
         using Wide = TileSmem<T, 8, 14, 2, 12, true>;
         using Pair = TileSmem<T, 8, 7, 2, 4, true>;
-        static constexpr double kOne = 2200, kMany = 3370, kWide = 3550, kPair = 3600;
-        static constexpr double kStart = 3400, kManyStart = 6000, kWideStart = 6000, kPairStart = 1500;
+        static constexpr double kOne = 2200, kMany = 3370, kCrowd = 3300, kWide = 3550, kPair = 3600;
+        static constexpr double kStart = 3400, kManyStart = 6000, kCrowdStart = 4000,
+                                kWideStart = 6000, kPairStart = 1500;
     };
 };
 template <> struct Forms<float> {
@@ -994,23 +1001,27 @@ template <> struct Forms<float> {
     struct Fwd {
         using One = TileSmem<T, 8, 12, 2, 1, false>;
         using Many = TileSmem<T, 8, 8, 2, 1, false>;
+        using Crowd = TileSmem<T, 4, 10, 2, 1, false>;
         using Wide = TileSmem<T, 8, 16, 2, 12, false>;
         using Pair = TileSmem<T, 8, 6, 2, 4, false>;
-        static constexpr double kOne = 2110, kMany = 2350, kWide = 2850, kPair = 2250;
-        static constexpr double kStart = 1500, kManyStart = 300, kWideStart = 4500, kPairStart = 300;
+        static constexpr double kOne = 2110, kMany = 2350, kCrowd = 2450, kWide = 2850, kPair = 2250;
+        static constexpr double kStart = 1500, kManyStart = 300, kCrowdStart = 1800,
+                                kWideStart = 4500, kPairStart = 300;
     };
     struct Bwd {
         using One = TileSmem<T, 8, 6, 3, 1, true>;
         using Many = TileSmem<T, 8, 6, 2, 1, true>;
+        using Crowd = TileSmem<T, 4, 7, 2, 1, true>;
         using Wide = TileSmem<T, 8, 12, 2, 12, true>;
         using Pair = TileSmem<T, 8, 5, 2, 4, true>;
-        static constexpr double kOne = 2230, kMany = 3490, kWide = 4100, kPair = 3000;
-        static constexpr double kStart = 3400, kManyStart = 6000, kWideStart = 6000, kPairStart = 1500;
+        static constexpr double kOne = 2230, kMany = 3490, kCrowd = 3450, kWide = 4100, kPair = 3000;
+        static constexpr double kStart = 3400, kManyStart = 6000, kCrowdStart = 2500,
+                                kWideStart = 6000, kPairStart = 1500;
     };
 };
 constexpr double kWideRank = 10, kPairRank = 50;  // a step's further ns for each CTA of the cluster
 
-enum Form { kOneForm, kManyForm, kWideForm, kPairForm };
+enum Form { kOneForm, kManyForm, kCrowdForm, kWideForm, kPairForm };
 
 template <typename F>
 void offer_single(Plan* plan, const RecurrenceParams& p) {
@@ -1019,11 +1030,15 @@ void offer_single(Plan* plan, const RecurrenceParams& p) {
         offer(plan, p, kOneForm, 1, sms, F::One::kRows, F::kOne, F::kStart, false);
     else
         offer(plan, p, kManyForm, 1, 2LL * sms, F::Many::kRows, F::kMany, F::kManyStart, false);
+    // packed sequences may be uneven, and the longest then waits for a slower CTA
+    if (units_of(p) > 2LL * sms && !p.cu_seqlens)
+        offer(plan, p, kCrowdForm, 1, 3LL * sms, F::Crowd::kRows, F::kCrowd, F::kCrowdStart, false);
 }
 
 // Whether the sequential form is the faster one: a chain of tokens, each at least a memory latency
-// and at least its bytes' time, against a plan.  It is for short sequences (64 sequences of
-// 6144 channels, forward: 31 against 82 us at 32 tokens, 117 against 134 at 128; one
+// and at least its bytes' time (backward in fp32, eight streams of wide rows, at half of a
+// copy's rate), against a plan.  It is for short sequences (64 sequences of 6144 channels,
+// forward: 31 against 82 us at 32 tokens, 59 against 58 at 64, 116 against 90 at 128; one
 // sequence: 16 against 8 at 16).  Of packed sequences only the mean length is known here; one
 // that holds most of the tokens may cost the sequential form at most 20 times a plan.
 bool sequential(const RecurrenceParams& p, const Plan& plan, double latency_ns, double channel_ns) {
@@ -1105,7 +1120,7 @@ cudaError_t forward(const RecurrenceParams& p, cudaStream_t stream) {
     static Capacity wide, pair;
     Plan plan = {};
     offer_single<F>(&plan, p);
-    if (sequential(p, plan, 620, 0.0023)) {
+    if (sequential(p, plan, 620, sizeof(Tin) == 2 ? 0.0023 : 0.0026)) {
         const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads),
                         (unsigned)std::min(p.nseq, 65535));
         recurrence_seq_kernel<Tin><<<grid, kSeqThreads, 0, stream>>>(p);
@@ -1122,6 +1137,7 @@ cudaError_t forward(const RecurrenceParams& p, cudaStream_t stream) {
     switch (plan.form) {
         case kOneForm: return forward_tiles<typename F::One, 1>(p, plan, stream);
         case kManyForm: return forward_tiles<typename F::Many, 2>(p, plan, stream);
+        case kCrowdForm: return forward_tiles<typename F::Crowd, 3>(p, plan, stream);
         case kWideForm: return forward_tiles<typename F::Wide, 1>(p, plan, stream);
         default: return forward_tiles<typename F::Pair, 2>(p, plan, stream);
     }
@@ -1133,7 +1149,7 @@ cudaError_t backward(const RecurrenceParams& p, const RecurrenceGrads& r, cudaSt
     static Capacity wide, pair;
     Plan plan = {};
     offer_single<F>(&plan, p);
-    if (sequential(p, plan, 750, 0.0038)) {
+    if (sequential(p, plan, 750, sizeof(Tin) == 2 ? 0.0038 : 0.0088)) {
         const int rows = seq_rows(p);
         float* part = nullptr;
         cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);
@@ -1157,6 +1173,7 @@ cudaError_t backward(const RecurrenceParams& p, const RecurrenceGrads& r, cudaSt
     switch (plan.form) {
         case kOneForm: return backward_tiles<typename F::One, 1>(p, r, plan, stream);
         case kManyForm: return backward_tiles<typename F::Many, 2>(p, r, plan, stream);
+        case kCrowdForm: return backward_tiles<typename F::Crowd, 3>(p, r, plan, stream);
         case kWideForm: return backward_tiles<typename F::Wide, 1>(p, r, plan, stream);
         default: return backward_tiles<typename F::Pair, 2>(p, r, plan, stream);
     }
