@@ -313,6 +313,35 @@ __device__ __forceinline__ void store_peer(float4* p, uint64_t* bar, uint32_t ra
                  ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
                  : "memory");
 }
+// Waits for the phase of `bar` that other CTAs' asynchronous stores complete; false if they did not
+// come within the limit.  The stores' completion releases at cluster scope, so the wait acquires
+// there too: at the default scope, the CTA's, nothing would order the peers' data before the
+// reads behind the wait.  (The TMA barriers' completion is this CTA's own: their waits keep the default.)
+__device__ __forceinline__ bool peers_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool peers_wait_slow(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = tc::globaltimer();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            __nanosleep(tc::kPollSleepNs);
+            if (peers_test(bar, parity)) return true;
+        }
+        if (tc::globaltimer() - t0 > tc::kWaitLimitNs) return false;
+    }
+}
+__device__ __forceinline__ bool peers_wait(uint64_t* bar, uint32_t parity) {
+    return peers_test(bar, parity) || peers_wait_slow(bar, parity);
+}
 __device__ __forceinline__ float2 smem_pair(const float* p) {
     return *reinterpret_cast<const float2*>(p);
 }
@@ -392,7 +421,7 @@ __device__ __forceinline__ float2 start_state(Smem& sm, const Joined& j, int lan
     const int step = j.step;
     float2 in = S;
     if constexpr (Cluster) {
-        if (!dead && !tc::mbar_wait(&sm.peers_in[step & 1], (uint32_t)(step >> 1) & 1u)) {
+        if (!dead && !peers_wait(&sm.peers_in[step & 1], (uint32_t)(step >> 1) & 1u)) {
             dead = true;
             if (lane == 0) atomicExch(&g_recurrence_status, 1);
         }
