@@ -6,7 +6,7 @@
 //          the three inputs before the call (the state) get the same sum, and the gradient of
 //          the state after the call goes to the inputs it copies.
 //   norm   y = o r w SiLU(z),  r = 1 / sqrt(mean(o^2) + eps),  q = dy w SiLU(z):
-//              do = r q - o r^3 mean(q o),  dz = dy o r w SiLU'(z),  dw = sum_rows dy o r SiLU(z).
+//              do = r (q - n mean(q n)),  dz = dy n w SiLU'(z),  dw = sum_rows dy n SiLU(z),  n = o r.
 // Both are bound by memory: every input is read once, s and r are computed again instead of
 // being kept by the forward pass.  Parameter gradients leave each CTA as one row of partial
 // sums, which column_sum.cu adds in a fixed order.
@@ -366,15 +366,17 @@ gated_rmsnorm_backward_kernel(NormGrads p, float* part) {
             ss += __shfl_xor_sync(0xffffffffu, ss, k);
             qo += __shfl_xor_sync(0xffffffffu, qo, k);
         }
+        // n = o r before it meets anything else: powers of r leave fp32's range (r^3 is zero for
+        // rows of 1e15, infinite for rows of 1e-13) where the gradient does not
         const float r = 1.0f / sqrtf(ss / (float)D + p.eps);
-        const float m = r * r * r * (qo / (float)D);
+        const float m = r * (qo / (float)D);
         float go[4], gz[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            go[e] = r * q[e] - o[e] * m;
-            const float gor = g[e] * o[e] * r;
-            gz[e] = gor * w[e] * dsilu[e];
-            if (live) acc[e] += gor * silu[e];
+            const float n = o[e] * r, gn = g[e] * n;
+            go[e] = r * (q[e] - n * m);
+            gz[e] = gn * w[e] * dsilu[e];
+            if (live) acc[e] += gn * silu[e];
         }
         if (live) {
             store_z4(p.grad_o + at, go);

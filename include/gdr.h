@@ -368,8 +368,8 @@ GDR_API int gdr_short_conv_silu_backward(const void* x, const float* weight, con
  * gdr_gated_rmsnorm_backward: from o, z, weight and eps as given to gdr_gated_rmsnorm and
  * the gradient grad_y of its y (fp32, o's layout), with r = 1 / sqrt(mean(o^2) + eps) and
  * q = grad_y weight SiLU(z):
- *   grad_o = r q - o r^3 mean(q o) (fp32),  grad_z = grad_y o r weight SiLU'(z) (z's type),
- *   grad_weight [d] = sum over the rows of grad_y o r SiLU(z) (fp32; zeros for no rows).
+ *   grad_o = r (q - n mean(q n)) (fp32),  grad_z = grad_y n weight SiLU'(z) (z's type),
+ *   grad_weight [d] = sum over the rows of grad_y n SiLU(z) (fp32; zeros for no rows), n = o r.
  * grad_y, grad_o and weight 16-byte aligned, grad_z as z.  grad_o may be grad_y or o, and
  * grad_z may be z.
  */

@@ -187,6 +187,37 @@ def test_gated_rmsnorm(rows, d, zf32):
 
 
 @gpu
+@pytest.mark.parametrize("zf32", [False, True])
+@pytest.mark.parametrize("scale,eps", [(1e12, 1e-6), (1e15, 1e-6), (1e17, 1e-6), (1e-13, 0.0),
+                                       (1e-17, 0.0)])
+def test_gated_rmsnorm_of_rows_whose_cubed_norm_no_float_holds(scale, eps, zf32):
+    """r^3 underflows for large rows and overflows for small ones, the gradient does not; the
+    tolerance is that of the test above with n = o r in the place of o (every factor that is
+    rounded is of the size of a factor there)"""
+    rng = np.random.default_rng(6)
+    rows, d = 90, 64
+    n, z, q = (rng.standard_normal((rows, d)).astype(np.float32) for _ in range(3))
+    o = n * np.float32(scale)
+    if not zf32:
+        z = synth.round_to_bf16(z)
+    dy = q + n * np.sign(z)  # a part along o, so that the second term counts
+    w = rng.uniform(0.5, 1.5, d).astype(np.float32)
+    got = gdr.gated_rmsnorm_backward(dev(o), dev(z, torch.float32 if zf32 else torch.bfloat16),
+                                     dev(w), dev(dy), eps)
+    torch.cuda.synchronize()
+    do, dz, dw = block.gated_rmsnorm_backward(o, z, w, dy, eps)
+    o, z, dy = (v.astype(np.float64) for v in (o, z, dy))
+    r = 1 / np.sqrt((o * o).mean(1, keepdims=True) + eps)
+    n, q = o * r, np.abs(dy * w * mixer_io.silu(z))
+    E = 2.0 ** -18
+    within(got[0], do, E * r * (q + np.abs(n) * (q * np.abs(n)).mean(1, keepdims=True)), "do")
+    within(got[1], dz, E * np.abs(dy * n * w) * (1 + np.abs(z)) +
+           (2.0 ** -24 if zf32 else H) * np.abs(dz) + 1e-30, "dz")
+    terms = np.abs(dy * n * mixer_io.silu(z)).sum(0)
+    within(got[2], dw, (E + rows / 64 * 2.0 ** -24) * 2 * terms + 1e-30, "dweight")
+
+
+@gpu
 def test_gated_rmsnorm_in_place_and_no_rows():
     rng = np.random.default_rng(3)
     o, z, dy = (dev(rng.standard_normal((100, 64)).astype(np.float32)) for _ in range(3))
