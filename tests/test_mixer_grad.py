@@ -218,6 +218,24 @@ def test_gated_rmsnorm_of_rows_whose_cubed_norm_no_float_holds(scale, eps, zf32)
 
 
 @gpu
+@pytest.mark.parametrize("zf32", [False, True])
+@pytest.mark.parametrize("lo,hi", [(-80, -20), (-20, -4), (-4, 4), (4, 90)])
+def test_gated_rmsnorm_keeps_the_gate_to_fp32_rounding(lo, hi, zf32):
+    """one row of ones without eps: r = 1 and n = 1 exactly, so dweight is SiLU(z) as computed:
+    an exponential of at most two ulps (2^-22), a sum, a quotient and a product (2^-24 each):
+    below 2^-21 of each value"""
+    ones = torch.ones(1, 128, device="cuda")
+    for seed in range(4):
+        z = np.random.default_rng(seed).uniform(lo, hi, (1, 128)).astype(np.float32)
+        if not zf32:
+            z = synth.round_to_bf16(z)
+        zd = dev(z, torch.float32 if zf32 else torch.bfloat16)
+        dw = gdr.gated_rmsnorm_backward(ones, zd, ones[0], ones, 0.0)[2]
+        ref = mixer_io.silu(z[0].astype(np.float64))
+        within(dw, ref, 2.0 ** -21 * np.abs(ref) + 1e-36, "dweight")
+
+
+@gpu
 def test_gated_rmsnorm_in_place_and_no_rows():
     rng = np.random.default_rng(3)
     o, z, dy = (dev(rng.standard_normal((100, 64)).astype(np.float32)) for _ in range(3))
