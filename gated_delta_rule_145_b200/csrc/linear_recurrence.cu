@@ -36,6 +36,16 @@ __device__ __forceinline__ float rcpf(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The decay 2^y of a token or of several: never zero, so that an infinite state stays infinite in
+// every form and not only where no product of decays underflows (0 inf).  Times a finite state
+// the floor, the smallest float, is nothing.  A NaN stays one (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+__device__ __forceinline__ float decay(float y) { return max_nan(ex2f(y), 1.4e-45f); }
+__device__ __forceinline__ float2 decay(float2 y) { return make_float2(decay(y.x), decay(y.y)); }
 __device__ __forceinline__ float2 ex2f2(float2 v) { return make_float2(ex2f(v.x), ex2f(v.y)); }
 __device__ __forceinline__ float2 rcpf2(float2 v) { return make_float2(rcpf(v.x), rcpf(v.y)); }
 __device__ __forceinline__ float2 bcast2(float v) { return make_float2(v, v); }
@@ -122,7 +132,7 @@ __device__ __forceinline__ void seq_bounds(const int32_t* cu, int s, int T, long
 __device__ __forceinline__ float2 decay_factors(float2 a, float2 prev, const Channels& ch, float2& lam,
                                                 float2& fa, float2& fA) {
     const Gate g = decay_gate(a, ch);
-    lam = ex2f2(g.y);
+    lam = decay(g.y);
     const float2 rz = rcpf2(__fadd2_rn(g.t, bcast2(1.f))), tz = __fmul2_rn(g.t, rz);
     const float2 slope = make_float2(g.zl.x >= 0.f ? rz.x : tz.x, g.zl.y >= 0.f ? rz.y : tz.y);
     const float2 lp = __fmul2_rn(lam, prev);
@@ -176,7 +186,7 @@ recurrence_seq_kernel(RecurrenceParams p) {
             const float2 xv = load_pair(x + t * p.ld), av = load_pair(a + t * p.ld),
                          bv = load_pair(b + t * p.ld);
             const Gate g = decay_gate(av, ch);
-            h = __ffma2_rn(ex2f2(g.y), h, gated_input(xv, bv));
+            h = __ffma2_rn(decay(g.y), h, gated_input(xv, bv));
             store_pair(p.out + t * p.C + c, h);
         }
         if (p.final_state) *reinterpret_cast<float2*>(p.final_state + at) = h;
@@ -281,11 +291,13 @@ __device__ __forceinline__ float code_factor(float y) {
     q = fmaf(q, y, 5.549040809e-02f);
     q = fmaf(q, y, 2.402256429e-01f);
     q = fmaf(q, y, 6.931471825e-01f);
-    return y > -0.5f ? __int_as_float(__float_as_int(q * y) | 0x80000000) : ex2f(y);
+    return y > -0.5f ? __int_as_float(__float_as_int(q * y) | 0x80000000) : decay(y);
 }
-// S <- 2^y S + H, the factor coded
+// S <- 2^y S + H, the factor coded.  An infinite S enters the product W S as the largest float: W is
+// negative, and W S + S would be -inf + inf.
 __device__ __forceinline__ float carry(float S, float code, float H) {
-    return fmaf(code, S, H) + (__float_as_int(code) < 0 ? S : 0.f);
+    const float most = 3.402823466e38f, F = fminf(fmaxf(S, -most), most);
+    return __float_as_int(code) < 0 ? fmaf(code, F, H) + S : fmaf(code, S, H);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -401,7 +413,7 @@ __device__ __forceinline__ Joined publish(Smem& sm, int step, int warp, int lane
     }
     Joined j;
     j.step = step;
-    j.P = ex2f2(Gp);
+    j.P = decay(Gp);
     j.H = Hp;
     j.all = make_float4(code_factor(G.x), code_factor(G.y), H.x, H.y);
     if constexpr (Cluster) {
@@ -615,7 +627,7 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
                 const float2 av = smem_pair(row + (kRows + i) * kStrip);
                 const float2 bv = smem_pair(row + (2 * kRows + i) * kStrip);
                 const float2 y = decay_gate(av, ch).y;
-                k.lam[i] = ex2f2(y);
+                k.lam[i] = decay(y);
                 k.u[i] = gated_input(xv, bv);
                 G = __fadd2_rn(G, y);
                 H = __ffma2_rn(k.lam[i], H, k.u[i]);
@@ -634,7 +646,7 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
                     }
                 }
             }
-            sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
+            sm.part[buf][w.warp][w.lane] = make_float4(decay(G.x), decay(G.y), H.x, H.y);
             sm.log_part[buf][w.warp][w.lane] = G;
             __syncthreads();
             // every warp has read the tile: its slot takes another
@@ -794,7 +806,7 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
                 }
             }
             if (step + 1 < part.s1) load_prev(step + 1);
-            sm.part[buf][w.warp][w.lane] = make_float4(ex2f(G.x), ex2f(G.y), H.x, H.y);
+            sm.part[buf][w.warp][w.lane] = make_float4(decay(G.x), decay(G.y), H.x, H.y);
             sm.log_part[buf][w.warp][w.lane] = G;
             __syncthreads();
             // every warp is done with the step before: its slot takes another tile

@@ -433,6 +433,7 @@ GDR_API int gdr_layer_norm_backward_f32(const float* x, const float* weight, con
  * [cu_seqlens[0], cu_seqlens[B]) are left as they were.  Sequences of length 0 are allowed: their
  * final state is their initial one.  C and ld multiples of 8, ld >= C, fewer than 2^31 - 256
  * tokens; x, a, b, out and the states 16-byte aligned.  A decode step is a call with T = 1.
+ * A state that has become infinite stays infinite: exp(g) counts as positive where it underflows.
  */
 GDR_API int gdr_linear_recurrence(const void* x, const void* a, const void* b,
                                   const float* A_log, const float* dt_bias,

@@ -309,6 +309,48 @@ def test_infinite_and_nan_inputs_stay_in_their_channel_and_after_their_token():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C", [(2, 40, 64), (1, 300, 64), (1, 5000, 192), (3, 3000, 2048),
+                                   (160, 256, 136), (5, 1300, 4104)])
+def test_an_infinite_state_stays_infinite(B, T, C, dtype):
+    """whatever form takes the call: no tile border makes inf - inf of it, nor an underflowing decay,
+    of one token or of many, 0 inf; the same for its gradient"""
+    m = make(B, T, C, dtype, seed=21)
+    m["A_log"][::2], m["A_log"][1::2] = synth.LN16, -2.0  # 2^-40 per token or so, some 2^-130; and slow
+    m["dt_bias"][::2], m["dt_bias"][1::2] = 1.5, -4.0
+    m["x"][0, 7, ::5], m["x"][0, 9, 1::5] = np.inf, -np.inf
+    m["init"][-1, 2::5] = np.inf
+    m["go"][0, T - 5, 3::5] = -np.inf
+    got = on_gpu(m)[1]
+    m, got = some_channels(m, got, max(1, B * T * C // 3_000_000) | 1)
+    with np.errstate(invalid="ignore"):
+        ref, mag = expected(m)
+    for i in (0, 1, 2, 7):  # h, the final state, dx and dinit
+        g, r = got[i].float().cpu().numpy(), ref[i]
+        assert np.isinf(r).any() and not np.isnan(r).any()
+        assert np.array_equal(np.isinf(g), np.isinf(r)), NAMES[i]
+        assert (g[np.isinf(r)] == r[np.isinf(r)]).all(), NAMES[i]
+    with np.errstate(invalid="ignore"):
+        check(m, [got[i] for i in (0, 1, 2)], ref[:3], mag[:3], T)
+
+
+@gpu
+@pytest.mark.parametrize("B,T,C", [(2, 40, 64), (1, 300, 64), (1, 5000, 192), (5, 1300, 4104)])
+def test_a_nan_gate_makes_the_state_nan(B, T, C):
+    m = make(B, T, C, "f32", seed=22)
+    m["a"][0, 20, 3], m["b"][0, 21, 5] = np.nan, np.nan
+    got = on_gpu(m)[1]
+    hit = torch.zeros_like(got[0], dtype=torch.bool)
+    hit[0, 20:, 3] = True
+    hit[0, 21:, 5] = True
+    assert torch.equal(torch.isnan(got[0]), hit) and torch.equal(torch.isnan(got[1]), hit[:, -1])
+    back = torch.zeros_like(hit)  # the gradients of what a NaN decay hands on
+    back[0, :20, 3] = True
+    assert torch.isnan(got[2][back]).all() and torch.isnan(got[7][0, 3])
+    assert torch.isnan(got[5][3]) and torch.isnan(got[6][3]) and torch.isnan(got[4][0, 21, 5])
+
+
+@gpu
 @pytest.mark.parametrize("T0", [1, 40, 300])
 def test_steps_continue_a_prompt_in_place(T0):
     """a prompt, then single-token calls that update the state in place, equal one call"""
