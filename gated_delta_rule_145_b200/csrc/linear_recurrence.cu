@@ -137,7 +137,8 @@ __device__ __forceinline__ float2 decay_factors(float2 a, float2 prev, const Cha
     const float2 slope = make_float2(g.zl.x >= 0.f ? rz.x : tz.x, g.zl.y >= 0.f ? rz.y : tz.y);
     const float2 lp = __fmul2_rn(lam, prev);
     fa = __fmul2_rn(__fmul2_rn(lp, ch.A), slope);
-    fA = __fmul2_rn(lp, g.y);
+    // (a at its type's highest value makes the log-decay infinite: lam times it would be NaN, not 0)
+    fA = __fmul2_rn(lp, make_float2(max_nan(g.y.x, -1024.f), max_nan(g.y.y, -1024.f)));
     return g.y;
 }
 // Those in dx and db.

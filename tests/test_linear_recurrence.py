@@ -294,6 +294,24 @@ def test_extreme_gates(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C", [(2, 5, 64), (2, 300, 64), (1, 5000, 192), (5, 1300, 4104)])
+def test_gates_masked_with_the_highest_and_lowest_values(B, T, C, dtype):
+    """a and b at the type's ends, as masks write them: the state is forgotten or kept, the input gate
+    shut or open, and every gradient is finite"""
+    m = make(B, T, C, dtype, seed=23)
+    high = torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).max
+    m["a"][:, 2::9], m["a"][:, 3::11, ::2] = high, -high
+    m["a"][:, 4::13, 1::2] = -np.inf
+    m["b"][:, 1::7], m["b"][:, 2::5, ::2], m["b"][:, 3::17, 1::2] = -high, high, -np.inf
+    got = on_gpu(m)[1]
+    m, got = some_channels(m, got, max(1, B * T * C // 3_000_000) | 1)
+    ref, mag = expected(m)
+    assert all(np.isfinite(r).all() for r in ref)
+    check(m, got, ref, mag, T)
+
+
+@gpu
 def test_infinite_and_nan_inputs_stay_in_their_channel_and_after_their_token():
     m = make(2, 200, 64, "f32", seed=12, init=False)
     clean = on_gpu(m)[1]
