@@ -74,8 +74,8 @@ struct Channels {
 
 // zl = log2(e) z for z = a + dt_bias; t = e^{-|z|} in (0, 1]; y = A log2(e) softplus(z), the
 // base-2 log-decay.  softplus(z) = max(z, 0) + log1p(t) and log2(e) log1p(t) = t Q(t), Q the
-// degree-8 polynomial whose largest relative error on [0, 1] is smallest (3e-8; a weighted
-// least-squares fit).  Small values of softplus are slow channels, whose state sums over
+// degree-8 polynomial whose largest relative error on [0, 1] is smallest (3.2e-8; a linear program,
+// each coefficient rounded to fp32 before the next ones are fitted).  Small values of softplus are slow channels, whose state sums over
 // many tokens: there the relative error of the log-decay, not the absolute one, is what the
 // result sees, so log(1 + t) from the special-function unit (absolute error) will not do.
 struct Gate {
@@ -85,14 +85,14 @@ __device__ __forceinline__ Gate decay_gate(float2 a, const Channels& ch) {
     Gate g;
     g.zl = __ffma2_rn(a, bcast2(kLog2e), ch.bias);
     g.t = ex2f2(make_float2(-fabsf(g.zl.x), -fabsf(g.zl.y)));
-    float2 q = bcast2(7.549088448e-03f);
-    q = __ffma2_rn(q, g.t, bcast2(-4.256669804e-02f));
-    q = __ffma2_rn(q, g.t, bcast2(1.128556207e-01f));
-    q = __ffma2_rn(q, g.t, bcast2(-1.971185058e-01f));
-    q = __ffma2_rn(q, g.t, bcast2(2.756412029e-01f));
-    q = __ffma2_rn(q, g.t, bcast2(-3.584084213e-01f));
-    q = __ffma2_rn(q, g.t, bcast2(4.806929529e-01f));
-    q = __ffma2_rn(q, g.t, bcast2(-7.213401794e-01f));
+    float2 q = bcast2(7.650659885e-03f);
+    q = __ffma2_rn(q, g.t, bcast2(-4.299838841e-02f));
+    q = __ffma2_rn(q, g.t, bcast2(1.136108041e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(-1.978190541e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(2.760109305e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(-3.585188985e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(4.807103872e-01f));
+    q = __ffma2_rn(q, g.t, bcast2(-7.213414311e-01f));
     q = __ffma2_rn(q, g.t, bcast2(1.442695022e+00f));
     q = __ffma2_rn(q, g.t, make_float2(fmaxf(g.zl.x, 0.f), fmaxf(g.zl.y, 0.f)));
     g.y = __fmul2_rn(ch.A, q);
@@ -285,12 +285,12 @@ struct alignas(128) TileSmem {
 
 // The factor 2^y, y <= 0, coded for carry(): for y > -0.5, W = expm1(y ln 2) with its sign
 // bit set (y times the degree-4 polynomial nearest to (2^y - 1) / y on [-0.5, 0], relative error
-// 1.3e-8; a weighted least-squares fit), else 2^y itself, its sign bit clear.
+// 1.6e-8; fitted as above), else 2^y itself, its sign bit clear.
 __device__ __forceinline__ float code_factor(float y) {
-    float q = 1.154452213e-03f;
-    q = fmaf(q, y, 9.541281499e-03f);
-    q = fmaf(q, y, 5.549040809e-02f);
-    q = fmaf(q, y, 2.402256429e-01f);
+    float q = 1.159412786e-03f;
+    q = fmaf(q, y, 9.546945803e-03f);
+    q = fmaf(q, y, 5.549255386e-02f);
+    q = fmaf(q, y, 2.402259409e-01f);
     q = fmaf(q, y, 6.931471825e-01f);
     return y > -0.5f ? __int_as_float(__float_as_int(q * y) | 0x80000000) : decay(y);
 }

@@ -3,6 +3,8 @@
 import os
 import re
 
+import numpy as np
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 with open(os.path.join(ROOT, "gated_delta_rule_145_b200", "csrc", "linear_recurrence.cu")) as f:
     SOURCE = f.read()
@@ -26,3 +28,20 @@ def test_what_peers_stored_is_waited_for_at_cluster_scope():
     for name in ("peers_wait", "peers_wait_slow"):
         assert "peers_test(" in body(name) and "mbar_" not in body(name)
     assert "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64" in body("peers_test")
+
+
+def horner(name):
+    """The fp32 coefficients of the polynomial in `name`, highest power first, in 64 bits."""
+    return [float(np.float32(c)) for c in re.findall(r"([-+]?\d\.\d{9}e[-+]\d\d)f", body(name))]
+
+
+def test_the_polynomials_are_as_exact_as_their_comments_say():
+    """log2(e) log1p(t) = t Q(t) on [0, 1], 2^y - 1 = y W(y) on [-1/2, 0]: the coefficients as rounded,
+    evaluated in 64 bits (Horner of at most nine terms: 1e-15)"""
+    t = np.linspace(0, 1, 20001)[1:]
+    Q, W = horner("decay_gate"), horner("code_factor")
+    assert len(Q) == 9 and len(W) == 5
+    assert "(3.2e-8;" in SOURCE and "1.6e-8; fitted as above" in SOURCE
+    assert np.abs(np.polyval(Q, t) * t / (np.log1p(t) / np.log(2.0)) - 1).max() <= 3.2e-8
+    y = -0.5 * t
+    assert np.abs(np.polyval(W, y) * y / np.expm1(y * np.log(2.0)) - 1).max() <= 1.6e-8
