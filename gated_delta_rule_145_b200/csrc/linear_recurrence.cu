@@ -25,6 +25,7 @@ namespace {
 __device__ int g_recurrence_status;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
 
 __device__ __forceinline__ float ex2f(float x) {
     float y;
@@ -36,14 +37,20 @@ __device__ __forceinline__ float rcpf(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// The decay 2^y of a token or of several: never zero, so that an infinite state stays infinite in
-// every form and not only where no product of decays underflows (0 inf).  Times a finite state
-// the floor, the smallest float, is nothing.  A NaN stays one (fmaxf would drop it).
+// The larger and the smaller of two; a NaN stays one (fmaxf and fminf would drop it).
 __device__ __forceinline__ float max_nan(float a, float b) {
     float m;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
     return m;
 }
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float m;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+// The decay 2^y of a token or of several: never zero, so that an infinite state stays infinite in
+// every form and not only where no product of decays underflows (0 inf).  Times a finite state
+// the floor, the smallest float, is nothing.
 __device__ __forceinline__ float decay(float y) { return max_nan(ex2f(y), 1.4e-45f); }
 __device__ __forceinline__ float2 decay(float2 y) { return make_float2(decay(y.x), decay(y.y)); }
 __device__ __forceinline__ float2 ex2f2(float2 v) { return make_float2(ex2f(v.x), ex2f(v.y)); }
@@ -99,10 +106,26 @@ __device__ __forceinline__ Gate decay_gate(float2 a, const Channels& ch) {
     return g;
 }
 
+// e^{-v}.  The product v log2(e) is rounded, which the power turns into a relative error of |v| 2^-24,
+// 2e-6 for far gates: nothing beside the 2^-9 that a bf16 b carries, so bf16 calls take it as it
+// is.  fp32 ones give the power what the product lost (kLog2eLow: what kLog2e lost), of a v that is
+// bounded where the power is 0 or infinite anyway, and stay near an ulp.
+template <typename Tin>
+__device__ __forceinline__ float2 neg_exp(float2 v) {
+    if constexpr (sizeof(Tin) == 2) {
+        return ex2f2(__fmul2_rn(v, bcast2(-kLog2e)));
+    } else {
+        v = make_float2(max_nan(min_nan(v.x, 1000.f), -1000.f), max_nan(min_nan(v.y, 1000.f), -1000.f));
+        const float2 p = __fmul2_rn(v, bcast2(-kLog2e));
+        float2 low = __ffma2_rn(v, bcast2(-kLog2e), make_float2(-p.x, -p.y));
+        low = __ffma2_rn(v, bcast2(-kLog2eLow), low);
+        return __fmul2_rn(ex2f2(p), __ffma2_rn(low, bcast2(kLn2), bcast2(1.f)));
+    }
+}
 // x sigmoid(b)
+template <typename Tin>
 __device__ __forceinline__ float2 gated_input(float2 x, float2 b) {
-    const float2 e = ex2f2(__fmul2_rn(b, bcast2(-kLog2e)));
-    return __fmul2_rn(x, rcpf2(__fadd2_rn(e, bcast2(1.f))));
+    return __fmul2_rn(x, rcpf2(__fadd2_rn(neg_exp<Tin>(b), bcast2(1.f))));
 }
 
 __device__ __forceinline__ Channels load_channels(const float* A_log, const float* dt_bias,
@@ -142,11 +165,11 @@ __device__ __forceinline__ float2 decay_factors(float2 a, float2 prev, const Cha
     return g.y;
 }
 // Those in dx and db.
+template <typename Tin>
 __device__ __forceinline__ void input_factors(float2 x, float2 b, float2& fx, float2& fb) {
-    const float2 bl = __fmul2_rn(b, bcast2(kLog2e));
-    const float2 tb = ex2f2(make_float2(-fabsf(bl.x), -fabsf(bl.y)));
+    const float2 tb = neg_exp<Tin>(make_float2(fabsf(b.x), fabsf(b.y)));
     const float2 rb = rcpf2(__fadd2_rn(tb, bcast2(1.f))), tr = __fmul2_rn(tb, rb);
-    fx = make_float2(bl.x >= 0.f ? rb.x : tr.x, bl.y >= 0.f ? rb.y : tr.y);
+    fx = make_float2(b.x >= 0.f ? rb.x : tr.x, b.y >= 0.f ? rb.y : tr.y);
     fb = __fmul2_rn(x, __fmul2_rn(rb, tr));
 }
 template <typename Tin>
@@ -187,7 +210,7 @@ recurrence_seq_kernel(RecurrenceParams p) {
             const float2 xv = load_pair(x + t * p.ld), av = load_pair(a + t * p.ld),
                          bv = load_pair(b + t * p.ld);
             const Gate g = decay_gate(av, ch);
-            h = __ffma2_rn(decay(g.y), h, gated_input(xv, bv));
+            h = __ffma2_rn(decay(g.y), h, gated_input<Tin>(xv, bv));
             store_pair(p.out + t * p.C + c, h);
         }
         if (p.final_state) *reinterpret_cast<float2*>(p.final_state + at) = h;
@@ -222,7 +245,7 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
             D = __fadd2_rn(load_pair(r.grad_out + t * p.C + c), D);
             float2 lam, fa, fA, fx, fb;
             decay_factors(load_pair(a + t * p.ld), prev, ch, lam, fa, fA);
-            input_factors(load_pair(x + t * p.ld), load_pair(b + t * p.ld), fx, fb);
+            input_factors<Tin>(load_pair(x + t * p.ld), load_pair(b + t * p.ld), fx, fb);
             store_grads(fx, fb, fa, fA, D, dx + t * r.ld_grad, da + t * r.ld_grad, db + t * r.ld_grad,
                         acc_A, acc_bias);
             D = __fmul2_rn(lam, D);
@@ -567,6 +590,7 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
     static_assert(sizeof(Smem) <= kSmemPerSm / Blocks - 1024, "the SM's CTAs have to fit");
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
     constexpr bool Cluster = Smem::Cluster;
+    using Tin = typename Smem::Tin;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     if (threadIdx.x == 0) init_cta(sm, sched, Cluster ? (int)cluster_rank() : 0);
@@ -629,7 +653,7 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
                 const float2 bv = smem_pair(row + (2 * kRows + i) * kStrip);
                 const float2 y = decay_gate(av, ch).y;
                 k.lam[i] = decay(y);
-                k.u[i] = gated_input(xv, bv);
+                k.u[i] = gated_input<Tin>(xv, bv);
                 G = __fadd2_rn(G, y);
                 H = __ffma2_rn(k.lam[i], H, k.u[i]);
             };
@@ -828,7 +852,7 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
                     const float2 D = __fadd2_rn(smem_pair(dout - i * kStrip), E);
                     const long long o = i * r.ld_grad;
                     float2 fx, fb;
-                    input_factors(smem_pair(x - i * kStrip), smem_pair(x + (2 * kRows - i) * kStrip), fx, fb);
+                    input_factors<Tin>(smem_pair(x - i * kStrip), smem_pair(x + (2 * kRows - i) * kStrip), fx, fb);
                     store_grads(fx, fb, k.a[i], k.A[i], D, dx - o, da - o, db - o, acc_A, acc_bias);
                     E = __fmul2_rn(k.lam[i], D);
                 };

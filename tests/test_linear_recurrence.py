@@ -294,6 +294,26 @@ def test_extreme_gates(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("lo,hi", [(-80, -30), (-30, -4), (-4, 4), (4, 80)])
+@pytest.mark.parametrize("B,T,C", [(3, 7, 136), (2, 700, 64), (5, 1300, 4104)])
+def test_fp32_input_gates_to_fp32_rounding(B, T, C, lo, hi):
+    """with the past forgotten at every token and x and grad_out of one, h is sigmoid(b), dx too,
+    db sigmoid(b) sigmoid(-b).  Each is at most an exponential (2 ulps, 2^-22, and three roundings
+    of its correction), a sum, two reciprocals (an ulp, 2^-23, each) and three products: below
+    14 x 2^-24 < 2^-20 of its value"""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    b = torch.rand(B, T, C, device="cuda", generator=g) * (hi - lo) + lo
+    one, p = torch.ones_like(b), torch.zeros(C, device="cuda")
+    a = torch.full_like(b, 1e30)
+    h, _ = gdr.linear_recurrence(one, a, b, p, p)
+    dx, _, db, *_ = gdr.linear_recurrence_backward(one, a, b, p, p, h, one)
+    s = torch.sigmoid(b.double())
+    for name, got, ref in (("h", h, s), ("dx", dx, s), ("db", db, s * torch.sigmoid(-b.double()))):
+        off = float(((got.double() - ref).abs() / (2.0 ** -20 * ref + 1e-36)).max())
+        assert off <= 1, f"{name}: {off:.2f} x"
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,C", [(2, 5, 64), (2, 300, 64), (1, 5000, 192), (5, 1300, 4104)])
 def test_gates_masked_with_the_highest_and_lowest_values(B, T, C, dtype):
