@@ -35,6 +35,7 @@ int check_common(const FwdParams& p, int elem_bytes) {
 
 int to_status(cudaError_t e) {
     if (e == cudaSuccess) return GDR_OK;
+    cudaGetLastError();  // it is reported here: left behind, the next call's launch would report it again
     if (e == cudaErrorNotSupported) return GDR_ERR_UNSUPPORTED;
     if (e == cudaErrorMemoryAllocation) return GDR_ERR_OOM;
     return GDR_ERR_CUDA;
@@ -626,15 +627,19 @@ int gdr_linear_recurrence_backward_f32(const float* x, const float* a, const flo
 }
 
 int gdr_device_status(gdr_stream_t stream) {
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return GDR_ERR_CUDA;
-    const int v = gdr::read_and_clear_tc_status();
-    if (v < 0) return GDR_ERR_CUDA;
+    const cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+    const int v = e == cudaSuccess ? gdr::read_and_clear_tc_status() : -1;
+    if (v < 0) {
+        cudaGetLastError();
+        return GDR_ERR_CUDA;
+    }
     return v ? GDR_ERR_TIMEOUT : GDR_OK;
 }
 
 int gdr_selftest_bounded_wait(gdr_stream_t stream) {
-    return gdr::launch_bounded_wait_selftest((cudaStream_t)stream) == cudaSuccess ? GDR_OK
-                                                                                 : GDR_ERR_CUDA;
+    return to_status(gdr::launch_bounded_wait_selftest((cudaStream_t)stream)) == GDR_OK
+               ? GDR_OK
+               : GDR_ERR_CUDA;
 }
 
 void gdr_release_workspace(void) { gdr::workspace_release(); }
