@@ -541,8 +541,9 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
 #pragma unroll
         for (int r = 0; r < kRingRows; ++r) {
             if (r < n_rows) {
-                // xh = x rstd - mean rstd: its rounding is of the size of the mean's own
-                const float2 r2 = bcast2(rs[r]), shift = bcast2(mu[r] * rs[r]);
+                // xh = (x - mean) rstd, as in the forward pass: x rstd - mean rstd would leave the
+                // rounding of mean rstd, which a row of one value (xh = 0) has nowhere else
+                const float2 r2 = bcast2(rs[r]), shift = bcast2(mu[r]);
                 float2 m1 = bcast2(0.f), m2 = m1;
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
@@ -556,7 +557,7 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
                         b.get(g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 xh = __ffma2_rn(xv[e], r2, shift);
+                            const float2 xh = __fmul2_rn(__fadd2_rn(xv[e], shift), r2);
                             dw[n][e] = __ffma2_rn(g[e], xh, dw[n][e]);
                             db[n][e] = __fadd2_rn(db[n][e], g[e]);
                             const float2 q = __fmul2_rn(g[e], w[n][e]);
@@ -576,12 +577,12 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
         Tin* dxp = dx + ring.row0(k) * d;
 #pragma unroll
         for (int r = 0; r < kRingRows; ++r) {
-            // dx = rstd (q - m1 - xh m2) as rstd (g w + x k1 + k0); rstd^2 could overflow
+            // dx = rstd (q - m1 - xh m2) as rstd (g w + (x - mean) k1 + n1); rstd^2 could overflow
             const float n1 = __shfl_sync(0xffffffffu, t, 2 * r);
             const float n2 = __shfl_sync(0xffffffffu, t, 2 * r + 1);
             if (r < n_rows) {
-                const float2 r2 = bcast2(rs[r]), k1 = bcast2(n2 * rs[r]);
-                const float2 k0 = bcast2(fmaf(mu[r] * rs[r], n2, n1));
+                const float2 r2 = bcast2(rs[r]), k1 = bcast2(n2 * rs[r]), k0 = bcast2(n1);
+                const float2 shift = bcast2(mu[r]);
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     const int c = kVec * (tid + n * (int)blockDim.x);
@@ -594,7 +595,7 @@ layer_norm_backward_kernel(const Tin* __restrict__ x, const float* __restrict__ 
                         b.get(g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            g[e] = __fmul2_rn(__ffma2_rn(g[e], w[n][e], __ffma2_rn(xv[e], k1, k0)), r2);
+                            g[e] = __fmul2_rn(__ffma2_rn(g[e], w[n][e], __ffma2_rn(__fadd2_rn(xv[e], shift), k1, k0)), r2);
                         store_vec(dxp + (long long)r * d + c, g);
                     }
                 }

@@ -129,6 +129,27 @@ def test_a_gradient_of_nan_stays_in_its_row(d):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 264, 1160, 4096, 6144, 8200, 20480])
+def test_rows_of_one_value_add_nothing_to_the_weight_gradient(d, dtype):
+    """x - mean is 0 exactly, so xh is, whatever rstd; grad_x = rstd (q - mean(q)) is left, to the
+    tolerance of the test above without X (xh's magnitude)"""
+    x, dy, w, _ = make(300, d, dtype, 10)
+    x[:] = np.linspace(-3, 40, 300, dtype=np.float32)[:, None]
+    x = synth.round_to_bf16(x)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    xd, wd = dev(x, dt), dev(w)
+    _, mean, rstd = gdr.layer_norm(xd, wd)
+    dx, dw, db = gdr.layer_norm_backward(xd, wd, mean, rstd, dev(dy, dt))
+    torch.cuda.synchronize()
+    assert torch.equal(mean, xd[:, 0].float()) and (dw == 0).all()
+    q = dy.astype(np.float64) * w
+    m = np.abs(q).mean(1, keepdims=True)
+    ref = (q - q.mean(1, keepdims=True)) * 1e-5 ** -0.5
+    within(dx, ref, 4 * E * (np.abs(q) + m) * 1e-5 ** -0.5 + HALF[dtype] * np.abs(ref), "dx")
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 1160])
 def test_a_row_of_nan_stays_alone(d):
     x, dy, w, b = make(40, d, "f32", 6)
