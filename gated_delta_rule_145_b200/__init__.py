@@ -22,7 +22,7 @@ __all__ = [
     "gdr_prefill_recurrent", "gdr_prefill_recurrent_f32", "gdr_decode_step",
     "gdr_decode_step_f32", "gdr_status_string", "gdr_device_status", "prefill", "decode_step", "LIB_PATH",
     "gdr_linear_recurrence", "gdr_linear_recurrence_f32", "gdr_linear_recurrence_backward",
-    "gdr_linear_recurrence_backward_f32", "gdr_layer_norm", "gdr_layer_norm_f32",
+    "gdr_linear_recurrence_backward_f32", "gdr_zero_outer_rows", "gdr_layer_norm", "gdr_layer_norm_f32",
     "gdr_layer_norm_backward", "gdr_layer_norm_backward_f32", "gdr_short_conv_silu_backward",
     "gdr_gated_rmsnorm_backward", "gdr_gated_rmsnorm_backward_f32", "linear_recurrence",
     "linear_recurrence_backward", "layer_norm", "layer_norm_backward",
@@ -82,6 +82,7 @@ _SIGS = {
     "gdr_linear_recurrence_f32": [_P] * 9 + [_I] * 3 + [_L, _P],
     "gdr_linear_recurrence_backward": [_P] * 16 + [_I] * 3 + [_L] * 2 + [_P],
     "gdr_linear_recurrence_backward_f32": [_P] * 16 + [_I] * 3 + [_L] * 2 + [_P],
+    "gdr_zero_outer_rows": [_P] * 4 + [_I] * 2 + [_L] * 2 + [_P],
     "gdr_prefill_segment_maps": [_P] * 10 + [_I] * 7 + [_P],
     "gdr_segment_combine": [_P] * 5 + [_I] * 4 + [_P],
     "gdr_prefill_chunked_cp": [_P] * 10 + [_I] * 7 + [_P],
@@ -146,13 +147,14 @@ def _stream(s):
 _INT_MAX = 0x7fffffff
 
 
-def _call(name, ptrs, ints, stream, check):
+def _call(name, ptrs, ints, stream, check, longs=()):
     fn = getattr(_lib or library(), name)
-    if max(ints) > _INT_MAX or min(ints) < -_INT_MAX:  # ctypes would drop the upper bits
+    if (max(ints) > _INT_MAX or min(ints) < -_INT_MAX or  # ctypes would drop the upper bits
+            any(not -1 << 62 < n < 1 << 62 for n in longs)):
         status = GDR_ERR_SHAPE
     else:
         status = fn(*[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs],
-                    *map(int, ints), _stream(stream))
+                    *map(int, ints), *map(int, longs), _stream(stream))
     if check and status != GDR_OK:
         raise GdrError(name, status)
     return status
@@ -402,6 +404,12 @@ def gdr_linear_recurrence_backward_f32(x, a, b, A_log, dt_bias, init_state, out,
                  (B, T, C, ld, ld_grad), stream, check)
 
 
+def gdr_zero_outer_rows(x, y, z, cu_seqlens, B, T, row_bytes, pitch_bytes, stream=None, check=True):
+    """Zeros in the rows of packed tensors that no sequence holds (see include/gdr.h)."""
+    return _call("gdr_zero_outer_rows", (x, y, z, cu_seqlens), (B, T), stream, check,
+                 (row_bytes, pitch_bytes))
+
+
 def prefill(q, k, v, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None, chunk=32,
             form="chunked", out=None, final_state=None, stream=None, erase=True):
     """Prefill over q, k [B, T, Hk, dk], v [B, T, Hv, dv], a, b [B, T, Hv] (bf16 or fp32).
@@ -566,20 +574,24 @@ def linear_recurrence(x, a, b, A_log, dt_bias, init_state=None, cu_seqlens=None,
     decay g = -exp(A_log) softplus(a + dt_bias): x, a, b [B, T, C] bf16 or fp32, dense or all
     three slices of the last dimension of a dense tensor; A_log, dt_bias [C]; ``init_state``
     [Nseq, C] (zeros if None).  With ``cu_seqlens`` (int32, device, [Nseq + 1]) the tokens are
-    packed along T (B must be 1).  T = 1 is a decode step; ``final_state`` may be
-    ``init_state``.  Returns (out [B, T, C] fp32, final_state [Nseq, C] fp32)."""
+    packed along T (B must be 1); rows outside them are zero in an ``out`` that the call
+    allocates and stay as they were in one that is given.  T = 1 is a decode step;
+    ``final_state`` may be ``init_state``.  Returns (out [B, T, C] fp32, final_state [Nseq, C] fp32)."""
     import torch
 
     dtype, nseq, T, C, ld = _recurrence_args(x, a, b, A_log, dt_bias, init_state, cu_seqlens)
     f32 = torch.float32
     _check(x, ("out", out, f32, x.shape, True),
            ("final_state", final_state, f32, (nseq, C), True))
-    if out is None:
+    fresh = out is None
+    if fresh:
         out, = _empty(x, stream, (x.shape, f32))
     if final_state is None:
         final_state, = _empty(x, stream, ((nseq, C), f32))
     _launch("gdr_linear_recurrence_f32" if dtype is f32 else "gdr_linear_recurrence", x, stream,
             (x, a, b, A_log, dt_bias, init_state, out, final_state, cu_seqlens), (nseq, T, C, ld))
+    if fresh and cu_seqlens is not None:
+        _launch("gdr_zero_outer_rows", x, stream, (out, None, None, cu_seqlens), (nseq, T, 4 * C, 4 * C))
     return out, final_state
 
 
@@ -589,7 +601,8 @@ def linear_recurrence_backward(x, a, b, A_log, dt_bias, out, grad_out, grad_fina
     """The gradient of ``linear_recurrence``: its arguments and its ``out``, with grad_out
     [B, T, C] fp32 and ``grad_final_state`` [Nseq, C] fp32 (zeros if None).  ``grad_x``,
     ``grad_a``, ``grad_b`` may be given, all three, in one layout as x, a, b may have (for
-    example slices of one projection's gradient).  Returns (grad_x, grad_a, grad_b,
+    example slices of one projection's gradient); their rows outside packed sequences stay as
+    they were, and are zero where the call allocates them.  Returns (grad_x, grad_a, grad_b,
     grad_A_log [C], grad_dt_bias [C], grad_init_state [Nseq, C])."""
     import torch
 
@@ -598,6 +611,7 @@ def linear_recurrence_backward(x, a, b, A_log, dt_bias, out, grad_out, grad_fina
     grads = (grad_x, grad_a, grad_b)
     _check(x, ("out", out, f32, x.shape, True), ("grad_out", grad_out, f32, x.shape, True),
            ("grad_final_state", grad_final_state, f32, (nseq, C), True))
+    fresh = grad_x is None
     if grad_x is None or grad_a is None or grad_b is None:
         if any(g is not None for g in grads):
             raise ValueError("give grad_x, grad_a and grad_b together, or none of them")
@@ -612,6 +626,9 @@ def linear_recurrence_backward(x, a, b, A_log, dt_bias, out, grad_out, grad_fina
             "gdr_linear_recurrence_backward", x, stream,
             (x, a, b, A_log, dt_bias, init_state, out, grad_out, grad_final_state, *grads,
              grad_A_log, grad_dt_bias, grad_init, cu_seqlens), (nseq, T, C, ld, ld_grad))
+    if fresh and cu_seqlens is not None:
+        row = C * (4 if dtype is f32 else 2)
+        _launch("gdr_zero_outer_rows", x, stream, (*grads, cu_seqlens), (nseq, T, row, row))
     return (*grads, grad_A_log, grad_dt_bias, grad_init)
 
 

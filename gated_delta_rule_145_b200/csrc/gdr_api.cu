@@ -626,6 +626,18 @@ int gdr_linear_recurrence_backward_f32(const float* x, const float* a, const flo
                                (cudaStream_t)stream);
 }
 
+int gdr_zero_outer_rows(void* x, void* y, void* z, const int32_t* cu_seqlens, int B, int T,
+                        long long row_bytes, long long pitch_bytes, gdr_stream_t stream) {
+    if (!cu_seqlens || (T > 0 && !x && !y && !z)) return GDR_ERR_NULL;
+    if (B < 1 || T < 0 || row_bytes < 16 || row_bytes % 16 != 0 || pitch_bytes < row_bytes ||
+        pitch_bytes % 16 != 0 || pitch_bytes > 0x1ffffffffLL)
+        return GDR_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(z, 16) || !aligned(cu_seqlens, 4))
+        return GDR_ERR_ALIGN;
+    return to_status(gdr::launch_zero_outer_rows(x, y, z, cu_seqlens, B, T, row_bytes, pitch_bytes,
+                                                 (cudaStream_t)stream));
+}
+
 int gdr_device_status(gdr_stream_t stream) {
     const cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
     const int v = e == cudaSuccess ? gdr::read_and_clear_tc_status() : -1;

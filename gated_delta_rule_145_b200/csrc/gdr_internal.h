@@ -96,6 +96,10 @@ struct RecurrenceGrads {
 cudaError_t launch_recurrence(const RecurrenceParams& p, cudaStream_t stream);
 cudaError_t launch_recurrence_backward(const RecurrenceParams& p, const RecurrenceGrads& r,
                                        cudaStream_t stream);
+// Zeros in the rows of up to three tensors (nullptr: none) outside [cu_seqlens[0], cu_seqlens[B]) of T
+// rows, 16-byte aligned, row_bytes and pitch_bytes multiples of 16; outer_rows.cu.
+cudaError_t launch_zero_outer_rows(void* x, void* y, void* z, const int32_t* cu_seqlens, int B, int T,
+                                   long long row_bytes, long long pitch_bytes, cudaStream_t stream);
 // Reads and clears the tiled recurrence's timeout record (nonzero if set, -1 on error).
 int read_and_clear_recurrence_status();
 

@@ -475,6 +475,16 @@ GDR_API int gdr_linear_recurrence_backward_f32(
     int B, int T, int C, long long ld, long long ld_grad, gdr_stream_t stream);
 
 /*
+ * Zeros in the rows of packed tensors that no sequence holds: rows outside [cu_seqlens[0],
+ * cu_seqlens[B]) of the T rows of up to three tensors (NULL: none) of one layout, rows of row_bytes,
+ * pitch_bytes apart (multiples of 16; a pitch below 2^33), 16-byte aligned.  For outputs of
+ * gdr_linear_recurrence and its backward call in memory that was only allocated: these calls
+ * leave such rows as they were.
+ */
+GDR_API int gdr_zero_outer_rows(void* x, void* y, void* z, const int32_t* cu_seqlens, int B, int T,
+                                long long row_bytes, long long pitch_bytes, gdr_stream_t stream);
+
+/*
  * Device-side status of the kernels enqueued so far.  Synchronises `stream`, then returns
  * GDR_ERR_TIMEOUT if any tensor-core prefill kernel (or the TMA-fed convolution that
  * gdr_short_conv_silu runs for T >= 256, a tiled kernel of gdr_linear_recurrence or its backward

@@ -281,6 +281,38 @@ def test_rows_outside_the_sequences_stay_and_are_not_read(lens, lead):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,lead,tail", [([100, 30, 200], 0, 37), ([70, 5], 12, 0), ([0, 0], 3, 9),
+                                            ([900, 700], 40, 2000)])
+def test_rows_outside_the_sequences_are_zero_in_tensors_that_the_call_allocates(lens, lead, tail,
+                                                                                dtype):
+    """whatever the memory held before: a padded row is then nothing in the sums that follow"""
+    C, T = 136, lead + sum(lens) + tail
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    x, a, b = (r(1, T, C).to(dtype) for _ in range(3))
+    A, d, init, gf, go = r(C), r(C), r(len(lens), C), r(len(lens), C), r(1, T, C)
+    cu = dev((lead + np.concatenate([[0], np.cumsum(lens)])).astype(np.int32))
+    kept = torch.full((1, T, C), 7.0, device="cuda")
+    want = [torch.full((1, T, C), 7.0, device="cuda", dtype=dtype) for _ in range(3)]
+    gdr.linear_recurrence(x, a, b, A, d, init, cu, out=kept)
+    gdr.linear_recurrence_backward(x, a, b, A, d, kept, go, gf, init, cu, *want)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    waste = [torch.full((1, T, C), float("nan"), device="cuda", dtype=t)
+             for t in (torch.float32, dtype) for _ in range(6)]
+    del waste
+    out, _ = gdr.linear_recurrence(x, a, b, A, d, init, cu)
+    grads = gdr.linear_recurrence_backward(x, a, b, A, d, out, go, gf, init, cu)[:3]
+    torch.cuda.synchronize()
+    inner = torch.zeros(T, device="cuda", dtype=torch.bool)
+    inner[lead:lead + sum(lens)] = True
+    for v, w in zip((out, *grads), (kept, *want)):
+        assert (v[:, ~inner] == 0).all() and (w[:, ~inner] == 7).all()
+        assert torch.equal(v[:, inner], w[:, inner])
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_extreme_gates(dtype):
     """decays that underflow in one token, decays of exactly 1, closed and open input gates"""
@@ -555,6 +587,22 @@ def test_refusals(call, suffix):
             assert call(name, **{p: A + 8}) == gdr.GDR_ERR_ALIGN, p
         assert call(name, ld_grad=56) == gdr.GDR_ERR_SHAPE
         assert call(name, ld_grad=68) == gdr.GDR_ERR_SHAPE
+
+
+def test_refusals_of_zero_outer_rows():
+    def call(**kw):
+        args = dict(x=A, y=A, z=None, cu_seqlens=A, B=2, T=16, row_bytes=64, pitch_bytes=64)
+        args.update(kw)
+        return gdr.gdr_zero_outer_rows(**args, stream=0, check=False)
+
+    assert call(cu_seqlens=None) == gdr.GDR_ERR_NULL == call(x=None, y=None)
+    for kw in (dict(B=0), dict(T=-1), dict(row_bytes=0), dict(row_bytes=24), dict(pitch_bytes=48),
+               dict(pitch_bytes=72), dict(pitch_bytes=1 << 33), dict(T=2 ** 32 + 16),
+               dict(row_bytes=2 ** 64 + 64)):
+        assert call(**kw) == gdr.GDR_ERR_SHAPE, kw
+    for p in ("x", "y", "z"):
+        assert call(**{p: A + 8}) == gdr.GDR_ERR_ALIGN, p
+    assert call(cu_seqlens=A + 2) == gdr.GDR_ERR_ALIGN
 
 
 @pytest.mark.parametrize("kw", [dict(T=2 ** 32 + 16), dict(C=2 ** 32 + 64), dict(B=2 ** 32 + 1),
