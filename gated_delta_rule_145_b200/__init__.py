@@ -9,7 +9,10 @@ tensors, and fails loudly otherwise.
 The functions named ``gdr_*`` mirror the C ABI in ``include/gdr.h`` one to one
 (pointer arguments take torch tensors, None or raw integer addresses).  ``prefill``,
 ``decode_step``, ``linear_recurrence``, ``layer_norm`` and the ``*_backward`` functions are
-conveniences that check tensors and allocate the outputs.
+conveniences that check tensors and allocate the outputs.  None of them is recorded by autograd: the
+trainable ones (``linear_recurrence``, ``layer_norm`` and the ``*_backward`` functions) refuse tensors that
+require gradients where these are recorded, instead of losing them; call them under
+``torch.no_grad()`` or from a ``torch.autograd.Function``.
 """
 
 from __future__ import annotations
@@ -473,11 +476,12 @@ def decode_step(q, k, v, a, b, A_log, dt_bias, state, out=None, stream=None, era
 
 def _check(first, *specs):
     """Every (name, tensor, dtype, shape, dense) of `specs` is a CUDA tensor on `first`'s device of
-    this type and shape, contiguous if `dense`; None passes."""
+    this type and shape, contiguous if `dense`, and autograd does not expect its gradient; None
+    passes."""
     index = first.get_device()  # -1: none; an integer, compared in half of a device's time
     for name, t, dtype, shape, dense in specs:
         if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and
-                         (not dense or t.is_contiguous())):
+                         (not dense or t.is_contiguous()) and not t.requires_grad):
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
@@ -487,7 +491,14 @@ def _check(first, *specs):
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.device != first.device:
             raise ValueError(f"{name} is on {t.device}, not on {first.device}")
-        raise ValueError(f"{name} must be contiguous")
+        if dense and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        import torch
+
+        if torch.is_grad_enabled():  # autograd would take the result for a constant
+            raise ValueError(f"{name} requires a gradient, and this call is not recorded by autograd: "
+                             "call it under torch.no_grad() or from a torch.autograd.Function (whose "
+                             "backward calls the *_backward functions)")
 
 
 def _token_stride(tensors, B, T, C):
