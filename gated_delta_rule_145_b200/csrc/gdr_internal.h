@@ -85,6 +85,7 @@ struct RecurrenceParams {
     int nseq, T, C;
     long long ld;
     InType in;
+    int limit = 0;  // packed, 0: none: longer sequences are not the sequential kernel's
 };
 struct RecurrenceGrads {
     const float *grad_out, *grad_final;  // [tokens, C]; [nseq, C] or nullptr (zeros)

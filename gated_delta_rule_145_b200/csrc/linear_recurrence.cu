@@ -202,6 +202,7 @@ recurrence_seq_kernel(RecurrenceParams p) {
     for (int s = blockIdx.y; s < p.nseq; s += gridDim.y) {
         long long t0, t1;
         seq_bounds(p.cu_seqlens, s, p.T, t0, t1);
+        if (p.limit && t1 - t0 > p.limit) continue;
         const size_t at = (size_t)s * p.C + c;
         float2 h = p.init_state ? *reinterpret_cast<const float2*>(p.init_state + at)
                                 : make_float2(0.f, 0.f);
@@ -217,9 +218,11 @@ recurrence_seq_kernel(RecurrenceParams p) {
     }
 }
 
-// part [gridDim.y][2 C]: this row of CTAs' sums for A_log, then for dt_bias.
+// part [gridDim.y][2 C]: this row of CTAs' sums for A_log, then for dt_bias.  Twelve blocks per SM: left
+// alone the compiler takes 118 registers for loads ahead, and 64 sequences of 32 tokens x 6144
+// channels take 113 us instead of 73.
 template <typename Tin>
-__global__ void __launch_bounds__(kSeqThreads)
+__global__ void __launch_bounds__(kSeqThreads, 12)
 recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* part) {
     const int c = 2 * (blockIdx.x * kSeqThreads + threadIdx.x);
     if (c >= p.C) return;
@@ -234,6 +237,8 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
     for (int s = blockIdx.y; s < p.nseq; s += gridDim.y) {
         long long t0, t1;
         seq_bounds(p.cu_seqlens, s, p.T, t0, t1);
+        const bool another = p.limit && t1 - t0 > p.limit;
+        if (another) t0 = t1;
         const size_t at = (size_t)s * p.C + c;
         float2 D = r.grad_final ? *reinterpret_cast<const float2*>(r.grad_final + at)
                                 : make_float2(0.f, 0.f);
@@ -250,7 +255,7 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
                         acc_A, acc_bias);
             D = __fmul2_rn(lam, D);
         }
-        if (r.grad_init) *reinterpret_cast<float2*>(r.grad_init + at) = D;
+        if (r.grad_init && !another) *reinterpret_cast<float2*>(r.grad_init + at) = D;
     }
     float* row = part + (size_t)blockIdx.y * 2 * p.C;
     *reinterpret_cast<float2*>(row + c) = __fmul2_rn(acc_A, bcast2(kLn2));
@@ -559,20 +564,48 @@ struct Place {
     bool in_c;
 };
 template <bool Cluster>
-__device__ __forceinline__ Place place_of(const RecurrenceParams& p, int unit, int strips, int rows) {
+__device__ __forceinline__ Place place_of(const RecurrenceParams& p, int seq, int strip, int rows) {
     Place w;
     w.warp = threadIdx.x / 32;
     w.lane = threadIdx.x % 32;
     w.K = Cluster ? (int)cluster_size() : 1;
     w.rank = Cluster ? (int)cluster_rank() : 0;
-    w.seq = unit / strips;
-    w.c0 = unit % strips * kStrip;
+    w.seq = seq;
+    w.c0 = strip * kStrip;
     w.c = w.c0 + 2 * w.lane;
     w.in_c = w.c < p.C;  // C is even
     seq_bounds(p.cu_seqlens, w.seq, p.T, w.t0, w.t1);
     w.tiles = (int)((w.t1 - w.t0 + rows - 1) / rows);
     w.steps = (w.tiles + w.K - 1) / w.K;
     return w;
+}
+// The k-th of the packed sequences with more than p.limit tokens (a block of Warps warps; -1: none).
+template <int Warps>
+__device__ __forceinline__ int kth_long(const RecurrenceParams& p, int k) {
+    __shared__ int counts[Warps], found;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (int base = 0; base < p.nseq; base += 32 * Warps) {  // nseq is kMostPicked at most
+        const int s = base + (int)threadIdx.x;
+        bool is = false;
+        if (s < p.nseq) {
+            long long t0, t1;
+            seq_bounds(p.cu_seqlens, s, p.T, t0, t1);
+            is = t1 - t0 > p.limit;
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, is);
+        if (lane == 0) counts[warp] = __popc(mask);
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < Warps; ++w) {
+            before += w < warp ? counts[w] : 0;
+            all += counts[w];
+        }
+        if (is && before + __popc(mask & ((1u << lane) - 1)) == k) found = s;
+        __syncthreads();
+        if (k < all) return found;
+        k -= all;
+    }
+    return -1;
 }
 // One thread: barriers, and the cluster's number where it is drawn.
 template <typename Smem>
@@ -583,7 +616,8 @@ __device__ __forceinline__ void init_cta(Smem& sm, const Schedule& s, int rank) 
     if (Smem::Cluster && s.span && rank == 0) sm.ticket = atomicAdd(s.ticket, 1);
 }
 
-template <typename Smem, int Blocks>
+// Pick (no cluster): CTAs k strips .. (k + 1) strips - 1 take the k-th sequence longer than p.limit.
+template <typename Smem, int Blocks, bool Pick = false>
 __global__ void __launch_bounds__(32 * Smem::WARPS, Blocks)
 recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, int strips,
                        Schedule sched) {
@@ -591,6 +625,12 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
     constexpr int TOK = Smem::TOK, STAGES = Smem::STAGES, kRows = Smem::kRows;
     constexpr bool Cluster = Smem::Cluster;
     using Tin = typename Smem::Tin;
+    int seq = 0;
+    if constexpr (Pick) {
+        static_assert(!Cluster, "a picked sequence is one CTA's per strip");
+        seq = kth_long<Smem::WARPS>(p, blockIdx.x / strips);
+        if (seq < 0) return;
+    }
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     if (threadIdx.x == 0) init_cta(sm, sched, Cluster ? (int)cluster_rank() : 0);
@@ -604,7 +644,8 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
     bool dead = false;
     int issued = 0, taken = 0, turn = 0;  // tiles copied, tiles waited for, steps begun
     for (int unit = parts.last; unit >= parts.first; --unit) {  // without a cluster: once
-        const Place w = place_of<Cluster>(p, Cluster ? unit : (int)blockIdx.x, strips, kRows);
+        const int place = Cluster ? unit : (int)blockIdx.x;
+        const Place w = place_of<Cluster>(p, Pick ? seq : place / strips, place % strips, kRows);
         const Part part = part_of<Cluster>(parts, sched, unit, w.steps);
         Channels ch = {};
         if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
@@ -728,8 +769,8 @@ recurrence_tile_kernel(const __grid_constant__ Maps maps, RecurrenceParams p, in
 // second run, from the slot: three values per token and channel to hold, not five.  h comes by
 // plain loads, one step ahead.
 // partial [rows][2 C]: each CTA's sums for A_log and dt_bias, one row per (sequence, rank), and
-// under a split schedule as many rows again for the units' later parts.
-template <typename Smem, int Blocks>
+// under a split schedule as many rows again for the units' later parts; Pick: one per k.
+template <typename Smem, int Blocks, bool Pick = false>
 __global__ void __launch_bounds__(32 * Smem::WARPS, Blocks)
 recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrenceParams p,
                                 RecurrenceGrads r, float* partial, int strips, Schedule sched) {
@@ -738,6 +779,17 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
     using Tin = typename Smem::Tin;
     static_assert(STAGES > 1, "a slot has to be free for the next tile");
     static_assert(sizeof(Smem) <= kSmemPerSm / Blocks - 1024, "the SM's CTAs have to fit");
+    int seq = 0;
+    if constexpr (Pick) {
+        static_assert(!Cluster, "a picked sequence is one CTA's per strip");
+        seq = kth_long<Smem::WARPS>(p, blockIdx.x / strips);
+        if (seq < 0) {  // its row of sums is added all the same
+            const int c = blockIdx.x % strips * kStrip + (int)threadIdx.x;
+            float* o = partial + (size_t)(blockIdx.x / strips) * 2 * p.C;
+            if (threadIdx.x < kStrip && c < p.C) o[c] = o[p.C + c] = 0.f;
+            return;
+        }
+    }
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     if (threadIdx.x == 0) init_cta(sm, sched, Cluster ? (int)cluster_rank() : 0);
@@ -752,7 +804,8 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
     bool dead = false;
     int issued = 0, taken = 0, turn = 0;  // tiles copied, tiles waited for, steps begun
     for (int unit = parts.last; unit >= parts.first; --unit) {  // without a cluster: once
-        const Place w = place_of<Cluster>(p, Cluster ? unit : (int)blockIdx.x, strips, kRows);
+        const int place = Cluster ? unit : (int)blockIdx.x;
+        const Place w = place_of<Cluster>(p, Pick ? seq : place / strips, place % strips, kRows);
         const Part part = part_of<Cluster>(parts, sched, unit, w.steps);
         Channels ch = {};
         if (w.in_c) ch = load_channels(p.A_log, p.dt_bias, w.c);
@@ -893,7 +946,8 @@ recurrence_tile_backward_kernel(const __grid_constant__ Maps maps, RecurrencePar
             }
             const float2 sum_A = __fmul2_rn(make_float2(s.x, s.y), bcast2(kLn2));
             const float2 sum_bias = make_float2(s.z, s.w);
-            const size_t row = (size_t)w.seq * w.K + w.rank, later = (size_t)p.nseq * w.K;
+            const size_t row = Pick ? (size_t)(blockIdx.x / strips) : (size_t)w.seq * w.K + w.rank;
+            const size_t later = (size_t)p.nseq * w.K;
             auto put = [&](size_t row, float2 a, float2 b) {
                 float* o = partial + row * 2 * p.C + w.c;
                 *reinterpret_cast<float2*>(o) = a;
@@ -1105,11 +1159,30 @@ void offer_single(Plan* plan, const RecurrenceParams& p) {
 // and at least its bytes' time (backward in fp32, eight streams of wide rows, at half of a
 // copy's rate), against a plan.  It is for short sequences (64 sequences of 6144 channels,
 // forward: 31 against 82 us at 32 tokens, 59 against 58 at 64, 116 against 90 at 128; one
-// sequence: 16 against 8 at 16).  Of packed sequences only the mean length is known here; one
-// that holds most of the tokens may cost the sequential form at most 20 times a plan.
+// sequence: 16 against 8 at 16).  Of packed sequences only the mean length is known here: the long
+// ones among them are left to tiles (long_limit); where there are too many to look through, one that
+// holds most of the tokens may cost the sequential form at most 20 times a plan.
+constexpr int kMostPicked = 16384;
 bool sequential(const RecurrenceParams& p, const Plan& plan, double latency_ns, double channel_ns) {
-    if (p.cu_seqlens && p.T * latency_ns > 20 * plan.time) return false;
+    if (p.cu_seqlens && p.nseq > kMostPicked && p.T * latency_ns > 20 * plan.time) return false;
     return mean_length(p) * std::max(latency_ns, channel_ns * p.nseq * p.C) < plan.time;
+}
+
+// Packed sequences that are short in the mean: those of more than `limit` tokens, `groups` at most,
+// go to a tiled kernel behind the sequential one, which finds them on the device.  A long prompt
+// among single tokens ([8192, 255 x 1], C = 6144) takes 157 us forward and 237 backward so, 5.0 and
+// 5.8 ms a token at a time.  The limit is the least whose groups fit four waves of CTAs, which
+// without any such sequence cost 5 us (64 x 32: 45 -> 50 us forward, 68 -> 73 backward), and never so
+// short that the tiles gain nothing; no limit (0) where one sequence of all the tokens would take
+// 0.2 ms at most.
+struct Long {
+    int limit, groups;
+};
+Long long_limit(const RecurrenceParams& p, double latency_ns) {
+    if (!p.cu_seqlens || p.nseq > kMostPicked || p.T * latency_ns <= 2e5) return {0, 0};
+    const int strips = (p.C + kStrip - 1) / kStrip, most = std::max(1, 4 * device_sms() / strips);
+    const int limit = std::max(64, (int)(((long long)p.T + most - 1) / most) - 1);
+    return p.T > limit ? Long{limit, std::min(p.nseq, p.T / (limit + 1))} : Long{0, 0};
 }
 
 // A split schedule's counters and states in `ws`, the counters set to zero.
@@ -1180,17 +1253,41 @@ cudaError_t backward_tiles(const RecurrenceParams& p, const RecurrenceGrads& r, 
     return e != cudaSuccess ? e : f;
 }
 
+// The tiled kernels on the sequences longer than p.limit, with a CTA per SM.
+template <typename Smem>
+cudaError_t forward_long(const RecurrenceParams& p, int groups, cudaStream_t stream) {
+    const int strips = (p.C + kStrip - 1) / kStrip;
+    Maps m;
+    if (!make_maps(m, p, nullptr, Smem::kRows)) return cudaErrorNotSupported;
+    return launch_tiles(recurrence_tile_kernel<Smem, 1, true>, (long long)groups * strips,
+                        32 * Smem::WARPS, 1, sizeof(Smem), stream, m, p, strips, Schedule{});
+}
+template <typename Smem>
+cudaError_t backward_long(const RecurrenceParams& p, const RecurrenceGrads& r, int groups, float* part,
+                          cudaStream_t stream) {
+    const int strips = (p.C + kStrip - 1) / kStrip;
+    Maps m;
+    if (!make_maps(m, p, r.grad_out, Smem::kRows)) return cudaErrorNotSupported;
+    return launch_tiles(recurrence_tile_backward_kernel<Smem, 1, true>, (long long)groups * strips,
+                        32 * Smem::WARPS, 1, sizeof(Smem), stream, m, p, r, part, strips, Schedule{});
+}
+
 template <typename Tin>
-cudaError_t forward(const RecurrenceParams& p, cudaStream_t stream) {
+cudaError_t forward(const RecurrenceParams& call, cudaStream_t stream) {
     using F = typename Forms<Tin>::Fwd;
+    RecurrenceParams p = call;
     static Capacity wide, pair;
     Plan plan = {};
     offer_single<F>(&plan, p);
     if (sequential(p, plan, 620, sizeof(Tin) == 2 ? 0.0023 : 0.0026)) {
         const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads),
                         (unsigned)std::min(p.nseq, 65535));
+        const Long rest = long_limit(p, 620);
+        p.limit = rest.limit;
         recurrence_seq_kernel<Tin><<<grid, kSeqThreads, 0, stream>>>(p);
-        return cudaGetLastError();
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess || !rest.groups ? e
+                                                : forward_long<typename F::One>(p, rest.groups, stream);
     }
     cudaError_t e = offer_clusters<typename F::Wide>(
         &plan, p, kWideForm, recurrence_tile_kernel<typename F::Wide, 1>, wide, F::kWide, kWideRank,
@@ -1210,21 +1307,26 @@ cudaError_t forward(const RecurrenceParams& p, cudaStream_t stream) {
 }
 
 template <typename Tin>
-cudaError_t backward(const RecurrenceParams& p, const RecurrenceGrads& r, cudaStream_t stream) {
+cudaError_t backward(const RecurrenceParams& call, const RecurrenceGrads& r, cudaStream_t stream) {
     using F = typename Forms<Tin>::Bwd;
+    RecurrenceParams p = call;
     static Capacity wide, pair;
     Plan plan = {};
     offer_single<F>(&plan, p);
     if (sequential(p, plan, 750, sizeof(Tin) == 2 ? 0.0038 : 0.0088)) {
-        const int rows = seq_rows(p);
+        const Long rest = long_limit(p, 750);
+        p.limit = rest.limit;
+        const int rows = seq_rows(p), all = rows + rest.groups;
         float* part = nullptr;
-        cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * rows * 2 * p.C, stream);
+        cudaError_t e = workspace_alloc((void**)&part, sizeof(float) * all * 2 * p.C, stream);
         if (e != cudaSuccess) return e;
         const dim3 grid((unsigned)((p.C / 2 + kSeqThreads - 1) / kSeqThreads), (unsigned)rows);
         recurrence_seq_backward_kernel<Tin><<<grid, kSeqThreads, 0, stream>>>(p, r, part);
         e = cudaGetLastError();
+        if (e == cudaSuccess && rest.groups)
+            e = backward_long<typename F::One>(p, r, rest.groups, part + (size_t)rows * 2 * p.C, stream);
         if (e == cudaSuccess)
-            e = launch_column_sum(part, rows, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
+            e = launch_column_sum(part, all, 2 * p.C, r.grad_A_log, p.C, r.grad_dt_bias, stream);
         const cudaError_t f = cudaFreeAsync(part, stream);
         return e != cudaSuccess ? e : f;
     }

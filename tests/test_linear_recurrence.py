@@ -133,6 +133,63 @@ def test_packed(lens, dtype):
     check(m, on_gpu(m)[1], ref, mag, max(lens))
 
 
+def median_ms(call, n=9):
+    times = []
+    for _ in range(n + 2):
+        start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+        start.record()
+        call()
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end))
+    return sorted(times[2:])[n // 2]
+
+
+@gpu
+@pytest.mark.parametrize("longest,others,each", [(2048, 255, 1), (8192, 255, 1), (30000, 999, 6)])
+def test_a_long_prompt_among_short_sequences(longest, others, each):
+    """the mean length says short sequences, for which a token at a time is best: the long one must
+    not be walked that way, which took 6 to 22 times as long as the same tokens in equal sequences"""
+    C, T = 6144, longest + others * each
+    x, a, b = (torch.randn(1, T, C, device="cuda").bfloat16() for _ in range(3))
+    p, go = torch.zeros(C, device="cuda"), torch.randn(1, T, C, device="cuda")
+    equal = [T // (others + 1)] * (others + 1)
+    equal[0] += T - sum(equal)
+    times = []
+    for lens in ([longest] + [each] * others, equal):
+        cu = dev(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+        out, final = gdr.linear_recurrence(x, a, b, p, p, None, cu)
+        times.append((median_ms(lambda: gdr.linear_recurrence(x, a, b, p, p, None, cu, out, final)),
+                      median_ms(lambda: gdr.linear_recurrence_backward(x, a, b, p, p, out, go, None, None, cu))))
+    assert times[0][0] <= 4 * times[1][0] and times[0][1] <= 4 * times[1][1], times
+
+
+# long sequences among many short ones: none long, one, several, lengths around the limit that
+# parts them (some 80 tokens here), the first, the last and empty ones, all tokens in one
+def _mixed(long, n=300):
+    lens = [(7 * i) % 6 for i in range(n)]
+    for at, length in long.items():
+        lens[at] = length
+    return lens
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,C", [
+    (_mixed({}), 1024), (_mixed({0: 3000}), 1000), (_mixed({299: 901, 298: 0, 0: 333}), 1024),
+    (_mixed({i: 70 + i // 7 for i in range(3, 290, 14)}), 1096), ([0] * 299 + [2000], 1024),
+    ([2000] + [0] * 299, 520), (_mixed({40: 5000}, 900), 6144)])
+def test_packed_with_long_and_short_sequences(lens, C, dtype):
+    m = make(1, 0, C, dtype, seed=len(lens) + C, lens=lens)
+    got = on_gpu(m)[1]
+    again = on_gpu(m)[1]
+    for name, p, q in zip(NAMES, got, again):
+        assert torch.equal(p, q), name
+    m, got = some_channels(m, got, max(1, C // 64) | 1)
+    ref, mag = expected(m)
+    check(m, got, ref, mag, max(lens))
+
+
 def some_channels(m, got, every):
     """the case and its results at every `every`-th channel: channels do not mix"""
     cut = dict(m)
