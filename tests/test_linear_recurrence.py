@@ -237,6 +237,29 @@ def test_more_strips_than_sms(B, T, C, dtype):
     check(m, got, ref, mag, T)
 
 
+# packed documents of ragged lengths, empty ones among them, by units (strips x documents): more
+# than the SMs take at once, between one and two per SM, and so few that clusters take them
+WIDE = [([433, 64, 751, 0, 228, 16, 325, 129], 6144), ([900, 0, 411, 77], 4096),
+        ([1733, 256, 3001, 0, 911, 64, 1300, 517], 1024), ([2500, 0, 1999], 2056), ([0, 7001, 3], 520)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,C", WIDE)
+def test_wide_packed(lens, C, dtype):
+    m = make(1, 0, C, dtype, seed=C + len(lens), lens=lens)
+    got = on_gpu(m)[1]
+    again = on_gpu(m)[1]
+    for name, p, q in zip(NAMES, got, again):
+        assert torch.equal(p, q), name
+    for i, n in enumerate(lens):
+        if n == 0:
+            assert torch.equal(got[1][i], dev(m["init"])[i]) and torch.equal(got[7][i], dev(m["gf"])[i])
+    m, got = some_channels(m, got, max(1, sum(lens) * C // 2_000_000) | 1)
+    ref, mag = expected(m)
+    check(m, got, ref, mag, max(lens))
+
+
 @gpu
 def test_large_calls_on_two_streams_and_from_a_graph():
     """calls whose clusters hand states to one another, two at a time"""
