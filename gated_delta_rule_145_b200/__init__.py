@@ -133,7 +133,7 @@ def gdr_selftest_bounded_wait(stream=None) -> int:
 
 
 def gdr_release_workspace() -> None:
-    """Return the workspace memory cached by earlier chunked prefill calls."""
+    """Return the workspace memory cached by earlier calls."""
     library().gdr_release_workspace()
 
 
@@ -153,7 +153,7 @@ _INT_MAX = 0x7fffffff
 def _call(name, ptrs, ints, stream, check, longs=()):
     fn = getattr(_lib or library(), name)
     if (max(ints) > _INT_MAX or min(ints) < -_INT_MAX or  # ctypes would drop the upper bits
-            any(not -1 << 62 < n < 1 << 62 for n in longs)):
+            longs and max(map(abs, longs)) >= 1 << 62):
         status = GDR_ERR_SHAPE
     else:
         status = fn(*[p if p is None or isinstance(p, int) else p.data_ptr() for p in ptrs],

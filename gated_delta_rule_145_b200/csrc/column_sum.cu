@@ -7,8 +7,8 @@
 // atomic adds.  With P = 0 the sums are zero.  A thread takes four columns; few blocks of
 // many rows (a norm's 128 columns) need all their loads in flight at once, many blocks of few rows
 // (a convolution's taps) need small blocks: Y = 16 up to 128 rows, above 128, or 32 where 256
-// blocks and more share the SMs.  Of 1184 rows of 128 columns it takes 6 us, of 148 of 12288 7 us
-// (9 with Y = 128; one thread per column and 32 rows of threads: 10 and 11).
+// blocks and more share the SMs.  Of 1184 rows of 128 columns it takes 7.5 us, of 148 of 12288 7.7
+// (two more with Y = 128; one thread per column and 32 rows of threads: four more).
 #include "gdr_internal.h"
 #include "tcgen05.cuh"
 

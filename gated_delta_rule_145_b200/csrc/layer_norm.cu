@@ -405,7 +405,7 @@ layer_norm_block_kernel(const Tin* x, const float* __restrict__ weight,
 // rows from a ring in shared memory (bulk copies: rows are contiguous), so the bytes in flight
 // depend neither on registers nor on barriers; the values are expanded again after the
 // barrier behind the two sums of each row instead of being held.  [8192, 6144] bf16 takes
-// 66 us (0.70 of a copy's rate), [8192, 4096] fp32 80 us (0.77): the two barriers of a group
+// 67 us (0.69 of a copy's rate), [8192, 4096] fp32 80 us (0.77): the two barriers of a group
 // and the sums between them, which one block per SM cannot overlap.  (Both phases of two
 // groups per barrier: 98 us; one barrier per group, a slot refilled behind the next one: 74;
 // a column's sums over a warp's rows by shared-memory atomics would add in no fixed order.)

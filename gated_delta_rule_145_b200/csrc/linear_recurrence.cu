@@ -186,8 +186,8 @@ __device__ __forceinline__ void store_grads(float2 fx, float2 fb, float2 fa, flo
 // ------------------------------------------------------------- sequential form
 // Thread -> two channels of the sequences s = blockIdx.y, + gridDim.y, ...; one token after
 // the other, the state in registers.  For single tokens and short sequences, where there is
-// nothing to split.  One token of 64 sequences x 6144 channels takes 4 us, bound by the
-// latency of three dependent loads; 32 tokens 31 us (0.62 of a copy's rate).
+// nothing to split.  One token of 64 sequences x 6144 channels takes 4 us: a launch, one round of
+// loads and the stores; 32 tokens 31 us (0.62 of a copy's rate).
 constexpr int kSeqThreads = 128;
 
 template <typename Tin>
@@ -272,12 +272,12 @@ recurrence_seq_backward_kernel(RecurrenceParams p, RecurrenceGrads r, float* par
 // then runs its tokens once more from its true start state and stores them.  Nothing is
 // read twice.
 //
-// What bounds it (B200, bf16): with as many units as SMs the backward pass runs at a copy's rate
-// ([1, 8192, 9472] 236 us) and the forward pass at 0.86 of it (137 us), where the
+// What bounds it (B200, bf16): with as many units as SMs the backward pass runs at 0.97 of a
+// copy's rate ([1, 8192, 9472] 245 us) and the forward pass at 0.86 (137 us), where the
 // special-function unit does eight operations per token and channel pair; other calls lose to
-// their last wave, to CTA starts and to the exchanges.  Forward [8, 1024, 6144] 88 us (0.87 of a
-// copy's rate), [1, 8192, 6144] 110 us (0.70), [1, 65536, 1024] 155 us (0.66); backward 170 us
-// (0.90), 195 us (0.79), 270 us (0.76).
+// their last wave, to CTA starts and to the exchanges.  The kernels alone, forward: [8, 1024, 6144]
+// 87 us (0.88 of a copy's rate), [1, 8192, 6144] 108 us (0.71), [1, 65536, 1024] 157 us (0.65);
+// backward 167 us (0.92), 190 us (0.81), 273 us (0.75).
 //
 // Decays are composed as sums of log-decays.  From tile to tile a factor P near 1 acts
 // through W = P - 1, formed as expm1 of its tile's sum: a slow channel's state lasts over
@@ -1090,8 +1090,9 @@ bool make_maps(Maps& m, const RecurrenceParams& p, const float* dout, int box) {
 // hold, since a step's exchange costs the same 0.6 us for any.  Pair: clusters with two CTAs
 // per SM, for units in between (a cluster's CTAs share SMs, so it needs enough clusters).
 // Registers set the tokens of two CTAs per SM (two values per token and channel forward, three
-// backward, where a slot is held through its step, too).  Times in ns as measured: a step, and
-// a CTA's start.
+// backward, where a slot is held through its step, too).  Times in ns, a step and a CTA's start, are
+// fitted to calls that fill the slots in part: a plan's time ranks the forms and foretells no call
+// (where units fill every slot, steps of kCrowd and of fp32's kMany would move 7.3 to 8.3 TB/s).
 template <typename Tin> struct Forms;
 template <> struct Forms<__nv_bfloat16> {
     using T = __nv_bfloat16;

@@ -125,9 +125,10 @@ union ConvBackwardSmem {
 // `seg` tokens, lane -> four channels, one token after the other, its loads two batches
 // ahead (held in registers, one batch at a time, the loads' latency showed: 0.6 of HBM; by
 // asynchronous copies of eight bytes per lane they cost a tenth of the instructions).
-// [1, 8192, 18432] takes 178 us (0.78 of a copy's rate, 5.1 TB/s), [8, 2048, 4096] 89 us (0.69):
-// 89 instructions per token and four channels use 54 % of the issue slots, the paired fp32
-// pipe more, and the segments' ends and one wave's uneven SMs take the rest.  (Two channels per
+// [1, 8192, 18432] takes 177 us with a cold L2 and 184 among other passes (0.78 and 0.75 of a
+// copy's rate), [8, 2048, 4096] 89 us (0.69): 89 instructions per token and four channels use 53 %
+// of the issue slots and 53 % of the fp32 pipe ([1, 2048, 18432]).  With four warps per scheduler
+// the largest stall is the wait for a dependent result, and registers allow no more warps.  (Two channels per
 // lane and twice the warps: 228 us; one reciprocal for two channels, with the minima that keep
 // the product finite: 189.)
 // part [groups][5 C]: the taps' sums as [C][4], then the bias's.
@@ -328,8 +329,8 @@ __device__ __forceinline__ void store_z4(__nv_bfloat16* p, const float (&z)[4]) 
 }
 
 // L = d / 4 adjacent lanes share a row, four values each; a warp takes 32 / L rows at a
-// time, grid-stride.  part [gridDim.x][d].  [393216, 128] with a bf16 gate takes 140 us with its
-// column sums (0.88 of a copy's rate), the kernel alone 0.94: memory bounds it.
+// time, grid-stride.  part [gridDim.x][d].  [393216, 128] with a bf16 gate takes 142 us with its
+// column sums (0.86 of a copy's rate), the kernel alone 0.90: memory bounds it.
 template <typename Tz, int D>
 __global__ void __launch_bounds__(kNThreads)
 gated_rmsnorm_backward_kernel(NormGrads p, float* part) {

@@ -1,4 +1,5 @@
-// workspace.cu -- the tensor-core prefill's workspace and dispatch, and the device status.
+// workspace.cu -- the tensor-core prefill's workspace and dispatch, the pool that it shares with the
+// backward passes and with recurrences cut between clusters, and the device status.
 //
 // The chunked prefill on the tcgen05 tensor cores (prefill_tc64.cu) keeps one record per
 // (64-token block, value head) in a workspace: taken per call from a private

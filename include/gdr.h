@@ -48,9 +48,12 @@
  *     (cudaMallocFromPoolAsync on `stream`, returned with cudaFreeAsync on the same
  *     stream once the call's kernels are enqueued).  Freed memory stays cached in the pool
  *     for later calls until gdr_release_workspace().  Calls on different streams get
- *     different workspace memory.  No other call allocates device memory.
- *   - CUDA graphs: the device-buffer calls enqueue only kernels (and, for the prefill, the
- *     pool allocation and free) on `stream`, so they may be captured in a graph and
+ *     different workspace memory.  From the same pool come the backward calls' partial sums
+ *     of the parameter gradients (some MB; the recurrence's up to 4 C floats per sequence and
+ *     CTA of a cluster) and the states that a recurrence of few sequences hands between
+ *     clusters (below 1 MB).  No other call allocates device memory.
+ *   - CUDA graphs: the device-buffer calls enqueue only kernels (and, for calls with a workspace,
+ *     the pool allocation and free and a memset) on `stream`, so they may be captured in a graph and
  *     replayed; the replay gives the direct call's results bit for bit (tested for
  *     gdr_decode_step and gdr_prefill_chunked).  A decode loop replayed from a graph pays
  *     no host work per step.
@@ -508,7 +511,7 @@ GDR_API int gdr_device_status(gdr_stream_t stream);
 GDR_API int gdr_selftest_bounded_wait(gdr_stream_t stream);
 
 /*
- * Returns the workspace memory cached by earlier gdr_prefill_chunked calls to the system
+ * Returns the workspace memory cached by earlier calls to the system
  * (every device's pool is trimmed to zero).  Memory still in use by enqueued work is
  * released once that work completes.  No counterpart on the pages: it manages this
  * library's own cache.
