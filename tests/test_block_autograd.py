@@ -24,7 +24,9 @@ def _calls():
     }
 
 
-@pytest.mark.parametrize("name", sorted(_calls()) if torch.cuda.is_available() else ["layer_norm"])
+@pytest.mark.parametrize("name", ["linear_recurrence", "linear_recurrence_backward", "layer_norm",
+                                  "layer_norm_backward", "short_conv_silu_backward",
+                                  "gated_rmsnorm_backward"])
 def test_a_gradient_that_would_be_lost_is_refused(name):
     fn, args = _calls()[name]
     for i in range(len(args)):

@@ -190,6 +190,42 @@ def test_packed_with_long_and_short_sequences(lens, C, dtype):
     check(m, got, ref, mag, max(lens))
 
 
+@gpu
+def test_packed_with_long_sequences_in_place_and_replayed_on_other_lengths():
+    """the lengths are read on the device: a graph of one batch serves the next, whose long sequences
+    are others; states updated in place have the bits of those apart"""
+    C, n = 1024, 300
+    batches = [_mixed({5: 1500, 200: 700}), _mixed({0: 90, 299: 2000}), _mixed({7: 64, 8: 0})]
+    T = max(map(sum, batches)) + 50
+    g = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    x, a, b = (r(1, T, C).bfloat16() for _ in range(3))
+    A, d, init, gf, go = r(C), r(C), r(n, C), r(n, C), r(1, T, C)
+    cus = [dev(np.concatenate([[0], np.cumsum(v)]).astype(np.int32)) for v in batches]
+    cu, state = cus[0].clone(), init.clone()
+
+    def step(state):
+        out, final = gdr.linear_recurrence(x, a, b, A, d, state, cu, final_state=state)
+        return (out, final) + gdr.linear_recurrence_backward(x, a, b, A, d, out, go, gf, init, cu)
+
+    step(state)
+    graph, cap = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=cap):
+        got = step(state)
+    torch.cuda.current_stream().wait_stream(cap)
+    for other in cus:
+        out, final = gdr.linear_recurrence(x, a, b, A, d, init, other)
+        want = (out, final) + gdr.linear_recurrence_backward(x, a, b, A, d, out, go, gf, init, other)
+        cu.copy_(other)
+        state.copy_(init)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, p, q in zip(NAMES, want, got):
+            assert torch.equal(p, q), name
+    del graph
+
+
 def some_channels(m, got, every):
     """the case and its results at every `every`-th channel: channels do not mix"""
     cut = dict(m)
